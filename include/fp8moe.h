@@ -72,6 +72,7 @@ extern "C" {
 #define FP8MOE_ERR_LAUNCH 6        /* the HIP runtime rejected a launch */
 #define FP8MOE_ERR_DEVICE 7        /* a HIP device query failed */
 #define FP8MOE_ERR_SCRATCH 8       /* the allocation-free entry point's fixed scratch is too small */
+#define FP8MOE_ERR_VALUE 9         /* a numeric argument (an epsilon, a factor) is out of range */
 
 /* FP8 codecs.  e4m3fn: OCP, bias 7, max 448, NaN 0x7F/0xFF, signed zero.
  * e4m3fnuz: bias 8, max 240, no NaN/Inf among finite codes, unsigned zero.
@@ -664,6 +665,75 @@ int grouped_mm_scaled(int mode, const void *a, int a_fmt, const void *a_scale,
                       const void *b, int b_fmt, const void *b_scale, int scale_kind,
                       const int32_t *offs, int32_t n_groups, int64_t M, int64_t N, int64_t K,
                       void *out, int out_dtype, void *stream);
+
+/*
+ * rmsnorm_quantize_rowwise -- the norm in front of a linear or MoE layer: the
+ * residual's addition, the root-mean-square norm and the rowwise FP8
+ * quantization of its output in one pass over the rows.
+ *   [P1 Details and P4 "Три уровня оптимизации Triton-ядер": quantization
+ *   fused into the kernel that produces the operand; the norm itself is the
+ *   layer's public definition.]
+ *   x         bf16 [rows][ld_x]         (the first `cols` of each row are read)
+ *   residual  bf16 [rows][ld_residual]  or NULL
+ *   gamma     [cols] of gamma_dtype (FP8MOE_OUT_BF16 or FP8MOE_OUT_F32), or NULL: all 1
+ *   With s = bf16(x + residual) (one fp32 sum, round to nearest even; s = x without
+ *   a residual), rstd = 1 / sqrt(sum(s^2) / cols + eps) and f = (s * gamma) * rstd,
+ *   each an fp32 operation and the sum in fp32:
+ *   sum       bf16 [rows][cols]  s, the new residual stream (written with a
+ *             residual; ignored without one).  It may be x or the residual itself.
+ *   h         bf16 [rows][cols]  bf16(f) (written), or NULL
+ *   q, scale  u8 [rows][cols], f32 [rows]: the rowwise recipe over the fp32 values f
+ *             (not over their bf16 copy h), or NULL together: no codes (written)
+ *   rstd      f32 [rows] (written), or NULL
+ *   Requires: cols >= 1, cols % 8 == 0, cols <= 16384 (else
+ *   FP8MOE_ERR_UNSUPPORTED), ld_x and ld_residual >= cols and % 8 == 0, eps > 0 and
+ *   finite (else FP8MOE_ERR_VALUE); bf16, code and gamma pointers 16-byte aligned.
+ *   A row holding NaN or infinity, or whose mean square overflows fp32, is outside
+ *   the contract (other rows are not touched by it).  One kernel, no allocation.
+ */
+int rmsnorm_quantize_rowwise(const void *x_bf16, const void *residual_bf16, const void *gamma, int gamma_dtype,
+                             int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_residual, float eps, int codec,
+                             void *sum_bf16, void *h_bf16, void *q, float *scale, float *rstd, void *stream);
+
+/*
+ * rmsnorm_quantize_mx -- rmsnorm_quantize_rowwise with MXFP8 codes: 1x32 blocks
+ * along the row, the e8m0 exponent of a block from the maximum of |f| in it, codes
+ * enc(clamp(f * 2^-X)).
+ *   q, scale_e8m0  as quantize_mx with axis 1 lays them out (rows of cols / 32
+ *                  scales, or the K4 layout of R = rows) (both written, required)
+ *   Requires: as rmsnorm_quantize_rowwise, and cols % 32 == 0.
+ */
+int rmsnorm_quantize_mx(const void *x_bf16, const void *residual_bf16, const void *gamma, int gamma_dtype,
+                        int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_residual, float eps, int rule,
+                        int scale_layout, void *sum_bf16, void *h_bf16, void *q, void *scale_e8m0, float *rstd,
+                        void *stream);
+
+/*
+ * rmsnorm_backward -- the gradients through the norm and the residual's addition,
+ * for the gradient dh of its output (codes pass gradients straight through).
+ *   dh      bf16 [rows][cols]
+ *   s       bf16 [rows][cols], rstd f32 [rows]: as the forward wrote them (s = x
+ *           without a residual)
+ *   gamma   as in the forward
+ *   dsum    bf16 [rows][cols]  gradient that reaches s past the norm (the residual
+ *           stream's), or NULL
+ *   dx      bf16 [rows][cols]  gradient of s, which is that of x and of the residual:
+ *           with n = s * rstd and g = dh * gamma, rstd * (g - n * mean(g * n)) + dsum,
+ *           fp32, rounded once (written).  It may be dh, s or dsum itself.
+ *   dgamma  f32 [cols]  sum over rows of dh * n, fp32 sums in a fixed order (written;
+ *           zeros without rows), or NULL: not computed
+ *   workspace  device memory of rmsnorm_backward_workspace_bytes(rows, cols) bytes,
+ *           16-byte aligned, owned by the caller (not needed without dgamma);
+ *           contents on entry do not matter
+ *   Requires: cols as in the forward; bf16 and gamma pointers 16-byte aligned.  Two
+ *   kernels (one without dgamma), no allocation.
+ */
+int rmsnorm_backward(const void *dh_bf16, const void *s_bf16, const float *rstd, const void *gamma, int gamma_dtype,
+                     const void *dsum_bf16, int64_t rows, int64_t cols, void *dx_bf16, float *dgamma,
+                     void *workspace, void *stream);
+
+/* Workspace bytes rmsnorm_backward needs (-1: invalid sizes). */
+int64_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 
 /*
  * fp8moe_encode_f32 -- the device FP8 encoder alone: q[i] = enc(y[i]) for

@@ -8,6 +8,8 @@ no CPU or eager fallback: a missing library or a rejected argument raises.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib
@@ -26,7 +28,8 @@ __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "swiglu_backward_quantize_rowwise", "moe_route", "moe_route_noalloc", "moe_route_rows_bound", "moe_route_workspace_bytes", "moe_permute", "moe_combine",
            "moe_permute_rowwise", "moe_combine_backward",
            "quantize_tensorwise", "moe_permute_quantized", "quantize_blockwise", "grouped_mm_blockwise",
-           "quantize_blockwise_tokens", "grouped_mm_blockwise_k"]
+           "quantize_blockwise_tokens", "grouped_mm_blockwise_k",
+           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes"]
 
 
 def _ptr(t):
@@ -520,6 +523,149 @@ def moe_combine_backward(dy, yg, dest, src, weights, topk, codec=E4M3FN, codes=T
         _ptr(dy), _ptr(yg), R, _ptr(dest), _ptr(src), _ptr(weights), T, topk, C, codec, _ptr(dyg), _ptr(q),
         _ptr(scale), _ptr(dweights), _stream(stream)))
     return dyg, q, scale, dweights
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(fn, stream, first, *others):
+    """The context an operator allocates and launches in: the device of its tensors (all on one GPU) and the given
+    stream, so that temporary and output memory belongs to the stream that uses it."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: needs GPU tensors, got {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"{fn}: tensors on {dev}, stream on {stream.device}")
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _rows2d(fn, name, t, dtypes):
+    """(rows, cols, row stride) of a 2D tensor whose rows are contiguous; other strides are refused, not copied."""
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} must be a 2D tensor of {' or '.join(map(str, dtypes))}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    R, C = t.shape
+    if R == 0 or C == 0:
+        return R, C, C
+    if (t.stride(1) != 1 and C > 1) or (t.stride(0) < C and R > 1):
+        raise ValueError(f"{fn}: {name} needs contiguous rows that do not overlap, got strides {t.stride()}")
+    return R, C, t.stride(0) if R > 1 else max(C, t.stride(0))
+
+
+def _out(fn, name, t, shape, dtype, dev):
+    """A caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _vec(fn, name, t, n, dtypes):
+    if t is not None and (t.dtype not in dtypes or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of {n} elements, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+_BF16, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _norm_inputs(fn, x, gamma, residual):
+    R, C, ld = _rows2d(fn, "x", x, _BF16)
+    ld_r = C
+    if residual is not None:
+        Rr, Cr, ld_r = _rows2d(fn, "residual", residual, _BF16)
+        if (Rr, Cr) != (R, C):
+            raise ValueError(f"{fn}: residual must have x's shape {(R, C)}, got {(Rr, Cr)}")
+    _vec(fn, "gamma", gamma, C, _BF16_F32)
+    return R, C, ld, ld_r, OUT_BF16 if gamma is not None and gamma.dtype == torch.bfloat16 else OUT_F32
+
+
+def rmsnorm_quantize_rowwise(x, gamma=None, eps=1e-6, residual=None, codec=E4M3FN, keep_bf16=True, codes=True,
+                             sum_out=None, h=None, q=None, scale=None, rstd=None, stream=None):
+    """x bf16 [R, C] (row stride may exceed C), gamma bf16 or f32 [C] or None, residual bf16 [R, C] or None ->
+    (h bf16 [R, C] or None, q u8 [R, C] or None, scale f32 [R] or None, rstd f32 [R], sum bf16 [R, C]): the residual's
+    addition, the RMS norm and the rowwise FP8 quantization of the normed rows (from fp32) in one pass.  sum is
+    x + residual, the new residual stream (x itself without a residual); sum_out may be x or residual.
+    keep_bf16=False skips h, codes=False skips q and scale."""
+    fn = "rmsnorm_quantize_rowwise"
+    R, C, ld, ld_r, gt = _norm_inputs(fn, x, gamma, residual)
+    with _on(fn, stream, x, gamma, residual):
+        dev = x.device
+        s = _out(fn, "sum_out", sum_out, (R, C), torch.bfloat16, dev) if residual is not None else x
+        h = _out(fn, "h", h, (R, C), torch.bfloat16, dev) if keep_bf16 else None
+        q = _out(fn, "q", q, (R, C), torch.uint8, dev) if codes else None
+        scale = _out(fn, "scale", scale, (R,), torch.float32, dev) if codes else None
+        rstd = _out(fn, "rstd", rstd, (R,), torch.float32, dev)
+        _lib.check(fn, _lib.lib().rmsnorm_quantize_rowwise(
+            _ptr(x), _ptr(residual), _ptr(gamma), gt, R, C, ld, ld_r, eps, codec, _ptr(s), _ptr(h), _ptr(q),
+            _ptr(scale), _ptr(rstd), _stream(None)))
+    return h, q, scale, rstd, s
+
+
+def rmsnorm_quantize_mx(x, gamma=None, eps=1e-6, residual=None, rule=MX_FLOOR_OCP, layout=MX_LAYOUT_ROWS, keep_bf16=True,
+                        sum_out=None, h=None, q=None, scale=None, rstd=None, stream=None):
+    """As rmsnorm_quantize_rowwise with MXFP8 codes: scale is e8m0 u8 [R, C / 32], or of shape
+    mx_k4_shape(R, C // 32) with layout=MX_LAYOUT_K4."""
+    fn = "rmsnorm_quantize_mx"
+    R, C, ld, ld_r, gt = _norm_inputs(fn, x, gamma, residual)
+    with _on(fn, stream, x, gamma, residual):
+        dev = x.device
+        s = _out(fn, "sum_out", sum_out, (R, C), torch.bfloat16, dev) if residual is not None else x
+        h = _out(fn, "h", h, (R, C), torch.bfloat16, dev) if keep_bf16 else None
+        q = _out(fn, "q", q, (R, C), torch.uint8, dev)
+        scale = _out(fn, "scale", scale, mx_k4_shape(R, C // 32) if layout == MX_LAYOUT_K4 else (R, C // 32), torch.uint8,
+                     dev)
+        rstd = _out(fn, "rstd", rstd, (R,), torch.float32, dev)
+        _lib.check(fn, _lib.lib().rmsnorm_quantize_mx(
+            _ptr(x), _ptr(residual), _ptr(gamma), gt, R, C, ld, ld_r, eps, rule, layout, _ptr(s), _ptr(h), _ptr(q),
+            _ptr(scale), _ptr(rstd), _stream(None)))
+    return h, q, scale, rstd, s
+
+
+def rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(_lib.lib().rmsnorm_backward_workspace_bytes(rows, cols))
+
+
+def rmsnorm_backward(dh, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, want_dgamma=True, workspace=None,
+                     stream=None):
+    """dh bf16 [R, C] (the gradient of h), s bf16 [R, C] and rstd f32 [R] from the forward (s = x without a residual),
+    gamma as there, dsum bf16 [R, C] or None (the gradient that reaches the residual stream past the norm) ->
+    (dx bf16 [R, C], the gradient of x and of the residual, dgamma f32 [C] or None).  dx may be dh, s or dsum."""
+    fn = "rmsnorm_backward"
+    dims = []
+    for name, t in (("dh", dh), ("s", s), ("dsum", dsum)):
+        if t is not None:
+            R, C, ld = _rows2d(fn, name, t, _BF16)
+            if ld != C and R > 1:
+                raise ValueError(f"{fn}: {name} must be contiguous, got strides {t.stride()}")
+            dims.append((R, C))
+    if len(set(dims)) != 1:
+        raise ValueError(f"{fn}: dh, s and dsum must have one shape, got {dims}")
+    R, C = dims[0]
+    _vec(fn, "rstd", rstd, R, _F32)
+    _vec(fn, "gamma", gamma, C, _BF16_F32)
+    with _on(fn, stream, dh, s, rstd, gamma, dsum, workspace):
+        dev = dh.device
+        dx = _out(fn, "dx", dx, (R, C), torch.bfloat16, dev)
+        dgamma = _out(fn, "dgamma", dgamma, (C,), torch.float32, dev) if want_dgamma else None
+        need = max(rmsnorm_backward_workspace_bytes(R, C), 16) if want_dgamma else 0
+        if want_dgamma and workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif want_dgamma and workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"{fn}: workspace of {need} bytes needed")
+        _lib.check(fn, _lib.lib().rmsnorm_backward(
+            _ptr(dh), _ptr(s), _ptr(rstd), _ptr(gamma),
+            OUT_BF16 if gamma is not None and gamma.dtype == torch.bfloat16 else OUT_F32, _ptr(dsum), R, C, _ptr(dx),
+            _ptr(dgamma), _ptr(workspace) if want_dgamma else None, _stream(None)))
+    return dx, dgamma
 
 
 def encode_f32(y, codec=E4M3FN, q=None, stream=None):

@@ -11,7 +11,7 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8moe.so")
 
 # status codes and enums (mirror include/fp8moe.h)
-OK, ERR_NULL, ERR_SHAPE, ERR_ENUM, ERR_ALIGN, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_DEVICE, ERR_SCRATCH = range(9)
+OK, ERR_NULL, ERR_SHAPE, ERR_ENUM, ERR_ALIGN, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_DEVICE, ERR_SCRATCH, ERR_VALUE = range(10)
 E4M3FN, E4M3FNUZ = 0, 1
 MX_FLOOR_OCP, MX_CEIL = 0, 1
 MX_LAYOUT_ROWS, MX_LAYOUT_K4 = 0, 1
@@ -28,11 +28,12 @@ EXPORTS = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "blockwise_token_blocks_bound", "grouped_mm_blockwise_k",
            "quantize_tensorwise_workspace_bytes", "fp8moe_set_colwise_poll_budget", "fp8moe_set_colwise_chunk_rows", "moe_route_noalloc",
            "moe_permute_rowwise", "moe_combine_backward", "quantize_mx_dual", "swiglu_quantize_mx_dual",
-           "swiglu_backward_quantize_mx_dual", "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise"]
+           "swiglu_backward_quantize_mx_dual", "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise",
+           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes"]
 
 _lib = None
 
-_vp, _i64, _i32, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+_vp, _i64, _i32, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_float
 
 _SIGS = {
     "quantize_rowwise": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp]),
@@ -75,6 +76,12 @@ _SIGS = {
     "moe_permute_rowwise": (_int, [_vp, _i64, _i64, _i32, _vp, _i64, _int, _vp, _vp, _vp, _vp]),
     "moe_combine_backward": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i64, _int, _vp, _vp, _vp, _vp,
                                     _vp]),
+    "rmsnorm_quantize_rowwise": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _i64, _f32, _int, _vp, _vp, _vp, _vp,
+                                        _vp, _vp]),
+    "rmsnorm_quantize_mx": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _i64, _f32, _int, _int, _vp, _vp, _vp, _vp,
+                                   _vp, _vp]),
+    "rmsnorm_backward": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "rmsnorm_backward_workspace_bytes": (_i64, [_i64, _i64]),
 }
 
 

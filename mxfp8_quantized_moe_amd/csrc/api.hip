@@ -285,6 +285,49 @@ int swiglu_backward_quantize_mx_dual(const void* da2_bf16, const void* h1_bf16, 
       offs_pad_out, as_stream(stream)));
 }
 
+int rmsnorm_quantize_rowwise(const void* x_bf16, const void* residual_bf16, const void* gamma, int gamma_dtype,
+                             int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_residual, float eps, int codec,
+                             void* sum_bf16, void* h_bf16, void* q, float* scale, float* rstd, void* stream) {
+  int st = check_rmsnorm(x_bf16, residual_bf16, gamma, gamma_dtype, rows, cols, ld_x, ld_residual, eps, sum_bf16,
+                         h_bf16, q, scale, rstd);
+  if (!st) st = check_rmsnorm_rowwise(codec, q, scale);
+  if (st) return st;
+  const NormArgs a{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16), gamma,
+                   gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps, q ? codec : 4, 0,
+                   static_cast<uint16_t*>(sum_bf16), static_cast<uint16_t*>(h_bf16), static_cast<uint8_t*>(q), scale,
+                   nullptr, rstd};
+  return launch_status(launch_rmsnorm_quantize(a, as_stream(stream)));
+}
+
+int rmsnorm_quantize_mx(const void* x_bf16, const void* residual_bf16, const void* gamma, int gamma_dtype,
+                        int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_residual, float eps, int rule,
+                        int scale_layout, void* sum_bf16, void* h_bf16, void* q, void* scale_e8m0, float* rstd,
+                        void* stream) {
+  int st = check_rmsnorm(x_bf16, residual_bf16, gamma, gamma_dtype, rows, cols, ld_x, ld_residual, eps, sum_bf16,
+                         h_bf16, q, scale_e8m0, rstd);
+  if (!st) st = check_rmsnorm_mx(rule, scale_layout, rows, cols, q, scale_e8m0);
+  if (st) return st;
+  const NormArgs a{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16), gamma,
+                   gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps, 2 + rule, scale_layout,
+                   static_cast<uint16_t*>(sum_bf16), static_cast<uint16_t*>(h_bf16), static_cast<uint8_t*>(q),
+                   nullptr, static_cast<uint8_t*>(scale_e8m0), rstd};
+  return launch_status(launch_rmsnorm_quantize(a, as_stream(stream)));
+}
+
+int64_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) { return norm_bwd_workspace_bytes(rows, cols); }
+
+int rmsnorm_backward(const void* dh_bf16, const void* s_bf16, const float* rstd, const void* gamma, int gamma_dtype,
+                     const void* dsum_bf16, int64_t rows, int64_t cols, void* dx_bf16, float* dgamma, void* workspace,
+                     void* stream) {
+  const int st = check_rmsnorm_backward(dh_bf16, s_bf16, rstd, gamma, gamma_dtype, dsum_bf16, rows, cols, dx_bf16,
+                                        dgamma, workspace);
+  if (st) return st;
+  return launch_status(launch_rmsnorm_backward(
+      static_cast<const uint16_t*>(dh_bf16), static_cast<const uint16_t*>(s_bf16), rstd, gamma,
+      gamma_dtype == FP8MOE_OUT_BF16, static_cast<const uint16_t*>(dsum_bf16), rows, cols,
+      static_cast<uint16_t*>(dx_bf16), dgamma, static_cast<float*>(workspace), as_stream(stream)));
+}
+
 int64_t quantize_mx_rows_bound(int64_t rows, int32_t n_groups) { return mx_rows_bound(rows, n_groups); }
 
 int grouped_mm_scaled(int mode, const void* a, int a_fmt, const void* a_scale, const void* b, int b_fmt,
@@ -314,6 +357,7 @@ const char* fp8moe_status_string(int status) {
     case FP8MOE_ERR_LAUNCH: return "kernel launch failed";
     case FP8MOE_ERR_DEVICE: return "device query failed";
     case FP8MOE_ERR_SCRATCH: return "the call needs more scratch than the allocation-free entry point holds";
+    case FP8MOE_ERR_VALUE: return "a numeric argument is out of range";
     default: return "unknown status";
   }
 }

@@ -99,4 +99,27 @@ hipError_t launch_swiglu_backward_quantize_rowwise(const uint16_t* da2, const ui
                                                    int64_t ld_h1, int codec, uint16_t* dh1, uint8_t* q, float* scale,
                                                    hipStream_t st);
 
+
+// RMS norm with a quantized output.  fmt 0, 1: rowwise codes of that codec; 2, 3: MX under the floor, ceil
+// rule; 4: no codes.
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;
+  const void* gamma;
+  bool gamma_bf16;
+  int64_t rows, cols, ld_x, ld_r;
+  float eps;
+  int fmt, layout;
+  uint16_t* sum;
+  uint16_t* h;
+  uint8_t* q;
+  float* scale;
+  uint8_t* sc;
+  float* rstd;
+};
+hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st);
+hipError_t launch_rmsnorm_backward(const uint16_t* dh, const uint16_t* s, const float* rstd, const void* gamma,
+                                   bool gamma_bf16, const uint16_t* dsum, int64_t rows, int64_t cols, uint16_t* dx,
+                                   float* dgamma, float* workspace, hipStream_t st);
+
 }  // namespace fp8moe

@@ -1,0 +1,458 @@
+// Root-mean-square norm of token rows with the residual's addition, quantized in
+// the same pass (rowwise FP8 or MXFP8 1x32 blocks along the row), and its
+// backward.
+//
+//   s = bf16(x + residual)            (s = x without a residual)
+//   rstd = 1 / sqrt(sum(s^2) / C + eps)
+//   f = (s * gamma) * rstd            fp32, never rounded before the cast
+//   h = bf16(f);  codes of f under the rowwise or the MX recipe
+//
+// f is (s * gamma) * rstd in this order because rounding is monotonic: the
+// largest |f| of a set is then exactly (largest |s * gamma|) * rstd, so the sum
+// of squares and the maxima come out of one reduction, and no code depends on a
+// second one.  The codes are cast from f itself, not from the bf16 copy h: one
+// rounding instead of two.
+//
+// The row stays in registers from the load to the cast: TPR threads own one
+// row, each with ITEMS 16-byte chunks of s.  HBM sees x and the residual once,
+// and s, h and the codes once.
+#include "device_common.hpp"
+#include "kernels.hpp"
+#include "validate.hpp"
+
+namespace fp8moe {
+
+typedef float rn_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 rn_bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(rn_f32x2{a, b}, rn_bf16x2));
+}
+__device__ __forceinline__ void unpack8(const u32x4& v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x);
+  f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z);
+  f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+}
+
+// Eight gamma values from column chunk c (GT 0: none, 1: fp32, 2: bf16).
+template <int GT>
+__device__ __forceinline__ void load_gamma(const void* __restrict__ gamma, int c, float (&g)[8]) {
+  if constexpr (GT == 1) {
+    const float4 a = reinterpret_cast<const float4*>(gamma)[2 * c], b = reinterpret_cast<const float4*>(gamma)[2 * c + 1];
+    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
+    g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+  } else if constexpr (GT == 2) {
+    unpack8(reinterpret_cast<const u32x4*>(gamma)[c], g);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = 1.0f;
+  }
+}
+
+// Sum over the aligned group of N lanes (16 or 64), the same bits in every lane:
+// each step adds two values that both lanes hold, and addition commutes.
+template <int N>
+__device__ __forceinline__ float group_sum_f32(float v) {
+  auto dpp = [](float a, auto ctl) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(a), decltype(ctl)::value, 0xF, 0xF, false));
+  };
+  v += dpp(v, std::integral_constant<int, 0x128>{});   // row_ror:8
+  v += dpp(v, std::integral_constant<int, 0x124>{});
+  v += dpp(v, std::integral_constant<int, 0x122>{});
+  v += dpp(v, std::integral_constant<int, 0x121>{});
+  if constexpr (N == 64) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+struct NormFwd {
+  const uint16_t* x;
+  const uint16_t* res;    // or null
+  const void* gamma;      // or null
+  int64_t rows, ld_x, ld_r;
+  int nchunk;             // cols / 8
+  float inv_c, eps;
+  uint16_t* sum;          // [rows][cols], written with a residual
+  uint16_t* h;            // [rows][cols] or null
+  uint8_t* q;             // [rows][cols] or null
+  float* scale;           // rowwise scales [rows]
+  uint8_t* sc;            // MX scales
+  float* rstd;            // [rows] or null
+  int layout;             // MX scale layout
+};
+
+// FMT 0: rowwise e4m3fn, 1: rowwise e4m3fnuz, 2: MX floor rule, 3: MX ceil rule, 4: no codes.
+template <int TPR, int ITEMS, int FMT, int GT>
+__global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
+  constexpr int RPB = 256 / TPR;
+  constexpr bool MX = FMT == 2 || FMT == 3, ROWWISE = FMT < 2;
+  __shared__ float red_s[4];
+  __shared__ uint32_t red_m[4];
+  const int lt = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool valid = row < p.rows;
+  const int64_t r = valid ? row : 0;
+  const int64_t cols = (int64_t)p.nchunk * 8;
+  const u32x4* __restrict__ xr = reinterpret_cast<const u32x4*>(p.x + r * p.ld_x);
+  u32x4 v[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = i * TPR + lt;
+    v[i] = valid && c < p.nchunk ? xr[c] : u32x4{0, 0, 0, 0};
+  }
+  if (p.res != nullptr) {
+    const u32x4* __restrict__ rr = reinterpret_cast<const u32x4*>(p.res + r * p.ld_r);
+    u32x4* __restrict__ so = reinterpret_cast<u32x4*>(p.sum + r * cols);
+    u32x4 w[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      w[i] = valid && c < p.nchunk ? rr[c] : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      float a[8], b[8];
+      unpack8(v[i], a);
+      unpack8(w[i], b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a[k] += b[k];
+      v[i] = pack8(a);
+      if (valid && c < p.nchunk) so[c] = v[i];
+    }
+  }
+  float ss = 0.0f;
+  float am[ITEMS];   // largest |s * gamma| of each chunk
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = i * TPR + lt;
+    float a[8], g[8];
+    unpack8(v[i], a);
+    am[i] = 0.0f;
+    if (c < p.nchunk) {
+      load_gamma<GT>(p.gamma, c, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ss += a[k] * a[k];
+        am[i] = fmaxf(am[i], fabsf(a[k] * g[k]));
+      }
+    }
+  }
+  float rm = 0.0f;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) rm = fmaxf(rm, am[i]);
+  uint32_t mb = __float_as_uint(rm);   // non-negative: ordered like the values
+  if constexpr (TPR <= 64) {
+    ss = group_sum_f32<TPR>(ss);
+    if constexpr (ROWWISE) mb = group_max_u32<TPR>(mb);
+  } else {
+    ss = group_sum_f32<64>(ss);
+    if constexpr (ROWWISE) mb = group_max_u32<64>(mb);
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      red_s[w] = ss;
+      red_m[w] = mb;
+    }
+    __syncthreads();
+    ss = (red_s[0] + red_s[1]) + (red_s[2] + red_s[3]);
+    if constexpr (ROWWISE) mb = max(max(red_m[0], red_m[1]), max(red_m[2], red_m[3]));
+  }
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ss * p.inv_c + p.eps));
+  float scale = 0.0f;
+  if constexpr (ROWWISE) scale = scale_from_amax(__uint_as_float(mb) * rstd, FMT);
+  if (valid && lt == 0) {
+    if (p.rstd != nullptr) p.rstd[row] = rstd;
+    if constexpr (ROWWISE) p.scale[row] = scale;
+  }
+  const int nb = p.nchunk >> 2;   // 32-blocks per row (MX)
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = i * TPR + lt;
+    const bool in = valid && c < p.nchunk;
+    float a[8], g[8];
+    unpack8(v[i], a);
+    if (c < p.nchunk) load_gamma<GT>(p.gamma, c, g);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = c < p.nchunk ? a[k] * g[k] * rstd : 0.0f;
+    if (in && p.h != nullptr) reinterpret_cast<u32x4*>(p.h + r * cols)[c] = pack8(a);
+    if constexpr (ROWWISE) {
+      if (in)
+        reinterpret_cast<u32x2*>(p.q + r * cols)[c] =
+            u32x2{quant4<FMT>(a[0], a[1], a[2], a[3], scale), quant4<FMT>(a[4], a[5], a[6], a[7], scale)};
+    }
+    if constexpr (MX) {
+      // four lanes hold one block (chunks 4b .. 4b+3; TPR is a multiple of four)
+      const uint32_t bm = lane_max_xor<2, false>(lane_max_xor<1, false>(__float_as_uint(am[i] * rstd)));
+      const int X = mx_exponent(bm, FMT - 2);
+      const float inv = exp2_neg(X);
+      if (in)
+        reinterpret_cast<u32x2*>(p.q + r * cols)[c] =
+            u32x2{quant4<0>(a[0], a[1], a[2], a[3], inv), quant4<0>(a[4], a[5], a[6], a[7], inv)};
+      if (in && (lt & 3) == 0) {
+        const int b = c >> 2;
+        const uint8_t code = (uint8_t)(X + 127);
+        if (p.layout == 0) {
+          p.sc[r * nb + b] = code;
+        } else {
+          uint8_t* const word = p.sc + ((int64_t)(b >> 2) * p.rows + r) * 4;
+          word[b & 3] = code;
+          if (b == nb - 1)
+            for (int t = (b & 3) + 1; t < 4; ++t) word[t] = 0;
+        }
+      }
+    }
+  }
+}
+
+template <int TPR, int ITEMS, int FMT>
+static hipError_t launch_fwd_g(const NormFwd& p, int gt, hipStream_t st) {
+  constexpr int RPB = 256 / TPR;
+  const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(256);
+  if (gt == 0) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 0>), grid, block, 0, st, p);
+  else if (gt == 1) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 1>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 2>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+template <int FMT>
+static hipError_t launch_fwd(const NormFwd& p, int gt, hipStream_t st) {
+  auto pick = [&](auto tpr_tag) -> hipError_t {
+    constexpr int TPR = decltype(tpr_tag)::value;
+    const int items = (p.nchunk + TPR - 1) / TPR;
+    if (items <= 1) return launch_fwd_g<TPR, 1, FMT>(p, gt, st);
+    if (items <= 2) return launch_fwd_g<TPR, 2, FMT>(p, gt, st);
+    if constexpr (TPR == 256)
+      if (items > 4) return launch_fwd_g<TPR, 8, FMT>(p, gt, st);   // cols <= kNormMaxCols
+    return launch_fwd_g<TPR, 4, FMT>(p, gt, st);
+  };
+  if (p.nchunk <= 64) return pick(std::integral_constant<int, 16>{});
+  if (p.nchunk <= 256) return pick(std::integral_constant<int, 64>{});
+  return pick(std::integral_constant<int, 256>{});
+}
+
+static_assert(kNormMaxCols == 256 * 8 * 8, "256 threads hold eight chunks of eight columns each");
+
+hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  NormFwd p;
+  p.x = a.x;
+  p.res = a.res;
+  p.gamma = a.gamma;
+  p.rows = a.rows;
+  p.ld_x = a.ld_x;
+  p.ld_r = a.ld_r;
+  p.nchunk = (int)(a.cols >> 3);
+  p.inv_c = 1.0f / (float)a.cols;
+  p.eps = a.eps;
+  p.sum = a.sum;
+  p.h = a.h;
+  p.q = a.q;
+  p.scale = a.scale;
+  p.sc = a.sc;
+  p.rstd = a.rstd;
+  p.layout = a.layout;
+  const int gt = a.gamma == nullptr ? 0 : (a.gamma_bf16 ? 2 : 1);
+  switch (a.fmt) {
+    case 0: return launch_fwd<0>(p, gt, st);
+    case 1: return launch_fwd<1>(p, gt, st);
+    case 2: return launch_fwd<2>(p, gt, st);
+    case 3: return launch_fwd<3>(p, gt, st);
+    default: return launch_fwd<4>(p, gt, st);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// With n = s * rstd and g = dh * gamma:
+//   dx = rstd * (g - n * mean(g * n)) (+ dsum),   dgamma = sum over rows of dh * n.
+// A workgroup walks rows with a stride of the grid and keeps its columns' share of
+// dgamma in registers (fp32); the shares go to the workspace, one row per
+// workgroup, and a second kernel adds them in a fixed order.
+
+struct NormBwd {
+  const uint16_t* dh;
+  const uint16_t* s;
+  const float* rstd;
+  const void* gamma;
+  const uint16_t* dsum;   // or null
+  int64_t rows;
+  int nchunk;
+  float inv_c;
+  uint16_t* dx;
+  float* part;            // [grid][cols] or null (no dgamma wanted)
+};
+
+template <int TPR, int ITEMS, int GT>
+__global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwd p) {
+  constexpr int RPB = 256 / TPR;
+  __shared__ float red[2][4];
+  const int lt = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t cols = (int64_t)p.nchunk * 8;
+  float acc[ITEMS][8];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < p.rows; base += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t row = base + sub;
+    const bool valid = row < p.rows;
+    const int64_t r = valid ? row : 0;
+    const float rstd = valid ? p.rstd[r] : 0.0f;
+    u32x4 dv[ITEMS], sv[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      const bool in = valid && c < p.nchunk;
+      dv[i] = in ? reinterpret_cast<const u32x4*>(p.dh + r * cols)[c] : u32x4{0, 0, 0, 0};
+      sv[i] = in ? reinterpret_cast<const u32x4*>(p.s + r * cols)[c] : u32x4{0, 0, 0, 0};
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      float d[8], n[8], g[8];
+      unpack8(dv[i], d);
+      unpack8(sv[i], n);
+      if (c < p.nchunk) {
+        load_gamma<GT>(p.gamma, c, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float nk = n[k] * rstd;
+          acc[i][k] += d[k] * nk;
+          dot += d[k] * g[k] * nk;
+        }
+      }
+    }
+    if constexpr (TPR <= 64) {
+      dot = group_sum_f32<TPR>(dot);
+    } else {
+      dot = group_sum_f32<64>(dot);
+      // two sets of slots in turn: the next row's write cannot meet this row's reads
+      if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = dot;
+      __syncthreads();
+      dot = (red[turn][0] + red[turn][1]) + (red[turn][2] + red[turn][3]);
+    }
+    const float m = dot * p.inv_c;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      if (valid && c < p.nchunk) {
+        float d[8], n[8], g[8], e[8];
+        unpack8(dv[i], d);
+        unpack8(sv[i], n);
+        load_gamma<GT>(p.gamma, c, g);
+        if (p.dsum != nullptr) {
+          unpack8(reinterpret_cast<const u32x4*>(p.dsum + r * cols)[c], e);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] += rstd * (d[k] * g[k] - n[k] * rstd * m);
+        reinterpret_cast<u32x4*>(p.dx + r * cols)[c] = pack8(e);
+      }
+    }
+  }
+  if (p.part == nullptr) return;   // uniform
+  float* const out = p.part + (int64_t)blockIdx.x * cols;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = i * TPR + lt;
+      if (c < p.nchunk) {
+        reinterpret_cast<float4*>(out)[2 * c] = float4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+        reinterpret_cast<float4*>(out)[2 * c + 1] = float4{acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+      }
+    }
+  } else {
+    // the RPB row slots of a column add up through LDS, one chunk set at a time
+    __shared__ float sh[256 * 8];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sh[(sub * TPR + lt) * 8 + k] = acc[i][k];
+      __syncthreads();
+      for (int e = threadIdx.x; e < TPR * 8; e += 256) {
+        float t = 0.0f;
+#pragma unroll
+        for (int u = 0; u < RPB; ++u) t += sh[u * TPR * 8 + e];
+        const int64_t col = (int64_t)i * TPR * 8 + e;
+        if (col < cols) out[col] = t;
+      }
+    }
+  }
+}
+
+// dgamma[c] = the workgroups' shares added in order: 64 columns and 4 row ranges per workgroup.
+__global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* __restrict__ part, int n, int64_t cols,
+                                                             float* __restrict__ dgamma) {
+  __shared__ float sh[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float t = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = w; i < n; i += 4) t += part[(int64_t)i * cols + c];
+  }
+  sh[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < cols) dgamma[c] = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+}
+
+template <int TPR, int ITEMS>
+static hipError_t launch_bwd_g(const NormBwd& p, int gt, int grid, hipStream_t st) {
+  if (gt == 0) hipLaunchKernelGGL((rmsnorm_bwd_kernel<TPR, ITEMS, 0>), dim3(grid), dim3(256), 0, st, p);
+  else if (gt == 1) hipLaunchKernelGGL((rmsnorm_bwd_kernel<TPR, ITEMS, 1>), dim3(grid), dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((rmsnorm_bwd_kernel<TPR, ITEMS, 2>), dim3(grid), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_backward(const uint16_t* dh, const uint16_t* s, const float* rstd, const void* gamma,
+                                   bool gamma_bf16, const uint16_t* dsum, int64_t rows, int64_t cols, uint16_t* dx,
+                                   float* dgamma, float* workspace, hipStream_t st) {
+  if (rows == 0 && dgamma == nullptr) return hipSuccess;
+  NormBwd p;
+  p.dh = dh;
+  p.s = s;
+  p.rstd = rstd;
+  p.gamma = gamma;
+  p.dsum = dsum;
+  p.rows = rows;
+  p.nchunk = (int)(cols >> 3);
+  p.inv_c = 1.0f / (float)cols;
+  p.dx = dx;
+  p.part = dgamma != nullptr ? workspace : nullptr;
+  const int gt = gamma == nullptr ? 0 : (gamma_bf16 ? 2 : 1);
+  const int grid = norm_bwd_blocks(rows, cols);
+  auto pick = [&](auto tpr_tag) -> hipError_t {
+    constexpr int TPR = decltype(tpr_tag)::value;
+    const int items = (p.nchunk + TPR - 1) / TPR;
+    if (items <= 1) return launch_bwd_g<TPR, 1>(p, gt, grid, st);
+    if (items <= 2) return launch_bwd_g<TPR, 2>(p, gt, grid, st);
+    if constexpr (TPR == 256)
+      if (items > 4) return launch_bwd_g<TPR, 8>(p, gt, grid, st);
+    return launch_bwd_g<TPR, 4>(p, gt, grid, st);
+  };
+  hipError_t e = hipSuccess;
+  if (grid > 0) {
+    if (p.nchunk <= 64) e = pick(std::integral_constant<int, 16>{});
+    else if (p.nchunk <= 256) e = pick(std::integral_constant<int, 64>{});
+    else e = pick(std::integral_constant<int, 256>{});
+  }
+  if (e != hipSuccess || dgamma == nullptr) return e;
+  hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, st, workspace, grid,
+                     cols, dgamma);
+  return hipGetLastError();
+}
+
+}  // namespace fp8moe

@@ -417,6 +417,61 @@ int check_moe_combine_backward(const void* dy, const void* yg, int64_t rows, con
   return FP8MOE_OK;
 }
 
+int check_rmsnorm(const void* x, const void* res, const void* gamma, int gamma_dtype, int64_t rows, int64_t cols,
+                  int64_t ld_x, int64_t ld_r, float eps, const void* sum, const void* h, const void* q,
+                  const void* scale, const void* rstd) {
+  if (gamma_dtype != FP8MOE_OUT_BF16 && gamma_dtype != FP8MOE_OUT_F32) return FP8MOE_ERR_ENUM;
+  if (rows < 0 || cols < 1 || ld_x < cols || (res && ld_r < cols) || rows > kI32Max) return FP8MOE_ERR_SHAPE;
+  if (cols > kNormMaxCols) return FP8MOE_ERR_UNSUPPORTED;
+  if (!(eps > 0.0f) || eps > 3.402823466e38f) return FP8MOE_ERR_VALUE;   // also NaN
+  if (mul(rows, ld_x) < 0 || (res && mul(rows, ld_r) < 0)) return FP8MOE_ERR_SHAPE;
+  if (!need(x, rows) || (res && !need(sum, rows))) return FP8MOE_ERR_NULL;
+  if ((q == nullptr) != (scale == nullptr) && rows) return FP8MOE_ERR_NULL;   // codes and scales come together
+  if (cols % 8 || ld_x % 8 || (res && ld_r % 8) || !aligned(x, 16) || !aligned(res, 16) || !aligned(gamma, 16) ||
+      !aligned(sum, 16) || !aligned(h, 16) || !aligned(q, 16) || !aligned(rstd, 4))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+int check_rmsnorm_rowwise(int codec, const void* q, const void* scale) {
+  (void)q;
+  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  return aligned(scale, 4) ? FP8MOE_OK : FP8MOE_ERR_ALIGN;
+}
+
+int check_rmsnorm_mx(int rule, int layout, int64_t rows, int64_t cols, const void* q, const void* sc) {
+  if (rule != FP8MOE_MX_FLOOR_OCP && rule != FP8MOE_MX_CEIL) return FP8MOE_ERR_ENUM;
+  if (layout != FP8MOE_MX_LAYOUT_ROWS && layout != FP8MOE_MX_LAYOUT_K4) return FP8MOE_ERR_ENUM;
+  if (cols % 32) return FP8MOE_ERR_ALIGN;
+  if (!need(q, rows) || !need(sc, rows)) return FP8MOE_ERR_NULL;
+  return FP8MOE_OK;
+}
+
+int norm_bwd_blocks(int64_t rows, int64_t cols) {
+  const int64_t rpb = cols <= 512 ? 16 : cols <= 2048 ? 4 : 1;   // rows a workgroup takes at a time
+  const int64_t steps = (rows + rpb - 1) / rpb;
+  return (int)(steps < 1024 ? steps : 1024);
+}
+
+int64_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1 || cols > kNormMaxCols) return -1;
+  return 4 * cols * norm_bwd_blocks(rows, cols);
+}
+
+int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, const void* gamma, int gamma_dtype,
+                           const void* dsum, int64_t rows, int64_t cols, const void* dx, const void* dgamma,
+                           const void* workspace) {
+  if (gamma_dtype != FP8MOE_OUT_BF16 && gamma_dtype != FP8MOE_OUT_F32) return FP8MOE_ERR_ENUM;
+  if (rows < 0 || cols < 1 || rows > kI32Max) return FP8MOE_ERR_SHAPE;
+  if (cols > kNormMaxCols) return FP8MOE_ERR_UNSUPPORTED;
+  if (!need(dh, rows) || !need(s, rows) || !need(rstd, rows) || !need(dx, rows)) return FP8MOE_ERR_NULL;
+  if (dgamma && !need(workspace, rows)) return FP8MOE_ERR_NULL;
+  if (cols % 8 || !aligned(dh, 16) || !aligned(s, 16) || !aligned(rstd, 4) || !aligned(gamma, 16) ||
+      !aligned(dsum, 16) || !aligned(dx, 16) || !aligned(dgamma, 4) || !aligned(workspace, 16))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
 int check_encode_f32(const void* y, int64_t n, int codec, const void* q) {
   if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
   if (n < 0 || n > kI32Max * 64LL) return FP8MOE_ERR_SHAPE;

@@ -88,4 +88,19 @@ int check_moe_combine_backward(const void* dy, const void* yg, int64_t rows, con
                                const int32_t* src, const float* w, int64_t tokens, int32_t topk, int64_t cols,
                                int codec, const void* dyg, const void* q, const float* scale, const float* dw);
 
+
+// RMS norm: 256 threads hold a row in registers.
+constexpr int64_t kNormMaxCols = 16384;
+int check_rmsnorm(const void* x, const void* res, const void* gamma, int gamma_dtype, int64_t rows, int64_t cols,
+                  int64_t ld_x, int64_t ld_r, float eps, const void* sum, const void* h, const void* q,
+                  const void* scale, const void* rstd);
+int check_rmsnorm_rowwise(int codec, const void* q, const void* scale);
+int check_rmsnorm_mx(int rule, int layout, int64_t rows, int64_t cols, const void* q, const void* sc);
+// Workgroups of the backward, each with one row of dgamma shares in the workspace.
+int norm_bwd_blocks(int64_t rows, int64_t cols);
+int64_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, const void* gamma, int gamma_dtype,
+                           const void* dsum, int64_t rows, int64_t cols, const void* dx, const void* dgamma,
+                           const void* workspace);
+
 }  // namespace fp8moe
