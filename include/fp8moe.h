@@ -121,6 +121,10 @@ extern "C" {
 #define FP8MOE_OUT_BF16 0          /* round to nearest even */
 #define FP8MOE_OUT_F32 1
 
+/* router scores */
+#define FP8MOE_GATE_SOFTMAX 0
+#define FP8MOE_GATE_SIGMOID 1
+
 /*
  * quantize_rowwise -- one fp32 scale per row, over the last dimension.
  *   [P1 Details: rowwise FP8 recipe and fused quantization kernels; P4 "Скейлы:
@@ -734,6 +738,97 @@ int rmsnorm_backward(const void *dh_bf16, const void *s_bf16, const float *rstd,
 
 /* Workspace bytes rmsnorm_backward needs (-1: invalid sizes). */
 int64_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * moe_gate -- the router's choice in front of moe_route: scores of the logits, the
+ * topk experts of each token and their weights.
+ *   [P4 "MoE" (tokens routed to experts, the experts' outputs summed with the
+ *   router's weights); the gate itself is the public definition of such layers.]
+ *   logits   [tokens][ld_logits] of logit_dtype (FP8MOE_OUT_BF16 or FP8MOE_OUT_F32);
+ *            the first n_experts of each row are read.  A logit that is NaN or
+ *            -infinity makes its expert ineligible for the token (score 0); +infinity
+ *            counts as the largest finite value
+ *   score    FP8MOE_GATE_SOFTMAX (over the eligible experts) or FP8MOE_GATE_SIGMOID,
+ *            fp32 arithmetic
+ *   bias     f32 [n_experts] or NULL: added to the score for the choice only (in 64
+ *            bits); a NaN or -infinite entry makes the expert ineligible.  Without it
+ *            the logits decide
+ *   token_mask  u8 [tokens] or NULL: a token of value 0 chooses nothing
+ *   ids      int32 [tokens][topk]  the experts of largest key, in decreasing order, equal
+ *            keys to the lower index (with a bias, keys within 2^-42 of each other count
+ *            as equal); -1 where no eligible expert is left (written)
+ *   weights  f32 [tokens][topk]  route_scale * score, the scores divided by their sum over
+ *            the token's choices when renormalize is non-zero; 0 where ids is -1, and for
+ *            choices whose scores sum to 0 (written)
+ *   ids and weights are what moe_route and moe_combine take (moe_route drops id -1).
+ *   Requires: 1 <= topk <= n_experts, ld_logits >= n_experts, tokens*topk within int32;
+ *   route_scale finite (else FP8MOE_ERR_VALUE); n_experts <= 1024 and topk <= 64 (else
+ *   FP8MOE_ERR_UNSUPPORTED); logits aligned to their type, the other arrays 4-byte
+ *   aligned.  One kernel, no allocation.
+ */
+int moe_gate(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+             int32_t topk, int score, const float *bias, const uint8_t *token_mask, int renormalize,
+             float route_scale, int32_t *ids, float *weights, void *stream);
+
+/*
+ * moe_balance_loss -- the load-balance loss of a routing and its per-expert counts.
+ *   logits .. token_mask  as moe_gate
+ *   ids       int32 [tokens][topk]  the tokens' choices (an id outside [0, n_experts) is
+ *             not counted)
+ *   seq_offs  int32 [n_seqs]  inclusive ends of the sequences the loss is averaged over,
+ *             read by the rule of group offsets above (disjoint, malformed entries cannot
+ *             reach outside; tokens behind the last one do not count), or NULL with
+ *             n_seqs == 1: all tokens
+ *   counts    int32 [n_seqs][n_experts]  c[s][i]: slots of sequence s's unmasked tokens that
+ *             chose expert i (written)
+ *   loss      f32 [1]  coef / n_seqs * sum over s and i of f[s][i] * P[s][i], with n[s] the
+ *             unmasked tokens of s, f = c * n_experts / (topk * n[s]) and P the mean over
+ *             those tokens of the scores divided by their sum over the experts (softmax
+ *             scores as they are); a sequence without tokens adds 0 (written)
+ *   dprob     f32 [n_seqs][n_experts]  the loss's derivative by one token's normalised score
+ *             of expert i: coef / n_seqs * f / n[s], what moe_gate_backward takes (written)
+ *   workspace device memory of moe_balance_workspace_bytes(...) bytes, 16-byte aligned,
+ *             owned by the caller; contents on entry do not matter
+ *   Sums over tokens are fp32 over at most 32 tokens of a wave, then in 64 bits, all in a
+ *   fixed order.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), n_seqs >= 1.
+ *   Two kernels (three with several sequences), no allocation.
+ */
+int moe_balance_loss(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                     int32_t topk, int score, const uint8_t *token_mask, const int32_t *ids,
+                     const int32_t *seq_offs, int32_t n_seqs, float coef, float *loss, int32_t *counts,
+                     float *dprob, void *workspace, void *stream);
+
+/* Workspace bytes of moe_balance_loss and moe_gate_balance (-1: invalid sizes). */
+int64_t moe_balance_workspace_bytes(int64_t tokens, int32_t n_experts, int32_t n_seqs);
+
+/*
+ * moe_gate_balance -- moe_gate and moe_balance_loss of its own choices from one read of
+ * the logits (every argument and result as there).
+ */
+int moe_gate_balance(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                     int32_t topk, int score, const float *bias, const uint8_t *token_mask, int renormalize,
+                     float route_scale, int32_t *ids, float *weights, const int32_t *seq_offs, int32_t n_seqs,
+                     float coef, float *loss, int32_t *counts, float *dprob, void *workspace, void *stream);
+
+/*
+ * moe_gate_backward -- the gradient of the router's logits through the gate's weights,
+ * the balance loss, or both.
+ *   logits .. route_scale  as in the forward
+ *   ids       int32 [tokens][topk] from the forward (an id outside [0, n_experts) passes
+ *             nothing; equal ids of a token add up)
+ *   dweights  f32 [tokens][topk]  gradient of the gate's weights, what
+ *             moe_combine_backward writes, or NULL: the loss alone (ids is then not read)
+ *   dprob     f32 [n_seqs][n_experts] and seq_offs as in the forward, or NULL: the gate alone
+ *   dloss     f32 [1] on the device: gradient of the loss; NULL: 1
+ *   dlogits   [tokens][n_experts] of logit_dtype, rounded once (written; zeros for masked
+ *             tokens and ineligible experts)
+ *   The choice itself (and so the bias) passes no gradient, and counts are constants of the
+ *   loss.  Requires: as moe_gate; dweights or dprob.  One kernel, no allocation.
+ */
+int moe_gate_backward(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                      int32_t topk, int score, const uint8_t *token_mask, int renormalize, float route_scale,
+                      const int32_t *ids, const float *dweights, const int32_t *seq_offs, int32_t n_seqs,
+                      const float *dprob, const float *dloss, void *dlogits, void *stream);
 
 /*
  * fp8moe_encode_f32 -- the device FP8 encoder alone: q[i] = enc(y[i]) for

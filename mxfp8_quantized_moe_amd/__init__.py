@@ -15,7 +15,7 @@ import torch
 from . import _lib
 from ._lib import (E4M3FN, E4M3FNUZ, MX_FLOOR_OCP, MX_CEIL, MX_LAYOUT_ROWS, MX_LAYOUT_K4, GROUPED_M, GROUPED_K,
                    OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16, SCALE_F32, SCALE_E8M0, SCALE_NONE, SCALE_E8M0_K4,
-                   OUT_BF16, OUT_F32,
+                   OUT_BF16, OUT_F32, GATE_SOFTMAX, GATE_SIGMOID,
                    Fp8MoeError)
 
 __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_rows_bound",
@@ -29,7 +29,9 @@ __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "moe_permute_rowwise", "moe_combine_backward",
            "quantize_tensorwise", "moe_permute_quantized", "quantize_blockwise", "grouped_mm_blockwise",
            "quantize_blockwise_tokens", "grouped_mm_blockwise_k",
-           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes"]
+           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
+           "GATE_SOFTMAX", "GATE_SIGMOID", "moe_gate", "moe_gate_balance", "moe_gate_backward", "moe_balance_loss",
+           "moe_balance_loss_backward", "moe_balance_workspace_bytes"]
 
 
 def _ptr(t):
@@ -666,6 +668,154 @@ def rmsnorm_backward(dh, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, w
             OUT_BF16 if gamma is not None and gamma.dtype == torch.bfloat16 else OUT_F32, _ptr(dsum), R, C, _ptr(dx),
             _ptr(dgamma), _ptr(workspace) if want_dgamma else None, _stream(None)))
     return dx, dgamma
+
+
+def _gate_inputs(fn, logits, token_mask):
+    T, E, ld = _rows2d(fn, "logits", logits, _BF16_F32)
+    if E < 1:
+        raise ValueError(f"{fn}: logits need at least one expert")
+    _vec(fn, "token_mask", token_mask, T, (torch.uint8, torch.bool))
+    return T, E, ld, OUT_F32 if logits.dtype == torch.float32 else OUT_BF16
+
+
+def _gate_topk(fn, topk, E):
+    if not 1 <= topk <= E:
+        raise ValueError(f"{fn}: topk must be between 1 and the {E} experts, got {topk}")
+
+
+def _gate_slots(fn, name, t, T, dtypes):
+    """topk of a contiguous [T, topk] tensor of slots."""
+    if t.dim() != 2 or t.shape[0] != T or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtypes[0]} tensor of shape [{T}, topk], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.shape[1]
+
+
+def _gate_seqs(fn, seq_offs):
+    if seq_offs is None:
+        return 1
+    if seq_offs.numel() < 1:
+        raise ValueError(f"{fn}: seq_offs needs at least one sequence")
+    _vec(fn, "seq_offs", seq_offs, seq_offs.numel(), _I32)
+    return seq_offs.numel()
+
+
+def moe_gate(logits, topk, score=GATE_SOFTMAX, bias=None, token_mask=None, renormalize=False, route_scale=1.0, ids=None,
+             weights=None, stream=None):
+    """logits f32 or bf16 [T, E] (row stride may exceed E), bias f32 [E] or None (added for the choice only), token_mask
+    u8 or bool [T] or None -> (ids int32 [T, topk], weights f32 [T, topk]): each token's topk experts in decreasing
+    order (ties to the lower index; -1 with weight 0 where no eligible expert is left) and their weights, what
+    moe_route and moe_combine take."""
+    fn = "moe_gate"
+    T, E, ld, dt = _gate_inputs(fn, logits, token_mask)
+    _gate_topk(fn, topk, E)
+    _vec(fn, "bias", bias, E, _F32)
+    with _on(fn, stream, logits, bias, token_mask):
+        ids = _out(fn, "ids", ids, (T, topk), torch.int32, logits.device)
+        weights = _out(fn, "weights", weights, (T, topk), torch.float32, logits.device)
+        _lib.check(fn, _lib.lib().moe_gate(_ptr(logits), dt, T, E, ld, topk, score, _ptr(bias), _ptr(token_mask),
+                                           bool(renormalize), route_scale, _ptr(ids), _ptr(weights), _stream(None)))
+    return ids, weights
+
+
+def moe_balance_workspace_bytes(tokens: int, n_experts: int, n_seqs: int = 1) -> int:
+    return int(_lib.lib().moe_balance_workspace_bytes(tokens, n_experts, n_seqs))
+
+
+def _balance_outputs(fn, T, E, S, loss, counts, dprob, workspace, dev):
+    need = moe_balance_workspace_bytes(T, E, S)
+    if need < 0:
+        raise ValueError(f"{fn}: invalid sizes tokens={T} experts={E} sequences={S}")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev:
+        raise ValueError(f"{fn}: workspace of {need} bytes needed on {dev}")
+    return (_out(fn, "loss", loss, (1,), torch.float32, dev), _out(fn, "counts", counts, (S, E), torch.int32, dev),
+            _out(fn, "dprob", dprob, (S, E), torch.float32, dev), workspace)
+
+
+def moe_gate_balance(logits, topk, coef, seq_offs=None, score=GATE_SOFTMAX, bias=None, token_mask=None,
+                     renormalize=False, route_scale=1.0, ids=None, weights=None, loss=None, counts=None, dprob=None,
+                     workspace=None, stream=None):
+    """moe_gate and moe_balance_loss of its choices from one read of the logits -> (ids, weights, loss f32 [1], counts
+    int32 [S, E], dprob f32 [S, E]); seq_offs int32 [S] are the inclusive ends of the sequences (None: one of all tokens)."""
+    fn = "moe_gate_balance"
+    T, E, ld, dt = _gate_inputs(fn, logits, token_mask)
+    _gate_topk(fn, topk, E)
+    _vec(fn, "bias", bias, E, _F32)
+    S = _gate_seqs(fn, seq_offs)
+    with _on(fn, stream, logits, bias, token_mask, seq_offs):
+        dev = logits.device
+        ids = _out(fn, "ids", ids, (T, topk), torch.int32, dev)
+        weights = _out(fn, "weights", weights, (T, topk), torch.float32, dev)
+        loss, counts, dprob, workspace = _balance_outputs(fn, T, E, S, loss, counts, dprob, workspace, dev)
+        _lib.check(fn, _lib.lib().moe_gate_balance(
+            _ptr(logits), dt, T, E, ld, topk, score, _ptr(bias), _ptr(token_mask), bool(renormalize), route_scale,
+            _ptr(ids), _ptr(weights), _ptr(seq_offs), S, coef, _ptr(loss), _ptr(counts), _ptr(dprob), _ptr(workspace),
+            _stream(None)))
+    return ids, weights, loss, counts, dprob
+
+
+def moe_balance_loss(logits, ids, coef, seq_offs=None, score=GATE_SOFTMAX, token_mask=None, loss=None, counts=None,
+                     dprob=None, workspace=None, stream=None):
+    """logits f32 or bf16 [T, E], ids int32 [T, topk] -> (loss f32 [1], counts int32 [S, E], dprob f32 [S, E]): the
+    load-balance loss of the choices, how many slots of each sequence chose each expert, and what the backward takes."""
+    fn = "moe_balance_loss"
+    T, E, ld, dt = _gate_inputs(fn, logits, token_mask)
+    topk = _gate_slots(fn, "ids", ids, T, _I32)
+    _gate_topk(fn, topk, E)
+    S = _gate_seqs(fn, seq_offs)
+    with _on(fn, stream, logits, ids, token_mask, seq_offs):
+        loss, counts, dprob, workspace = _balance_outputs(fn, T, E, S, loss, counts, dprob, workspace, logits.device)
+        _lib.check(fn, _lib.lib().moe_balance_loss(
+            _ptr(logits), dt, T, E, ld, topk, score, _ptr(token_mask), _ptr(ids), _ptr(seq_offs), S, coef, _ptr(loss),
+            _ptr(counts), _ptr(dprob), _ptr(workspace), _stream(None)))
+    return loss, counts, dprob
+
+
+def moe_gate_backward(logits, ids, dweights, score=GATE_SOFTMAX, token_mask=None, renormalize=False, route_scale=1.0,
+                      dprob=None, dloss=None, seq_offs=None, dlogits=None, stream=None):
+    """The gradient [T, E] of the logits (in their type) for dweights f32 [T, topk] (or flat, as moe_combine_backward
+    gives it) and, with dprob f32 [S, E] from the forward, for the balance loss (dloss f32 [1] on the device, None: 1)."""
+    fn = "moe_gate_backward"
+    T, E, ld, dt = _gate_inputs(fn, logits, token_mask)
+    topk = _gate_slots(fn, "ids", ids, T, _I32)
+    _gate_topk(fn, topk, E)
+    if dweights.dim() == 1 and dweights.numel() == T * topk:
+        dweights = dweights.view(T, topk)
+    if _gate_slots(fn, "dweights", dweights, T, _F32) != topk:
+        raise ValueError(f"{fn}: dweights must have ids' shape {(T, topk)}, got {tuple(dweights.shape)}")
+    return _gate_backward(fn, logits, T, E, ld, dt, topk, ids, dweights, score, token_mask, renormalize, route_scale, dprob,
+                          dloss, seq_offs, dlogits, stream)
+
+
+def moe_balance_loss_backward(logits, dprob, dloss=None, seq_offs=None, score=GATE_SOFTMAX, token_mask=None,
+                              dlogits=None, stream=None):
+    """The gradient [T, E] of the logits (in their type) through the balance loss alone."""
+    fn = "moe_balance_loss_backward"
+    T, E, ld, dt = _gate_inputs(fn, logits, token_mask)
+    if dprob is None:
+        raise ValueError(f"{fn}: needs dprob")
+    return _gate_backward(fn, logits, T, E, ld, dt, 1, None, None, score, token_mask, False, 1.0, dprob, dloss, seq_offs,
+                          dlogits, stream)
+
+
+def _gate_backward(fn, logits, T, E, ld, dt, topk, ids, dweights, score, token_mask, renormalize, route_scale, dprob,
+                   dloss, seq_offs, dlogits, stream):
+    S = _gate_seqs(fn, seq_offs)
+    if dprob is None and (dloss is not None or seq_offs is not None):
+        raise ValueError(f"{fn}: dloss and seq_offs go with dprob")
+    if dprob is not None and (dprob.dtype != torch.float32 or tuple(dprob.shape) != (S, E) or not dprob.is_contiguous()):
+        raise ValueError(f"{fn}: dprob must be a contiguous torch.float32 tensor of shape {(S, E)}, got {dprob.dtype} "
+                         f"{tuple(dprob.shape)}")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        raise ValueError(f"{fn}: dloss must be one torch.float32 value on the device")
+    with _on(fn, stream, logits, ids, dweights, token_mask, dprob, dloss, seq_offs):
+        dlogits = _out(fn, "dlogits", dlogits, (T, E), logits.dtype, logits.device)
+        _lib.check(fn, _lib.lib().moe_gate_backward(
+            _ptr(logits), dt, T, E, ld, topk, score, _ptr(token_mask), bool(renormalize), route_scale, _ptr(ids),
+            _ptr(dweights), _ptr(seq_offs), S, _ptr(dprob), _ptr(dloss), _ptr(dlogits), _stream(None)))
+    return dlogits
 
 
 def encode_f32(y, codec=E4M3FN, q=None, stream=None):

@@ -19,6 +19,7 @@ GROUPED_M, GROUPED_K = 0, 1
 OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16 = 0, 1, 2
 SCALE_F32, SCALE_E8M0, SCALE_NONE, SCALE_E8M0_K4 = 0, 1, 2, 3
 OUT_BF16, OUT_F32 = 0, 1
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 
 EXPORTS = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_rows_bound",
            "grouped_mm_scaled", "fp8moe_encode_f32", "fp8moe_status_string", "fp8moe_default_codec",
@@ -29,7 +30,8 @@ EXPORTS = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "quantize_tensorwise_workspace_bytes", "fp8moe_set_colwise_poll_budget", "fp8moe_set_colwise_chunk_rows", "moe_route_noalloc",
            "moe_permute_rowwise", "moe_combine_backward", "quantize_mx_dual", "swiglu_quantize_mx_dual",
            "swiglu_backward_quantize_mx_dual", "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise",
-           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes"]
+           "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
+           "moe_gate", "moe_balance_loss", "moe_balance_workspace_bytes", "moe_gate_balance", "moe_gate_backward"]
 
 _lib = None
 
@@ -82,6 +84,14 @@ _SIGS = {
                                    _vp, _vp]),
     "rmsnorm_backward": (_int, [_vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "rmsnorm_backward_workspace_bytes": (_i64, [_i64, _i64]),
+    "moe_gate": (_int, [_vp, _int, _i64, _i32, _i64, _i32, _int, _vp, _vp, _int, _f32, _vp, _vp, _vp]),
+    "moe_balance_loss": (_int, [_vp, _int, _i64, _i32, _i64, _i32, _int, _vp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _vp,
+                                _vp]),
+    "moe_balance_workspace_bytes": (_i64, [_i64, _i32, _i32]),
+    "moe_gate_balance": (_int, [_vp, _int, _i64, _i32, _i64, _i32, _int, _vp, _vp, _int, _f32, _vp, _vp, _vp, _i32,
+                                _f32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_gate_backward": (_int, [_vp, _int, _i64, _i32, _i64, _i32, _int, _vp, _int, _f32, _vp, _vp, _vp, _i32, _vp,
+                                 _vp, _vp, _vp]),
 }
 
 

@@ -328,6 +328,77 @@ int rmsnorm_backward(const void* dh_bf16, const void* s_bf16, const float* rstd,
       static_cast<uint16_t*>(dx_bf16), dgamma, static_cast<float*>(workspace), as_stream(stream)));
 }
 
+int moe_gate(const void* logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits, int32_t topk,
+             int score, const float* bias, const uint8_t* token_mask, int renormalize, float route_scale, int32_t* ids,
+             float* weights, void* stream) {
+  int st = check_moe_gate_logits(logits, logit_dtype, tokens, n_experts, ld_logits, topk, score, token_mask);
+  if (!st) st = check_moe_gate(tokens, topk, bias, route_scale, ids, weights);
+  if (st) return st;
+  GateArgs a{};
+  a.logits = logits;
+  a.bf16 = logit_dtype == FP8MOE_OUT_BF16;
+  a.sigmoid = score == FP8MOE_GATE_SIGMOID;
+  a.gate = true;
+  a.tokens = tokens;
+  a.ld = ld_logits;
+  a.E = n_experts;
+  a.topk = topk;
+  a.bias = bias;
+  a.mask = token_mask;
+  a.renorm = renormalize != 0;
+  a.route_scale = route_scale;
+  a.ids = ids;
+  a.weights = weights;
+  a.S = 1;
+  return launch_status(launch_moe_gate(a, as_stream(stream)));
+}
+
+int moe_gate_balance(const void* logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                     int32_t topk, int score, const float* bias, const uint8_t* token_mask, int renormalize,
+                     float route_scale, int32_t* ids, float* weights, const int32_t* seq_offs, int32_t n_seqs,
+                     float coef, float* loss, int32_t* counts, float* dprob, void* workspace, void* stream) {
+  int st = check_moe_gate_logits(logits, logit_dtype, tokens, n_experts, ld_logits, topk, score, token_mask);
+  if (!st) st = check_moe_gate(tokens, topk, bias, route_scale, ids, weights);
+  if (!st) st = check_moe_balance(tokens, n_experts, topk, ids, seq_offs, n_seqs, coef, loss, counts, dprob, workspace);
+  if (st) return st;
+  const GateArgs a{logits, logit_dtype == FP8MOE_OUT_BF16, score == FP8MOE_GATE_SIGMOID, true, tokens, ld_logits,
+                   n_experts, topk, bias, token_mask, renormalize != 0, route_scale, ids, weights, seq_offs, n_seqs,
+                   coef, loss, counts, dprob, workspace};
+  return launch_status(launch_moe_gate(a, as_stream(stream)));
+}
+
+int moe_balance_loss(const void* logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                     int32_t topk, int score, const uint8_t* token_mask, const int32_t* ids, const int32_t* seq_offs,
+                     int32_t n_seqs, float coef, float* loss, int32_t* counts, float* dprob, void* workspace,
+                     void* stream) {
+  int st = check_moe_gate_logits(logits, logit_dtype, tokens, n_experts, ld_logits, topk, score, token_mask);
+  if (!st) st = check_moe_balance(tokens, n_experts, topk, ids, seq_offs, n_seqs, coef, loss, counts, dprob, workspace);
+  if (st) return st;
+  const GateArgs a{logits, logit_dtype == FP8MOE_OUT_BF16, score == FP8MOE_GATE_SIGMOID, false, tokens, ld_logits,
+                   n_experts, topk, nullptr, token_mask, 0, 1.0f, const_cast<int32_t*>(ids), nullptr, seq_offs, n_seqs,
+                   coef, loss, counts, dprob, workspace};
+  return launch_status(launch_moe_gate(a, as_stream(stream)));
+}
+
+int64_t moe_balance_workspace_bytes(int64_t tokens, int32_t n_experts, int32_t n_seqs) {
+  return gate_workspace_bytes(tokens, n_experts, n_seqs);
+}
+
+int moe_gate_backward(const void* logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
+                      int32_t topk, int score, const uint8_t* token_mask, int renormalize, float route_scale,
+                      const int32_t* ids, const float* dweights, const int32_t* seq_offs, int32_t n_seqs,
+                      const float* dprob, const float* dloss, void* dlogits, void* stream) {
+  int st = check_moe_gate_logits(logits, logit_dtype, tokens, n_experts, ld_logits, topk, score, token_mask);
+  if (!st)
+    st = check_moe_gate_backward(tokens, topk, route_scale, ids, dweights, seq_offs, n_seqs, dprob, dloss, dlogits,
+                                 logit_dtype);
+  if (st) return st;
+  const GateBwdArgs a{logits, logit_dtype == FP8MOE_OUT_BF16, score == FP8MOE_GATE_SIGMOID, tokens, ld_logits,
+                      n_experts, topk, token_mask, renormalize != 0, route_scale, ids, dweights, seq_offs, n_seqs,
+                      dprob, dloss, dlogits};
+  return launch_status(launch_moe_gate_backward(a, as_stream(stream)));
+}
+
 int64_t quantize_mx_rows_bound(int64_t rows, int32_t n_groups) { return mx_rows_bound(rows, n_groups); }
 
 int grouped_mm_scaled(int mode, const void* a, int a_fmt, const void* a_scale, const void* b, int b_fmt,

@@ -122,4 +122,43 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dh, const uint16_t* s, const 
                                    bool gamma_bf16, const uint16_t* dsum, int64_t rows, int64_t cols, uint16_t* dx,
                                    float* dgamma, float* workspace, hipStream_t st);
 
+// Router gate and balance loss (either or both): gate writes ids and weights, loss non-null asks for the loss.
+struct GateArgs {
+  const void* logits;
+  bool bf16, sigmoid, gate;
+  int64_t tokens, ld;
+  int E, topk;
+  const float* bias;
+  const uint8_t* mask;
+  int renorm;
+  float route_scale;
+  int32_t* ids;
+  float* weights;
+  const int32_t* seq_offs;
+  int S;
+  float coef;
+  float* loss;
+  int32_t* counts;
+  float* dprob;
+  void* workspace;
+};
+hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st);
+struct GateBwdArgs {
+  const void* logits;
+  bool bf16, sigmoid;
+  int64_t tokens, ld;
+  int E, topk;
+  const uint8_t* mask;
+  int renorm;
+  float route_scale;
+  const int32_t* ids;
+  const float* dweights;
+  const int32_t* seq_offs;
+  int S;
+  const float* dprob;
+  const float* dloss;
+  void* dlogits;
+};
+hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st);
+
 }  // namespace fp8moe

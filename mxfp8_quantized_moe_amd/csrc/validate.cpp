@@ -472,6 +472,71 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
   return FP8MOE_OK;
 }
 
+int gate_chunk(int64_t tokens) {
+  int c = 16;
+  while (c < 128 && tokens / c > 1024) c *= 2;
+  return c;
+}
+
+int64_t gate_units(int64_t tokens, int32_t n_seqs) { return tokens / gate_chunk(tokens) + n_seqs + 1; }
+
+int64_t gate_workspace_bytes(int64_t tokens, int32_t E, int32_t n_seqs) {
+  if (tokens < 0 || tokens > kI32Max || E < 1 || E > kGateMaxExperts || n_seqs < 1 || n_seqs > (1 << 20)) return -1;
+  const int64_t units = gate_units(tokens, n_seqs);
+  return 8LL * n_seqs + units * (8LL * E + 4);
+}
+
+int check_moe_gate_logits(const void* logits, int dtype, int64_t tokens, int32_t E, int64_t ld, int32_t topk, int score,
+                          const void* mask) {
+  if (dtype != FP8MOE_OUT_BF16 && dtype != FP8MOE_OUT_F32) return FP8MOE_ERR_ENUM;
+  if (score != FP8MOE_GATE_SOFTMAX && score != FP8MOE_GATE_SIGMOID) return FP8MOE_ERR_ENUM;
+  if (tokens < 0 || E < 1 || ld < E || topk < 1 || topk > E) return FP8MOE_ERR_SHAPE;
+  if (E > kGateMaxExperts || topk > kGateMaxTopk) return FP8MOE_ERR_UNSUPPORTED;
+  if (tokens > kI32Max - 1024 || mul(tokens, topk) > kI32Max || mul(tokens, ld) < 0) return FP8MOE_ERR_SHAPE;
+  if (!need(logits, tokens)) return FP8MOE_ERR_NULL;
+  if (!aligned(logits, dtype == FP8MOE_OUT_F32 ? 4 : 2)) return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+static bool finite_f32(float v) { return v >= -3.402823466e38f && v <= 3.402823466e38f; }   // false for NaN
+
+int check_moe_gate(int64_t tokens, int32_t topk, const void* bias, float route_scale, const void* ids,
+                   const void* weights) {
+  (void)topk;
+  if (!finite_f32(route_scale)) return FP8MOE_ERR_VALUE;
+  if (!need(ids, tokens) || !need(weights, tokens)) return FP8MOE_ERR_NULL;
+  if (!aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+int check_moe_balance(int64_t tokens, int32_t E, int32_t topk, const void* ids, const void* seq_offs, int32_t n_seqs,
+                      float coef, const void* loss, const void* counts, const void* dprob, const void* workspace) {
+  (void)topk;
+  if (n_seqs < 1 || n_seqs > (1 << 20) || gate_workspace_bytes(tokens, E, n_seqs) < 0) return FP8MOE_ERR_SHAPE;
+  if (gate_units(tokens, n_seqs) > kI32Max) return FP8MOE_ERR_SHAPE;
+  if (!finite_f32(coef)) return FP8MOE_ERR_VALUE;
+  if (n_seqs > 1 && seq_offs == nullptr) return FP8MOE_ERR_NULL;
+  if (!need(ids, tokens) || !loss || !counts || !dprob || !workspace) return FP8MOE_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(seq_offs, 4) || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(dprob, 4) ||
+      !aligned(workspace, 16))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+int check_moe_gate_backward(int64_t tokens, int32_t topk, float route_scale, const void* ids, const void* dweights,
+                            const void* seq_offs, int32_t n_seqs, const void* dprob, const void* dloss,
+                            const void* dlogits, int dtype) {
+  (void)topk;
+  if (dweights && !finite_f32(route_scale)) return FP8MOE_ERR_VALUE;
+  if (dprob && (n_seqs < 1 || n_seqs > (1 << 20))) return FP8MOE_ERR_SHAPE;
+  if (dprob && n_seqs > 1 && seq_offs == nullptr) return FP8MOE_ERR_NULL;
+  if (tokens && ((!dweights && !dprob) || (dweights && !ids) || !dlogits)) return FP8MOE_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(dweights, 4) || !aligned(seq_offs, 4) || !aligned(dprob, 4) || !aligned(dloss, 4) ||
+      !aligned(dlogits, dtype == FP8MOE_OUT_F32 ? 4 : 2))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
 int check_encode_f32(const void* y, int64_t n, int codec, const void* q) {
   if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
   if (n < 0 || n > kI32Max * 64LL) return FP8MOE_ERR_SHAPE;
