@@ -789,9 +789,9 @@ int moe_gate(const void *logits, int logit_dtype, int64_t tokens, int32_t n_expe
  *             of expert i: coef / n_seqs * f / n[s], what moe_gate_backward takes (written)
  *   workspace device memory of moe_balance_workspace_bytes(...) bytes, 16-byte aligned,
  *             owned by the caller; contents on entry do not matter
- *   Sums over tokens are fp32 over at most 32 tokens of a wave, then in 64 bits, all in a
- *   fixed order.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), n_seqs >= 1.
- *   Two kernels (three with several sequences), no allocation.
+ *   Sums over tokens are fp32 over at most 128 tokens, then in 64 bits, all in a fixed
+ *   order.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), 1 <= n_seqs <= 65535.
+ *   Two kernels, no allocation.
  */
 int moe_balance_loss(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,
                      int32_t topk, int score, const uint8_t *token_mask, const int32_t *ids,

@@ -11,72 +11,157 @@
 // A logit that is NaN or -inf makes its expert ineligible for the token; +inf
 // counts as the largest finite value.
 //
-// Selection works on 64-bit keys: a double holds an fp32 logit exactly, and its low
-// ten bits, which the key does not need, hold the expert's index (complemented for
-// positive keys), so one maximum finds the winner and breaks ties to the lower
-// index.  With a bias the key is the score plus the bias in 64 bits: scores next to
-// each other would otherwise be ordered by fp32 rounding.
+// Layout: LPT lanes (4, 16 or 64) share a token, so a wave takes up to 16 tokens;
+// lane l of the group holds VPL logits in chunks of four, experts
+// 4 (l + LPT c) + 0..3, which are 16-byte loads and stores.  Sums and maxima over a
+// token then take 2, 4 or 6 VALU lane steps, shared by the wave's tokens.
 //
-// One wave takes one token; lane l holds experts l, l + 64, ...
+// Selection: a key is an fp32 value made sortable as an unsigned integer, with the
+// complemented expert index below it, all in the 63 low bits of a positive double,
+// so that one v_max_f64 compares values and breaks ties to the lower index.  Each
+// lane sorts its VPL keys once (a network of max/min pairs); a choice is then the
+// group's maximum of the list heads, and the lane that owned it moves its list up.
+// With a bias the fp32 keys carry rounding errors: where two consecutive choices
+// (or the last choice and the first key left out) are closer than those errors
+// allow, the wave forms its keys again in 64 bits and selects once more.
 #include "device_common.hpp"
 #include "kernels.hpp"
+#include "lane_groups.hpp"
 #include "validate.hpp"
 
 namespace fp8moe {
 
-static_assert(kGateMaxExperts == 1024, "ten bits of a key hold the index, a wave holds 16 logits a lane");
+static_assert(kGateMaxExperts == 1024, "a key's index has ten bits; 64 lanes hold 16 logits each");
 
 constexpr float kFltMax = 3.402823466e38f;
+typedef float gt_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 gt_bf16x2 __attribute__((ext_vector_type(2)));
 
-// ---------------------------------------------------------------- wave helpers
+// ---------------------------------------------------------------- logits
 
-__device__ __forceinline__ float gate_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
-__device__ __forceinline__ float gate_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ double gate_sum(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ double gate_max(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
-}
+// NaN as -inf, at most the largest finite value.
+__device__ __forceinline__ float gate_clean(float v) { return v > -INFINITY ? fminf(v, kFltMax) : -INFINITY; }
 
-// The logit as the gate reads it: NaN as -inf, at most the largest finite value.
 template <bool BF16>
 __device__ __forceinline__ float gate_logit(const void* __restrict__ logits, int64_t at) {
-  float v;
-  if constexpr (BF16) v = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
-  else v = static_cast<const float*>(logits)[at];
-  return v != v ? -INFINITY : fminf(v, kFltMax);
+  if constexpr (BF16) return gate_clean(__uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16));
+  else return gate_clean(static_cast<const float*>(logits)[at]);
 }
 
-// key with the index in its low ten bits; -inf stays as it is (no expert to name).
-__device__ __forceinline__ double gate_pack(double key, int idx) {
-  if (!(key > -INFINITY)) return -INFINITY;
-  const int64_t b = __double_as_longlong(fmin(fmax(key, -1.7e308), 1.7e308) + 0.0);   // -0 -> +0
-  return __longlong_as_double((b & ~1023ll) | (b >= 0 ? 1023 - idx : idx));
+// The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  vec: E and the row
+// stride are multiples of four and the rows start aligned, so a chunk is one load.
+template <int LPT, int VPL, bool BF16>
+__device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64_t row, int E, int l, bool on, bool vec,
+                                          float (&z)[VPL]) {
+#pragma unroll
+  for (int c = 0; c < VPL / 4; ++c) {
+    const int e0 = 4 * (l + LPT * c);
+    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (vec) {
+      if (on && e0 < E) {
+        if constexpr (BF16) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(logits) + row + e0);
+          v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+        } else {
+          const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e0);
+          v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (on && e0 + r < E) {
+          if constexpr (BF16) v[r] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[row + e0 + r] << 16);
+          else v[r] = static_cast<const float*>(logits)[row + e0 + r];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z[4 * c + r] = gate_clean(v[r]);
+  }
 }
-__device__ __forceinline__ int gate_index(double key) {
-  const int64_t b = __double_as_longlong(key);
-  return (int)(b >= 0 ? 1023 - (b & 1023) : (b & 1023));
+
+// fp32 vector of the experts (a bias, the loss's derivative), 0 past E.
+template <int LPT, int VPL>
+__device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E, int l, bool vec, float (&out)[VPL]) {
+#pragma unroll
+  for (int c = 0; c < VPL / 4; ++c) {
+    const int e0 = 4 * (l + LPT * c);
+    if (vec) {
+      const float4 w = e0 < E ? *reinterpret_cast<const float4*>(x + e0) : float4{0.f, 0.f, 0.f, 0.f};
+      out[4 * c] = w.x; out[4 * c + 1] = w.y; out[4 * c + 2] = w.z; out[4 * c + 3] = w.w;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) out[4 * c + r] = e0 + r < E ? x[e0 + r] : 0.0f;
+    }
+  }
 }
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
+// Scores of the lane's logits, the softmax's before its division: m is the row's maximum, total their sum
+// over the token.
+template <int LPT, int VPL, bool SIGMOID>
+__device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VPL], float& m, float& total) {
+  m = -kFltMax;
+  if constexpr (!SIGMOID) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) m = fmaxf(m, z[v]);
+    m = group_max_f32<LPT>(m);
+  }
+  total = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    s[v] = SIGMOID ? sigmoid_f32(z[v]) : __expf(z[v] - m);   // 0 for -inf
+    total += s[v];
+  }
+  total = group_sum_f32<LPT>(total);
+}
+
+// ---------------------------------------------------------------- keys
+//
+// 0.0 is no expert: every key of one is above it.  The top of the fp32 range maps to 0x7FBFFFFF, below the
+// patterns of infinity and NaN.
+
+__device__ __forceinline__ double gate_key(float v, int idx) {
+  const uint32_t b = __float_as_uint(v + 0.0f);   // -0 -> +0
+  const uint32_t s = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return __longlong_as_double((int64_t)(((uint64_t)(s >> 1) << 32) | (s << 31) | (uint32_t)(1023 - idx)));
+}
+// The same of a 64-bit value (1e300 and more count as equal; the low 11 bits give way to the index).
+__device__ __forceinline__ double gate_key64(double v, int idx) {
+  const uint64_t b = (uint64_t)__double_as_longlong(fmin(fmax(v, -1e300), 1e300) + 0.0);
+  const uint64_t s = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+  return __longlong_as_double((int64_t)(((s >> 1) & ~1023ull) | (uint32_t)(1023 - idx)));
+}
+__device__ __forceinline__ int gate_index(double key) { return 1023 - (int)(__double_as_longlong(key) & 1023); }
+__device__ __forceinline__ float gate_key_value(double key) {   // of gate_key
+  const uint64_t k = (uint64_t)__double_as_longlong(key);
+  const uint32_t s = (uint32_t)(k >> 31);
+  return __uint_as_float(s ^ ((int32_t)s < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Descending order by Batcher's odd-even merge network.
+template <int N>
+__device__ __forceinline__ void sort_desc(double (&k)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const double a = k[i + j], b = k[i + j + q];
+            k[i + j] = fmax(a, b);
+            k[i + j + q] = fmin(a, b);
+          }
+}
+
 // ---------------------------------------------------------------- work units
 //
 // A workgroup takes one unit: up to `chunk` tokens of one sequence (or of the
-// tokens behind the last one).  Without the loss there is one sequence of all.
+// tokens behind the last one).
 
 struct TokenRange {
   int seq;      // -1: behind the last sequence (or past the end)
@@ -100,6 +185,7 @@ struct GateFwd {
   const void* logits;
   int64_t ld;
   int T, E, topk, renorm, chunk, S;
+  int vec, vec_bias;       // aligned rows, bias
   const float* bias;
   const uint8_t* mask;
   float route_scale;
@@ -109,17 +195,22 @@ struct GateFwd {
   float* part_p;           // [units][E] sums of normalised scores
   int32_t* part_c;         // [units][E] slots choosing the expert
   int32_t* part_n;         // [units] tokens that count
+  int32_t* arrived;        // the loss kernel's counter, cleared here
 };
 
-template <int VPL, bool BF16, bool SIGMOID, bool GATE, bool BAL>
+template <int LPT, int VPL, bool BF16, bool SIGMOID, bool GATE, bool BAL>
 __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
-  __shared__ int s_cnt[BAL ? kGateMaxExperts : 1];
-  __shared__ float s_sum[BAL ? 4 : 1][BAL ? 64 * VPL : 1];
+  constexpr int TPW = 64 / LPT;                  // tokens a wave takes at a time
+  constexpr int KR = LPT == 64 ? 1 : 4;          // slots a lane holds: topk <= min(64, LPT * VPL) <= KR * LPT
+  constexpr int W = LPT * VPL;
+  __shared__ int s_cnt[BAL ? W : 1];
+  __shared__ __attribute__((aligned(16))) float s_sum[BAL ? 256 * VPL : 1];
   __shared__ int s_n[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, g = lane / LPT;
   TokenRange rg;
   if constexpr (BAL) {
     rg = gate_unit(p.offs, p.S, p.T, blockIdx.x, p.chunk);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0;
     for (int e = threadIdx.x; e < p.E; e += 256) s_cnt[e] = 0;
     __syncthreads();
   } else {
@@ -132,103 +223,136 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
 #pragma unroll
   for (int v = 0; v < VPL; ++v) acc[v] = 0.0f;
 
-  for (int t = rg.t0 + wave; t < rg.t1; t += 4) {
-    const bool on = p.mask == nullptr || p.mask[t] != 0;   // wave-uniform
-    const int64_t slot0 = (int64_t)t * p.topk;
-    if (!on) {
-      if constexpr (GATE) {
-        if (lane < p.topk) {
-          p.ids[slot0 + lane] = -1;
-          p.weights[slot0 + lane] = 0.0f;
-        }
-      }
-      continue;
-    }
-    float z[VPL], s[VPL];   // logits; scores up to the softmax's denominator
-    float m = -kFltMax;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int e = lane + 64 * v;
-      z[v] = e < p.E ? gate_logit<BF16>(p.logits, (int64_t)t * p.ld + e) : -INFINITY;
-      m = fmaxf(m, z[v]);
-    }
-    if constexpr (!SIGMOID) m = gate_max(m);
-    float total = 0.0f;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      s[v] = SIGMOID ? sigmoid_f32(z[v]) : __expf(z[v] - m);   // 0 for -inf
-      total += s[v];
-    }
-    if constexpr (!SIGMOID || BAL) total = gate_sum(total);
+  for (int base = rg.t0 + wave * TPW; base < rg.t1; base += 4 * TPW) {   // wave-uniform
+    const int t = base + g;
+    const bool live = t < rg.t1;
+    const bool on = live && (p.mask == nullptr || p.mask[t] != 0);
+    const int64_t row = (int64_t)t * p.ld, slot0 = (int64_t)t * p.topk;
+    float z[VPL], s[VPL], m, total;
+    gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
+    gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);
     const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 
-    int my_id = -1;   // lane j < topk: slot j
+    int my_id[KR];   // slot r * LPT + l
+#pragma unroll
+    for (int r = 0; r < KR; ++r) my_id[r] = -1;
     if constexpr (GATE) {
       double key[VPL];
       if (p.bias == nullptr) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) key[v] = gate_pack((double)z[v], lane + 64 * v);
+        for (int v = 0; v < VPL; ++v)
+          key[v] = z[v] > -INFINITY ? gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
       } else {
-        double d[VPL], dt = 0.0;
+        float b[VPL];
+        gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-          d[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
-          dt += d[v];
+          const float k = fminf((SIGMOID ? s[v] : s[v] * inv) + b[v], kFltMax);
+          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? gate_key(k, 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
         }
-        if constexpr (!SIGMOID) dt = gate_sum(dt);
+      }
+      // One round with fp32 keys; with a bias a second one in 64 bits where they are too close.  Error of an
+      // fp32 key: u = 2^-24; a sigmoid is within 5 u (its exponential's relative error |z| 3 u + 2 u enters
+      // times s (1 - s) <= min(1/4, e^-|z|)), a softmax score within 55 u (exponent e^-x (3 x + 2) u, the sum's
+      // error up to 50 u), the sum with the bias rounds by u |key|.  Two keys can swap below twice that.
+      const float tol = SIGMOID ? 0x1p-20f : 0x1p-17f;
+      for (int round = 0;; ++round) {
+        sort_desc<VPL>(key);
+        float before = INFINITY;
+        bool close = false;
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+          for (int j = 0; j < LPT; ++j) {
+            if (r * LPT + j >= p.topk) break;   // uniform
+            const double best = group_max_f64<LPT>(key[0]);
+            if (l == j) my_id[r] = best > 0.0 ? gate_index(best) : -1;
+            const bool mine = key[0] == best;
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) key[v] = mine ? (v + 1 < VPL ? key[v + 1] : 0.0) : key[v];
+            if (p.bias != nullptr && best > 0.0) {
+              const float k = gate_key_value(best);
+              close = close || before - k <= tol * (1.0f + fabsf(k));
+              before = k;
+            }
+          }
+        }
+        if (p.bias == nullptr || round == 1) break;
+        const double left = group_max_f64<LPT>(key[0]);
+        if (left > 0.0) {
+          const float k = gate_key_value(left);
+          close = close || before - k <= tol * (1.0f + fabsf(k));
+        }
+        if (__ballot(close) == 0) break;
+        float b[VPL];
+        gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
+        double dt = 0.0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-          const int e = lane + 64 * v;
-          const double k = e < p.E ? (SIGMOID ? d[v] : d[v] / dt) + (double)p.bias[e] : 0.0;
-          key[v] = z[v] > -INFINITY ? gate_pack(k, e) : -INFINITY;
+          key[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
+          dt += key[v];
+        }
+        if constexpr (!SIGMOID) dt = group_sum_f64<LPT>(dt);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+          const double k = (SIGMOID ? key[v] : key[v] / dt) + (double)b[v];
+          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
         }
       }
-      for (int j = 0; j < p.topk; ++j) {
-        double best = -INFINITY;
+      float w[KR], ws = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) best = fmax(best, key[v]);
-        best = gate_max(best);
-        if (!(best > -INFINITY)) break;   // no eligible expert left (wave-uniform)
-        if (lane == j) my_id = gate_index(best);
+      for (int r = 0; r < KR; ++r) {
+        w[r] = 0.0f;
+        if (my_id[r] >= 0) {
+          const float zj = gate_logit<BF16>(p.logits, row + my_id[r]);
+          w[r] = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+        }
+        ws += w[r];
+      }
+      if (p.renorm) ws = group_sum_f32<LPT>(ws);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) key[v] = key[v] == best ? -INFINITY : key[v];
-      }
-      float w = 0.0f;
-      if (my_id >= 0) {
-        const float zj = gate_logit<BF16>(p.logits, (int64_t)t * p.ld + my_id);
-        w = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
-      }
-      if (p.renorm) {
-        const float ws = gate_sum(w);
-        w = ws > 0.0f ? __fdiv_rn(w, ws) : 0.0f;   // exactly 1 for a single choice
-      } else if constexpr (!SIGMOID) {
-        w *= inv;
-      }
-      if (lane < p.topk) {
-        p.ids[slot0 + lane] = my_id;
-        p.weights[slot0 + lane] = w * p.route_scale;
+      for (int r = 0; r < KR; ++r) {
+        const int j = r * LPT + l;
+        if (live && j < p.topk) {
+          if (p.renorm) w[r] = ws > 0.0f ? __fdiv_rn(w[r], ws) : 0.0f;   // exactly 1 for a single choice
+          else if constexpr (!SIGMOID) w[r] *= inv;
+          p.ids[slot0 + j] = my_id[r];
+          p.weights[slot0 + j] = w[r] * p.route_scale;
+        }
       }
     }
     if constexpr (BAL) {
-      if (counted) {
-        if constexpr (!GATE)
-          if (lane < p.topk) my_id = p.ids[slot0 + lane];
-        if (my_id >= 0 && my_id < p.E) atomicAdd(&s_cnt[my_id], 1);
-        ++n;
+      if (counted && on) {
+        if constexpr (!GATE) {
+#pragma unroll
+          for (int r = 0; r < KR; ++r)
+            if (r * LPT + l < p.topk) my_id[r] = p.ids[slot0 + r * LPT + l];
+        }
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          if (my_id[r] >= 0 && my_id[r] < p.E) atomicAdd(&s_cnt[my_id[r]], 1);
+        if (l == 0) ++n;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) acc[v] += s[v] * inv;
       }
     }
   }
   if constexpr (BAL) {
+    constexpr int NG = 256 / LPT;   // token groups of the workgroup, each with its share of the sums
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) s_sum[wave][lane + 64 * v] = acc[v];
+    for (int c = 0; c < VPL / 4; ++c)
+      *reinterpret_cast<float4*>(&s_sum[(wave * TPW + g) * W + 4 * (l + LPT * c)]) =
+          float4{acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]};
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
     if (lane == 0) s_n[wave] = n;
     __syncthreads();
     if (!counted) return;
     const int64_t at = (int64_t)blockIdx.x * p.E;
     for (int e = threadIdx.x; e < p.E; e += 256) {
-      p.part_p[at + e] = (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]);
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NG; ++i) sum[i & 3] += s_sum[i * W + e];
+      p.part_p[at + e] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       p.part_c[at + e] = s_cnt[e];
     }
     if (threadIdx.x == 0) p.part_n[blockIdx.x] = (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
@@ -244,8 +368,9 @@ struct GateLoss {
   const float* part_p;
   const int32_t* part_c;
   const int32_t* part_n;
-  double* seq_loss;    // [S]
-  float* loss;         // written here with one sequence
+  double* slice_loss;  // [S][slices]
+  int32_t* arrived;    // 0 on entry
+  float* loss;
   int32_t* counts;     // [S][E]
   float* dprob;        // [S][E]
 };
@@ -257,6 +382,27 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
   if (offs == nullptr) {
     first = 0;
     count = (T + chunk - 1) / chunk;
+    return;
+  }
+  if (S <= 64) {   // every wave on its own, no barrier
+    const int lane = threadIdx.x & 63;
+    int hi = lane < S ? clamp_off(offs[lane], T) : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(hi, d, 64);
+      if (lane >= d) hi = max(hi, o);
+    }
+    int lo = __shfl_up(hi, 1, 64);
+    if (lane == 0) lo = 0;
+    const int cnt = lane < S ? (hi - lo + chunk - 1) / chunk : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    first = __shfl(incl - cnt, s, 64);
+    count = __shfl(cnt, s, 64);
     return;
   }
   __shared__ int tmp[NT / 64], s_hi[NT], s_total, s_first, s_count;
@@ -285,45 +431,75 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
   count = s_count;
 }
 
-// One workgroup per sequence.
-__global__ __launch_bounds__(256) void gate_loss_kernel(GateLoss p) {
-  __shared__ double red[4];
-  const int s = blockIdx.x;
+// One workgroup for 64 experts of a sequence: its 16 waves each add every 16th
+// unit, in 64 bits.  The last workgroup to arrive adds the slices' losses in
+// their order.
+__global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
+  __shared__ double sh_p[16][64];
+  __shared__ int sh_c[16][64], sh_n[16], s_last;
+  __shared__ double red[16];
+  const int s = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
   int first, count;
-  seq_units<256>(p.offs, p.S, p.T, s, p.chunk, first, count);
+  seq_units<1024>(p.offs, p.S, p.T, s, p.chunk, first, count);
   int n = 0;
-  for (int u = 0; u < count; ++u) n += p.part_n[first + u];
-  const double scale = (double)p.coef / p.S;
-  double loss = 0.0;
-  for (int e = threadIdx.x; e < p.E; e += 256) {
-    double sum = 0.0;
-    int c = 0;
+  for (int u = threadIdx.x; u < count; u += 1024) n += p.part_n[first + u];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+  if (lane == 0) sh_n[wave] = n;
+  double sum = 0.0;
+  int c = 0;
+  if (e < p.E) {
 #pragma unroll 4
-    for (int u = 0; u < count; ++u) {
+    for (int u = wave; u < count; u += 16) {
       sum += (double)p.part_p[(int64_t)(first + u) * p.E + e];
       c += p.part_c[(int64_t)(first + u) * p.E + e];
     }
-    const double f = n > 0 ? (double)c * p.E / ((double)p.topk * n) : 0.0;
-    loss += n > 0 ? f * sum / n : 0.0;
-    p.counts[(int64_t)s * p.E + e] = c;
-    p.dprob[(int64_t)s * p.E + e] = n > 0 ? (float)(scale * f / n) : 0.0f;
   }
-  loss = gate_sum(loss);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = loss;
+  sh_p[wave][lane] = sum;
+  sh_c[wave][lane] = c;
+  __syncthreads();
+  if (wave == 0) {
+    n = 0;
+    for (int i = 0; i < 16; ++i) n += sh_n[i];
+    for (int i = 1; i < 16; ++i) {
+      sum += sh_p[i][lane];
+      c += sh_c[i][lane];
+    }
+    const double scale = (double)p.coef / p.S;
+    double loss = 0.0;
+    if (e < p.E) {
+      const double f = n > 0 ? (double)c * p.E / ((double)p.topk * n) : 0.0;
+      loss = n > 0 ? f * sum / n : 0.0;
+      p.counts[(int64_t)s * p.E + e] = c;
+      p.dprob[(int64_t)s * p.E + e] = n > 0 ? (float)(scale * f / n) : 0.0f;
+    }
+    loss = scale * group_sum_f64<64>(loss);
+    const int total = gridDim.x * gridDim.y;
+    if (lane == 0) {
+      if (total == 1) {
+        *p.loss = (float)loss;
+      } else {
+        p.slice_loss[(int64_t)s * gridDim.x + blockIdx.x] = loss;
+        __threadfence();   // before the arrival: the last workgroup reads it
+        s_last = atomicAdd(p.arrived, 1) == total - 1;
+      }
+    }
+  }
+  if (gridDim.x * gridDim.y == 1) return;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  const int total = gridDim.x * gridDim.y;
+  double all = 0.0;
+  for (int i = threadIdx.x; i < total; i += 1024) all += p.slice_loss[i];
+  all = group_sum_f64<64>(all);
+  if (lane == 0) red[wave] = all;
   __syncthreads();
   if (threadIdx.x == 0) {
-    loss = scale * ((red[0] + red[1]) + (red[2] + red[3]));
-    if (p.S == 1) *p.loss = (float)loss;
-    else p.seq_loss[s] = loss;
+    for (int i = 1; i < 16; ++i) all += red[i];
+    *p.loss = (float)all;
   }
-}
-
-__global__ __launch_bounds__(64) void gate_loss_sum_kernel(const double* __restrict__ seq_loss, int S,
-                                                           float* __restrict__ loss) {
-  double t = 0.0;
-  for (int s = threadIdx.x; s < S; s += 64) t += seq_loss[s];
-  t = gate_sum(t);
-  if (threadIdx.x == 0) *loss = (float)t;
 }
 
 // ---------------------------------------------------------------- backward
@@ -333,11 +509,14 @@ __global__ __launch_bounds__(64) void gate_loss_sum_kernel(const double* __restr
 // ds of a chosen expert: route_scale dw, or with renormalisation
 // (route_scale dw - sum over slots of route_scale dw u) / (chosen scores' sum), u the
 // normalised weights; plus the loss's dloss * dprob on the normalised scores.
+// The slots' values reach the lanes that hold their experts through one LDS row a
+// token (the wave's own, so no barrier).
 
 struct GateBwd {
   const void* logits;
   int64_t ld;
   int T, E, topk, renorm, chunk, S;
+  int vec, vec_dprob, vec_out;
   const uint8_t* mask;
   float route_scale;
   const int32_t* ids;
@@ -348,9 +527,19 @@ struct GateBwd {
   void* dlogits;           // [T][E]
 };
 
-template <int VPL, bool BF16, bool SIGMOID>
+// Orders the wave's own LDS accesses for the compiler (the hardware keeps them in order).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int LPT, int VPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int TPW = 64 / LPT, W = LPT * VPL;
+  constexpr int KR = LPT == 64 ? 1 : 4;
+  __shared__ __attribute__((aligned(16))) float s_row[256 * VPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane % LPT, g = lane / LPT;
+  float* const mine = s_row + (wave * TPW + g) * W;
   TokenRange rg;
   if (p.dprob != nullptr) {
     rg = gate_unit(p.offs, p.S, p.T, blockIdx.x, p.chunk);
@@ -358,87 +547,151 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     rg = TokenRange{-1, (int)min(t0, (int64_t)p.T), (int)min(t0 + p.chunk, (int64_t)p.T)};
   }
-  const float dl = p.dloss != nullptr ? *p.dloss : 1.0f;
-  for (int t = rg.t0 + wave; t < rg.t1; t += 4) {
-    const bool on = p.mask == nullptr || p.mask[t] != 0;   // wave-uniform
-    float z[VPL], s[VPL], ds[VPL];
-    float m = -kFltMax;
+  float dp[VPL];   // the loss's gradient by the normalised scores
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int e = lane + 64 * v;
-      z[v] = on && e < p.E ? gate_logit<BF16>(p.logits, (int64_t)t * p.ld + e) : -INFINITY;
-      m = fmaxf(m, z[v]);
-      ds[v] = 0.0f;
+  for (int v = 0; v < VPL; ++v) dp[v] = 0.0f;
+  if (rg.seq >= 0) {
+    const float dl = p.dloss != nullptr ? *p.dloss : 1.0f;
+    gate_load_vec<LPT, VPL>(p.dprob + (int64_t)rg.seq * p.E, p.E, l, p.vec_dprob, dp);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) dp[v] *= dl;
+  }
+  for (int base = rg.t0 + wave * TPW; base < rg.t1; base += 4 * TPW) {   // wave-uniform
+    const int t = base + g;
+    const bool live = t < rg.t1;
+    const bool on = live && (p.mask == nullptr || p.mask[t] != 0);
+    const int64_t row = (int64_t)t * p.ld, slot0 = (int64_t)t * p.topk;
+    float z[VPL], s[VPL], ds[VPL], m, total;
+    gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
+    int id[KR];
+    float dw[KR];
+    if (p.dweights != nullptr) {
+#pragma unroll
+      for (int r = 0; r < KR; ++r) {
+        const int j = r * LPT + l;
+        id[r] = on && j < p.topk ? p.ids[slot0 + j] : -1;
+        if (id[r] < 0 || id[r] >= p.E) id[r] = -1;
+        dw[r] = id[r] >= 0 ? p.dweights[slot0 + j] * p.route_scale : 0.0f;
+      }
     }
-    if (on) {
-      if constexpr (!SIGMOID) m = gate_max(m);
-      float total = 0.0f;
+    gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);   // all scores 0 when the token is off
+    const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+    float dot = 0.0f;
+    if constexpr (SIGMOID) {   // the loss's part through the division by the scores' sum
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) dot += dp[v] * s[v];
+      dot = group_sum_f32<LPT>(dot) * inv;
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? (dp[v] - dot) * inv : dp[v];
+
+    if (p.dweights != nullptr) {
+      if (p.renorm) {
+        float w[KR], ws = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+          w[r] = 0.0f;
+          if (id[r] >= 0) {
+            const float zj = gate_logit<BF16>(p.logits, row + id[r]);
+            w[r] = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+          }
+          ws += w[r];
+        }
+        ws = group_sum_f32<LPT>(ws);
+#pragma unroll
+        for (int r = 0; r < KR; ++r) mean += ws > 0.0f ? dw[r] * __fdiv_rn(w[r], ws) : 0.0f;
+        mean = group_sum_f32<LPT>(mean);
+        // the softmax's denominator cancels between the chosen scores and their sum
+        const float f = ws > 0.0f ? __fdiv_rn(SIGMOID ? 1.0f : total, ws) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * f;
+      }
+      // Slot values into the token's row.  Each slot first leaves its number at its expert: a slot that reads
+      // another's shares its expert with it, and then the slots add up one after another, in their order.
+#pragma unroll
+      for (int c = 0; c < VPL / 4; ++c)
+        *reinterpret_cast<float4*>(mine + 4 * (l + LPT * c)) = float4{0.f, 0.f, 0.f, 0.f};
+      wave_lds_fence();
+#pragma unroll
+      for (int r = 0; r < KR; ++r)
+        if (id[r] >= 0) mine[id[r]] = (float)(r * LPT + l);
+      wave_lds_fence();
+      bool shared = false;
+#pragma unroll
+      for (int r = 0; r < KR; ++r)
+        if (id[r] >= 0) shared = shared || mine[id[r]] != (float)(r * LPT + l);
+      wave_lds_fence();
+      if (__ballot(shared) == 0) {
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          if (id[r] >= 0) mine[id[r]] = dw[r];
+      } else {
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          if (id[r] >= 0) mine[id[r]] = 0.0f;
+        wave_lds_fence();
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          for (int j = 0; j < LPT; ++j) {
+            if (r * LPT + j >= p.topk) break;   // uniform
+            if (l == j && id[r] >= 0) mine[id[r]] += dw[r];
+            wave_lds_fence();
+          }
+      }
+      wave_lds_fence();
+#pragma unroll
+      for (int c = 0; c < VPL / 4; ++c) {
+        const float4 d = *reinterpret_cast<const float4*>(mine + 4 * (l + LPT * c));
+        ds[4 * c] += d.x;
+        ds[4 * c + 1] += d.y;
+        ds[4 * c + 2] += d.z;
+        ds[4 * c + 3] += d.w;
+      }
+      wave_lds_fence();
+    }
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) ds[v] *= s[v] * (1.0f - s[v]);
+    } else {
+      dot = 0.0f;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        s[v] = SIGMOID ? sigmoid_f32(z[v]) : __expf(z[v] - m);
-        total += s[v];
+        s[v] *= inv;
+        dot += s[v] * ds[v];
       }
-      total = gate_sum(total);
-      const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
-      if (rg.seq >= 0) {
-        float dot = 0.0f;
+      dot = group_sum_f32<LPT>(dot);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          const int e = lane + 64 * v;
-          ds[v] = e < p.E ? dl * p.dprob[(int64_t)rg.seq * p.E + e] : 0.0f;
-          dot += ds[v] * s[v];
-        }
-        if constexpr (SIGMOID) {   // through the division by the scores' sum
-          dot = gate_sum(dot) * inv;
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) ds[v] = (ds[v] - dot) * inv;
-        }
-      }
-      if (p.dweights != nullptr) {
-        int id = -1;
-        float dw = 0.0f, w = 0.0f;   // lane j: slot j
-        if (lane < p.topk) id = p.ids[(int64_t)t * p.topk + lane];
-        if (id < 0 || id >= p.E) id = -1;
-        if (id >= 0) {
-          dw = p.dweights[(int64_t)t * p.topk + lane] * p.route_scale;
-          const float zj = gate_logit<BF16>(p.logits, (int64_t)t * p.ld + id);
-          w = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
-        }
-        if (p.renorm) {
-          const float ws = gate_sum(w);
-          const float u = ws > 0.0f ? __fdiv_rn(w, ws) : 0.0f;
-          const float mean = gate_sum(dw * u);
-          // the softmax's denominator cancels between the chosen scores and their sum
-          dw = ws > 0.0f && id >= 0 ? (dw - mean) * __fdiv_rn(SIGMOID ? 1.0f : total, ws) : 0.0f;
-        }
-        for (int j = 0; j < p.topk; ++j) {
-          const int ij = __shfl(id, j, 64);
-          const float dj = __shfl(dw, j, 64);
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) ds[v] += lane + 64 * v == ij ? dj : 0.0f;
-        }
-      }
-      if constexpr (SIGMOID) {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) ds[v] *= s[v] * (1.0f - s[v]);
-      } else {
-        float dot = 0.0f;
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          s[v] *= inv;
-          dot += s[v] * ds[v];
-        }
-        dot = gate_sum(dot);
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
-      }
+      for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
     }
+    if (live) {
+      const int64_t out = (int64_t)t * p.E;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int e = lane + 64 * v;
-      if (e < p.E) {
-        if constexpr (BF16) static_cast<__bf16*>(p.dlogits)[(int64_t)t * p.E + e] = (__bf16)ds[v];
-        else static_cast<float*>(p.dlogits)[(int64_t)t * p.E + e] = ds[v];
+      for (int c = 0; c < VPL / 4; ++c) {
+        const int e0 = 4 * (l + LPT * c);
+        if constexpr (BF16) {
+          __bf16* const o = static_cast<__bf16*>(p.dlogits) + out + e0;
+          if (p.vec_out) {
+            if (e0 < p.E)
+              *reinterpret_cast<u32x2*>(o) =
+                  u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(gt_f32x2{ds[4 * c], ds[4 * c + 1]}, gt_bf16x2)),
+                        __builtin_bit_cast(uint32_t,
+                                           __builtin_convertvector(gt_f32x2{ds[4 * c + 2], ds[4 * c + 3]}, gt_bf16x2))};
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (e0 + r < p.E) o[r] = (__bf16)ds[4 * c + r];
+          }
+        } else {
+          float* const o = static_cast<float*>(p.dlogits) + out + e0;
+          if (p.vec_out) {
+            if (e0 < p.E)
+              *reinterpret_cast<float4*>(o) = float4{ds[4 * c], ds[4 * c + 1], ds[4 * c + 2], ds[4 * c + 3]};
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (e0 + r < p.E) o[r] = ds[4 * c + r];
+          }
+        }
       }
     }
   }
@@ -448,18 +701,22 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 
 template <typename F>
 static hipError_t gate_dispatch(int E, bool bf16, bool sigmoid, F&& f) {
-  auto types = [&](auto vpl) -> hipError_t {
+  auto types = [&](auto lpt, auto vpl) -> hipError_t {
     using T = std::true_type;
     using N = std::false_type;
-    if (bf16) return sigmoid ? f(vpl, T{}, T{}) : f(vpl, T{}, N{});
-    return sigmoid ? f(vpl, N{}, T{}) : f(vpl, N{}, N{});
+    if (bf16) return sigmoid ? f(lpt, vpl, T{}, T{}) : f(lpt, vpl, T{}, N{});
+    return sigmoid ? f(lpt, vpl, N{}, T{}) : f(lpt, vpl, N{}, N{});
   };
-  if (E <= 64) return types(std::integral_constant<int, 1>{});
-  if (E <= 128) return types(std::integral_constant<int, 2>{});
-  if (E <= 256) return types(std::integral_constant<int, 4>{});
-  if (E <= 512) return types(std::integral_constant<int, 8>{});
-  return types(std::integral_constant<int, 16>{});
+  using std::integral_constant;
+  if (E <= 16) return types(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (E <= 64) return types(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (E <= 128) return types(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  if (E <= 256) return types(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+  if (E <= 512) return types(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  return types(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
+
+static bool ptr_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   const bool gate = a.gate, bal = a.loss != nullptr;
@@ -470,8 +727,10 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   p.E = a.E;
   p.topk = a.topk;
   p.renorm = a.renorm;
-  p.chunk = gate_chunk(a.tokens);
+  p.chunk = bal ? gate_chunk(a.tokens, a.E) : gate_step(a.E);
   p.S = a.S;
+  p.vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16);
+  p.vec_bias = a.E % 4 == 0 && ptr_aligned(a.bias, 16);
   p.bias = a.bias;
   p.mask = a.mask;
   p.route_scale = a.route_scale;
@@ -481,31 +740,33 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   p.part_p = nullptr;
   p.part_c = nullptr;
   p.part_n = nullptr;
-  const int64_t units = bal ? gate_units(a.tokens, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
-  double* seq_loss = nullptr;
+  p.arrived = nullptr;
+  const int64_t units = bal ? gate_units(a.tokens, a.E, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
+  const int slices = (a.E + 63) / 64;
+  double* slice_loss = nullptr;
   if (bal) {
-    seq_loss = static_cast<double*>(a.workspace);
-    p.part_p = reinterpret_cast<float*>(seq_loss + a.S);
+    slice_loss = static_cast<double*>(a.workspace);
+    p.part_p = reinterpret_cast<float*>(slice_loss + (int64_t)a.S * slices);
     p.part_c = reinterpret_cast<int32_t*>(p.part_p + units * a.E);
     p.part_n = p.part_c + units * a.E;
+    p.arrived = p.part_n + units;
   }
-  if (a.tokens > 0) {
-    const hipError_t e = gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto vpl, auto bf, auto sg) -> hipError_t {
-      constexpr int V = decltype(vpl)::value;
+  if (units > 0) {
+    const hipError_t e = gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto sg) -> hipError_t {
+      constexpr int L = decltype(lpt)::value, V = decltype(vpl)::value;
       constexpr bool B = decltype(bf)::value, G = decltype(sg)::value;
       const dim3 grid((unsigned)units), block(256);
-      if (gate && bal) hipLaunchKernelGGL((gate_kernel<V, B, G, true, true>), grid, block, 0, st, p);
-      else if (gate) hipLaunchKernelGGL((gate_kernel<V, B, G, true, false>), grid, block, 0, st, p);
-      else hipLaunchKernelGGL((gate_kernel<V, B, G, false, true>), grid, block, 0, st, p);
+      if (gate && bal) hipLaunchKernelGGL((gate_kernel<L, V, B, G, true, true>), grid, block, 0, st, p);
+      else if (gate) hipLaunchKernelGGL((gate_kernel<L, V, B, G, true, false>), grid, block, 0, st, p);
+      else hipLaunchKernelGGL((gate_kernel<L, V, B, G, false, true>), grid, block, 0, st, p);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
   }
   if (!bal) return hipSuccess;
-  const GateLoss l{p.T,      p.E,      p.topk,   p.chunk,  a.S,    a.coef,   a.seq_offs,
-                   p.part_p, p.part_c, p.part_n, seq_loss, a.loss, a.counts, a.dprob};
-  hipLaunchKernelGGL(gate_loss_kernel, dim3((unsigned)a.S), dim3(256), 0, st, l);
-  if (a.S > 1) hipLaunchKernelGGL(gate_loss_sum_kernel, dim3(1), dim3(64), 0, st, seq_loss, a.S, a.loss);
+  const GateLoss l{p.T,      p.E,      p.topk,     p.chunk,   a.S,    a.coef,   a.seq_offs, p.part_p,
+                   p.part_c, p.part_n, slice_loss, p.arrived, a.loss, a.counts, a.dprob};
+  hipLaunchKernelGGL(gate_loss_kernel, dim3((unsigned)slices, (unsigned)a.S), dim3(1024), 0, st, l);
   return hipGetLastError();
 }
 
@@ -518,8 +779,11 @@ hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st) {
   p.E = a.E;
   p.topk = a.topk;
   p.renorm = a.renorm;
-  p.chunk = gate_chunk(a.tokens);
+  p.chunk = gate_chunk(a.tokens, a.E);
   p.S = a.S;
+  p.vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16);
+  p.vec_dprob = a.E % 4 == 0 && ptr_aligned(a.dprob, 16);
+  p.vec_out = a.E % 4 == 0 && ptr_aligned(a.dlogits, a.bf16 ? 8 : 16);
   p.mask = a.mask;
   p.route_scale = a.route_scale;
   p.ids = a.ids;
@@ -528,11 +792,11 @@ hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st) {
   p.dprob = a.dprob;
   p.dloss = a.dloss;
   p.dlogits = a.dlogits;
-  const int64_t units = a.dprob != nullptr ? gate_units(a.tokens, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
-  return gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto vpl, auto bf, auto sg) -> hipError_t {
-    constexpr int V = decltype(vpl)::value;
-    hipLaunchKernelGGL((gate_bwd_kernel<V, decltype(bf)::value, decltype(sg)::value>), dim3((unsigned)units), dim3(256),
-                       0, st, p);
+  const int64_t units =
+      a.dprob != nullptr ? gate_units(a.tokens, a.E, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
+  return gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto sg) -> hipError_t {
+    hipLaunchKernelGGL((gate_bwd_kernel<decltype(lpt)::value, decltype(vpl)::value, decltype(bf)::value, decltype(sg)::value>),
+                       dim3((unsigned)units), dim3(256), 0, st, p);
     return hipGetLastError();
   });
 }

@@ -18,6 +18,7 @@
 // and s, h and the codes once.
 #include "device_common.hpp"
 #include "kernels.hpp"
+#include "lane_groups.hpp"
 #include "validate.hpp"
 
 namespace fp8moe {
@@ -51,26 +52,6 @@ __device__ __forceinline__ void load_gamma(const void* __restrict__ gamma, int c
 #pragma unroll
     for (int k = 0; k < 8; ++k) g[k] = 1.0f;
   }
-}
-
-// Sum over the aligned group of N lanes (16 or 64), the same bits in every lane:
-// each step adds two values that both lanes hold, and addition commutes.
-template <int N>
-__device__ __forceinline__ float group_sum_f32(float v) {
-  auto dpp = [](float a, auto ctl) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(a), decltype(ctl)::value, 0xF, 0xF, false));
-  };
-  v += dpp(v, std::integral_constant<int, 0x128>{});   // row_ror:8
-  v += dpp(v, std::integral_constant<int, 0x124>{});
-  v += dpp(v, std::integral_constant<int, 0x122>{});
-  v += dpp(v, std::integral_constant<int, 0x121>{});
-  if constexpr (N == 64) {
-    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  return v;
 }
 
 struct NormFwd {

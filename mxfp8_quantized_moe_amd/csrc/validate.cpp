@@ -472,18 +472,19 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
   return FP8MOE_OK;
 }
 
-int gate_chunk(int64_t tokens) {
-  int c = 16;
+int gate_step(int32_t E) { return E <= 16 ? 64 : E <= 256 ? 16 : 4; }
+
+int gate_chunk(int64_t tokens, int32_t E) {
+  int c = gate_step(E);
   while (c < 128 && tokens / c > 1024) c *= 2;
   return c;
 }
 
-int64_t gate_units(int64_t tokens, int32_t n_seqs) { return tokens / gate_chunk(tokens) + n_seqs + 1; }
+int64_t gate_units(int64_t tokens, int32_t E, int32_t n_seqs) { return tokens / gate_chunk(tokens, E) + n_seqs + 1; }
 
 int64_t gate_workspace_bytes(int64_t tokens, int32_t E, int32_t n_seqs) {
-  if (tokens < 0 || tokens > kI32Max || E < 1 || E > kGateMaxExperts || n_seqs < 1 || n_seqs > (1 << 20)) return -1;
-  const int64_t units = gate_units(tokens, n_seqs);
-  return 8LL * n_seqs + units * (8LL * E + 4);
+  if (tokens < 0 || tokens > kI32Max || E < 1 || E > kGateMaxExperts || n_seqs < 1 || n_seqs > kGateMaxSeqs) return -1;
+  return 8LL * n_seqs * ((E + 63) / 64) + gate_units(tokens, E, n_seqs) * (8LL * E + 4) + 4;
 }
 
 int check_moe_gate_logits(const void* logits, int dtype, int64_t tokens, int32_t E, int64_t ld, int32_t topk, int score,
@@ -512,8 +513,7 @@ int check_moe_gate(int64_t tokens, int32_t topk, const void* bias, float route_s
 int check_moe_balance(int64_t tokens, int32_t E, int32_t topk, const void* ids, const void* seq_offs, int32_t n_seqs,
                       float coef, const void* loss, const void* counts, const void* dprob, const void* workspace) {
   (void)topk;
-  if (n_seqs < 1 || n_seqs > (1 << 20) || gate_workspace_bytes(tokens, E, n_seqs) < 0) return FP8MOE_ERR_SHAPE;
-  if (gate_units(tokens, n_seqs) > kI32Max) return FP8MOE_ERR_SHAPE;
+  if (gate_workspace_bytes(tokens, E, n_seqs) < 0) return FP8MOE_ERR_SHAPE;
   if (!finite_f32(coef)) return FP8MOE_ERR_VALUE;
   if (n_seqs > 1 && seq_offs == nullptr) return FP8MOE_ERR_NULL;
   if (!need(ids, tokens) || !loss || !counts || !dprob || !workspace) return FP8MOE_ERR_NULL;
@@ -528,7 +528,7 @@ int check_moe_gate_backward(int64_t tokens, int32_t topk, float route_scale, con
                             const void* dlogits, int dtype) {
   (void)topk;
   if (dweights && !finite_f32(route_scale)) return FP8MOE_ERR_VALUE;
-  if (dprob && (n_seqs < 1 || n_seqs > (1 << 20))) return FP8MOE_ERR_SHAPE;
+  if (dprob && (n_seqs < 1 || n_seqs > kGateMaxSeqs)) return FP8MOE_ERR_SHAPE;
   if (dprob && n_seqs > 1 && seq_offs == nullptr) return FP8MOE_ERR_NULL;
   if (tokens && ((!dweights && !dprob) || (dweights && !ids) || !dlogits)) return FP8MOE_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(dweights, 4) || !aligned(seq_offs, 4) || !aligned(dprob, 4) || !aligned(dloss, 4) ||

@@ -5,7 +5,8 @@ ids and counts are whole numbers and must match exactly.  Tolerances, with u = 2
 (u |x|), the product with log2 e (constant and product: 2 u |x|) and 2 u of its own, so (3 X + 2) u relative; the
 denominator holds the same error, at most 22 additions and a reciprocal (2 u); the product one more.  A score is
 within (6 X + 30) u relative, its renormalisation twice that; values below the fp32 normal range may be flushed
-(2^-126 absolute).  The loss adds fp32 sums over at most 32 tokens of a wave and 4 waves: 36 u more.  A logit's gradient
+(2^-126 absolute).  The loss adds fp32 sums
+over at most 32 tokens of a lane, then over the lanes' groups four at a time: at most 35 roundings.  A logit's gradient
 is a sum of terms of total magnitude `size` (oracle), each a product of at most four such factors: (24 X + 160) u size.
 """
 import numpy as np
