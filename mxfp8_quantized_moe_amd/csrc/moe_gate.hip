@@ -48,50 +48,65 @@ __device__ __forceinline__ float gate_logit(const void* __restrict__ logits, int
   else return gate_clean(static_cast<const float*>(logits)[at]);
 }
 
+// A copy the compiler cannot see through: the bounds of the element-wise paths are compared where they are used
+// instead of being kept as one lane mask each (16 spilled mask pairs).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  vec: E and the row
 // stride are multiples of four and the rows start aligned, so a chunk is one load.
 template <int LPT, int VPL, bool BF16>
 __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64_t row, int E, int l, bool on, bool vec,
                                           float (&z)[VPL]) {
+  if (vec) {
 #pragma unroll
-  for (int c = 0; c < VPL / 4; ++c) {
-    const int e0 = 4 * (l + LPT * c);
-    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (vec) {
+    for (int c = 0; c < VPL / 4; ++c) {
+      const int e0 = 4 * (l + LPT * c);
+      float4 w = float4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (on && e0 < E) {
         if constexpr (BF16) {
-          const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(logits) + row + e0);
-          v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+          const u32x2 h = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(logits) + row + e0);
+          w = float4{bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y)};
         } else {
-          const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e0);
-          v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+          w = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e0);
         }
       }
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (on && e0 + r < E) {
-          if constexpr (BF16) v[r] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[row + e0 + r] << 16);
-          else v[r] = static_cast<const float*>(logits)[row + e0 + r];
-        }
+      z[4 * c] = w.x; z[4 * c + 1] = w.y; z[4 * c + 2] = w.z; z[4 * c + 3] = w.w;
     }
+  } else {
+    const int n = on ? opaque(E) : 0;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z[4 * c + r] = gate_clean(v[r]);
+    for (int v = 0; v < VPL; ++v) {
+      const int e = 4 * (l + LPT * (v / 4)) + v % 4;
+      z[v] = -INFINITY;
+      if (e < n) {
+        if constexpr (BF16) z[v] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[row + e] << 16);
+        else z[v] = static_cast<const float*>(logits)[row + e];
+      }
+    }
   }
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) z[v] = gate_clean(z[v]);
 }
 
 // fp32 vector of the experts (a bias, the loss's derivative), 0 past E.
 template <int LPT, int VPL>
 __device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E, int l, bool vec, float (&out)[VPL]) {
+  if (vec) {
 #pragma unroll
-  for (int c = 0; c < VPL / 4; ++c) {
-    const int e0 = 4 * (l + LPT * c);
-    if (vec) {
+    for (int c = 0; c < VPL / 4; ++c) {
+      const int e0 = 4 * (l + LPT * c);
       const float4 w = e0 < E ? *reinterpret_cast<const float4*>(x + e0) : float4{0.f, 0.f, 0.f, 0.f};
       out[4 * c] = w.x; out[4 * c + 1] = w.y; out[4 * c + 2] = w.z; out[4 * c + 3] = w.w;
-    } else {
+    }
+  } else {
+    const int n = opaque(E);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) out[4 * c + r] = e0 + r < E ? x[e0 + r] : 0.0f;
+    for (int v = 0; v < VPL; ++v) {
+      const int e = 4 * (l + LPT * (v / 4)) + v % 4;
+      out[v] = e < n ? x[e] : 0.0f;
     }
   }
 }
@@ -119,8 +134,9 @@ __device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VP
 
 // ---------------------------------------------------------------- keys
 //
-// 0.0 is no expert: every key of one is above it.  The top of the fp32 range maps to 0x7FBFFFFF, below the
-// patterns of infinity and NaN.
+// The fp32 range -FLT_MAX .. FLT_MAX maps to the high words 0x00400000 .. 0x7FBFFFFF, below the patterns of
+// infinity and NaN; -inf (no eligible expert) maps below all of them, and so does 0.0 (an emptied list).
+constexpr double kLeastKey = 0x1p-1019;   // high word 0x00400000
 
 __device__ __forceinline__ double gate_key(float v, int idx) {
   const uint32_t b = __float_as_uint(v + 0.0f);   // -0 -> +0
@@ -156,6 +172,28 @@ __device__ __forceinline__ void sort_desc(double (&k)[N]) {
             k[i + j] = fmax(a, b);
             k[i + j + q] = fmin(a, b);
           }
+}
+
+// The list without its head where `take`: of a sorted list only the first topk keys can be chosen.
+template <int N>
+__device__ __forceinline__ void move_up(double (&k)[N], bool take, int topk) {
+  auto shift = [&](auto last_tag) {
+    constexpr int LAST = decltype(last_tag)::value;
+#pragma unroll
+    for (int v = 0; v < LAST; ++v) {
+      const double here = k[v], next = k[v + 1];
+      k[v] = take ? next : here;
+    }
+    const double here = k[LAST];
+    k[LAST] = take ? 0.0 : here;
+  };
+  if constexpr (N > 8) {
+    if (topk <= 8) {
+      shift(std::integral_constant<int, 7>{});
+      return;
+    }
+  }
+  shift(std::integral_constant<int, N - 1>{});
 }
 
 // ---------------------------------------------------------------- work units
@@ -241,14 +279,14 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       if (p.bias == nullptr) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-          key[v] = z[v] > -INFINITY ? gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
+          key[v] = gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4);
       } else {
         float b[VPL];
         gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
-          const float k = fminf((SIGMOID ? s[v] : s[v] * inv) + b[v], kFltMax);
-          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? gate_key(k, 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
+          const float k = gate_clean((SIGMOID ? s[v] : s[v] * inv) + b[v]);
+          key[v] = gate_key(z[v] > -INFINITY ? k : -INFINITY, 4 * (l + LPT * (v / 4)) + v % 4);
         }
       }
       // One round with fp32 keys; with a bias a second one in 64 bits where they are too close.  Error of an
@@ -258,6 +296,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       const float tol = SIGMOID ? 0x1p-20f : 0x1p-17f;
       for (int round = 0;; ++round) {
         sort_desc<VPL>(key);
+        const double ninth = key[VPL > 8 ? 8 : 0];
         float before = INFINITY;
         bool close = false;
 #pragma unroll
@@ -265,11 +304,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           for (int j = 0; j < LPT; ++j) {
             if (r * LPT + j >= p.topk) break;   // uniform
             const double best = group_max_f64<LPT>(key[0]);
-            if (l == j) my_id[r] = best > 0.0 ? gate_index(best) : -1;
-            const bool mine = key[0] == best;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) key[v] = mine ? (v + 1 < VPL ? key[v + 1] : 0.0) : key[v];
-            if (p.bias != nullptr && best > 0.0) {
+            if (l == j) my_id[r] = best >= kLeastKey ? gate_index(best) : -1;
+            move_up<VPL>(key, key[0] == best, p.topk);
+            if (p.bias != nullptr && best >= kLeastKey) {
               const float k = gate_key_value(best);
               close = close || before - k <= tol * (1.0f + fabsf(k));
               before = k;
@@ -277,8 +314,11 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           }
         }
         if (p.bias == nullptr || round == 1) break;
+        // the first key left out (move_up keeps eight of a lane's keys for topk 8: one that gave all eight away
+        // and had a ninth cannot tell)
+        if constexpr (VPL > 8) close = close || (p.topk == 8 && key[0] == 0.0 && ninth >= kLeastKey);
         const double left = group_max_f64<LPT>(key[0]);
-        if (left > 0.0) {
+        if (left >= kLeastKey) {
           const float k = gate_key_value(left);
           close = close || before - k <= tol * (1.0f + fabsf(k));
         }
@@ -295,7 +335,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
           const double k = (SIGMOID ? key[v] : key[v] / dt) + (double)b[v];
-          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4) : 0.0;
+          const double packed = gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4);
+          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
         }
       }
       float w[KR], ws = 0.0f;
