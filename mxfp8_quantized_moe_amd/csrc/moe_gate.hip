@@ -297,33 +297,41 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       for (int round = 0;; ++round) {
         sort_desc<VPL>(key);
         const double ninth = key[VPL > 8 ? 8 : 0];
-        float before = INFINITY;
-        bool close = false;
+        double last = 0.0, my_key[KR];   // this lane's choices
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
+          my_key[r] = 0.0;
           for (int j = 0; j < LPT; ++j) {
             if (r * LPT + j >= p.topk) break;   // uniform
-            const double best = group_max_f64<LPT>(key[0]);
-            if (l == j) my_id[r] = best >= kLeastKey ? gate_index(best) : -1;
-            move_up<VPL>(key, key[0] == best, p.topk);
-            if (p.bias != nullptr && best >= kLeastKey) {
-              const float k = gate_key_value(best);
-              close = close || before - k <= tol * (1.0f + fabsf(k));
-              before = k;
-            }
+            last = group_max_f64<LPT>(key[0]);
+            if (l == j) my_key[r] = last;
+            move_up<VPL>(key, key[0] == last, p.topk);
           }
         }
+#pragma unroll
+        for (int r = 0; r < KR; ++r) my_id[r] = my_key[r] >= kLeastKey ? gate_index(my_key[r]) : -1;
         if (p.bias == nullptr || round == 1) break;
-        // the first key left out (move_up keeps eight of a lane's keys for topk 8: one that gave all eight away
-        // and had a ninth cannot tell)
+        // Each choice against the next one, the last against the first key left out (move_up keeps eight of a
+        // lane's keys for topk 8: one that gave all eight away and had a ninth cannot tell).
+        auto near = [&](double a, double b) {
+          const float x = gate_key_value(a), y = gate_key_value(b);
+          return b >= kLeastKey && x - y <= tol * (1.0f + fabsf(y));
+        };
+        bool close = near(last, group_max_f64<LPT>(key[0]));
         if constexpr (VPL > 8) close = close || (p.topk == 8 && key[0] == 0.0 && ninth >= kLeastKey);
-        const double left = group_max_f64<LPT>(key[0]);
-        if (left >= kLeastKey) {
-          const float k = gate_key_value(left);
-          close = close || before - k <= tol * (1.0f + fabsf(k));
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+          if (r * LPT >= p.topk) break;   // uniform
+          // slot r LPT + l - 1: the lane below, or the last lane of the block before
+          const double up = __shfl_up(my_key[r], 1, LPT);
+          const double over = r > 0 ? __shfl(my_key[r > 0 ? r - 1 : 0], LPT - 1, LPT) : 0.0;
+          const double prev = l > 0 ? up : over;
+          close = close || (prev >= kLeastKey && near(prev, my_key[r]));
         }
         if (__ballot(close) == 0) break;
+        // loaded again: this round is rare, and what it needs would occupy registers through the first one
         float b[VPL];
+        gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
         gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
         double dt = 0.0;
 #pragma unroll
@@ -342,6 +350,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       float w[KR], ws = 0.0f;
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
+        if (r * LPT >= p.topk) break;   // uniform
         w[r] = 0.0f;
         if (my_id[r] >= 0) {
           const float zj = gate_logit<BF16>(p.logits, row + my_id[r]);
@@ -352,6 +361,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       if (p.renorm) ws = group_sum_f32<LPT>(ws);
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
+        if (r * LPT >= p.topk) break;   // uniform
         const int j = r * LPT + l;
         if (live && j < p.topk) {
           if (p.renorm) w[r] = ws > 0.0f ? __fdiv_rn(w[r], ws) : 0.0f;   // exactly 1 for a single choice
