@@ -16,14 +16,18 @@
 // 4 (l + LPT c) + 0..3, which are 16-byte loads and stores.  Sums and maxima over a
 // token then take 2, 4 or 6 VALU lane steps, shared by the wave's tokens.
 //
-// Selection: a key is an fp32 value made sortable as an unsigned integer, with the
-// complemented expert index below it, all in the 63 low bits of a positive double,
-// so that one v_max_f64 compares values and breaks ties to the lower index.  Each
-// lane sorts its VPL keys once (a network of max/min pairs); a choice is then the
-// group's maximum of the list heads, and the lane that owned it moves its list up.
-// With a bias the fp32 keys carry rounding errors: where two consecutive choices
-// (or the last choice and the first key left out) are closer than those errors
-// allow, the wave forms its keys again in 64 bits and selects once more.
+// Selection, first round: a key is an fp32 value (the logit, or score + bias) made
+// sortable as an unsigned integer, its low four bits replaced by the complement of
+// the value's place in the lane.  Each lane sorts its VPL keys once (a network of
+// max/min pairs); a choice is then the group's maximum of the list heads, equal
+// heads go to the lower place and then to the lower lane, which is the lower
+// expert, and the lane that owned the head moves its list up.  The chosen experts'
+// exact values are formed anyway, for the weights: where two consecutive choices
+// are in the wrong order or, with a bias, closer than the rounding of fp32 keys
+// allows, or where the first key left out may be as large as the last choice, the
+// wave selects again in a second round over keys that hold everything: the exact
+// fp32 logit, or score + bias formed in 64 bits, above the expert's index, as a
+// positive double.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "lane_groups.hpp"
@@ -36,6 +40,12 @@ static_assert(kGateMaxExperts == 1024, "a key's index has ten bits; 64 lanes hol
 constexpr float kFltMax = 3.402823466e38f;
 typedef float gt_f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 gt_bf16x2 __attribute__((ext_vector_type(2)));
+
+// Orders the wave's own LDS accesses for the compiler (the hardware keeps them in order).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // ---------------------------------------------------------------- logits
 
@@ -133,14 +143,21 @@ __device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VP
 }
 
 // ---------------------------------------------------------------- keys
-//
-// The fp32 range -FLT_MAX .. FLT_MAX maps to the high words 0x00400000 .. 0x7FBFFFFF, below the patterns of
-// infinity and NaN; -inf (no eligible expert) maps below all of them, and so does 0.0 (an emptied list).
-constexpr double kLeastKey = 0x1p-1019;   // high word 0x00400000
 
-__device__ __forceinline__ double gate_key(float v, int idx) {
+__device__ __forceinline__ uint32_t sortable(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);   // -0 -> +0
-  const uint32_t s = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float sorted_value(uint32_t s) {
+  return __uint_as_float(s ^ ((int32_t)s < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+constexpr uint32_t kLeast32 = 0x00800000u;   // -FLT_MAX; -inf (no eligible expert) and 0 (an emptied list) are below
+
+// Keys of the second round: positive doubles, the expert's complemented index in the low ten bits.  The fp32
+// range maps to the high words 0x00400000 .. 0x7FBFFFFF, below the patterns of infinity and NaN.
+constexpr double kLeastKey = 0x1p-1019;      // high word 0x00400000
+__device__ __forceinline__ double gate_key(float v, int idx) {
+  const uint32_t s = sortable(v);
   return __longlong_as_double((int64_t)(((uint64_t)(s >> 1) << 32) | (s << 31) | (uint32_t)(1023 - idx)));
 }
 // The same of a 64-bit value (1e300 and more count as equal; the low 11 bits give way to the index).
@@ -150,15 +167,14 @@ __device__ __forceinline__ double gate_key64(double v, int idx) {
   return __longlong_as_double((int64_t)(((s >> 1) & ~1023ull) | (uint32_t)(1023 - idx)));
 }
 __device__ __forceinline__ int gate_index(double key) { return 1023 - (int)(__double_as_longlong(key) & 1023); }
-__device__ __forceinline__ float gate_key_value(double key) {   // of gate_key
-  const uint64_t k = (uint64_t)__double_as_longlong(key);
-  const uint32_t s = (uint32_t)(k >> 31);
-  return __uint_as_float(s ^ ((int32_t)s < 0 ? 0x80000000u : 0xFFFFFFFFu));
-}
 
 // Descending order by Batcher's odd-even merge network.
-template <int N>
-__device__ __forceinline__ void sort_desc(double (&k)[N]) {
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
+template <typename T, int N>
+__device__ __forceinline__ void sort_desc(T (&k)[N]) {
 #pragma unroll
   for (int p = 1; p < N; p *= 2)
 #pragma unroll
@@ -168,24 +184,36 @@ __device__ __forceinline__ void sort_desc(double (&k)[N]) {
 #pragma unroll
         for (int i = 0; i < q; ++i)
           if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const double a = k[i + j], b = k[i + j + q];
-            k[i + j] = fmax(a, b);
-            k[i + j + q] = fmin(a, b);
+            const T a = k[i + j], b = k[i + j + q];
+            k[i + j] = larger(a, b);
+            k[i + j + q] = smaller(a, b);
           }
 }
 
+// Whether this is the lowest lane of its group of LPT for which `is` holds.
+template <int LPT>
+__device__ __forceinline__ bool lowest_lane(bool is, int lane) {
+  const uint64_t all = __ballot(is);
+  if constexpr (LPT == 64) {
+    return lane == __ffsll((unsigned long long)all) - 1;
+  } else {
+    const uint32_t m = (uint32_t)(all >> (lane & ~(LPT - 1))) & ((1u << LPT) - 1u);
+    return (m & (0u - m)) == 1u << (lane & (LPT - 1));
+  }
+}
+
 // The list without its head where `take`: of a sorted list only the first topk keys can be chosen.
-template <int N>
-__device__ __forceinline__ void move_up(double (&k)[N], bool take, int topk) {
+template <typename T, int N>
+__device__ __forceinline__ void move_up(T (&k)[N], bool take, int topk) {
   auto shift = [&](auto last_tag) {
     constexpr int LAST = decltype(last_tag)::value;
 #pragma unroll
     for (int v = 0; v < LAST; ++v) {
-      const double here = k[v], next = k[v + 1];
+      const T here = k[v], next = k[v + 1];
       k[v] = take ? next : here;
     }
-    const double here = k[LAST];
-    k[LAST] = take ? 0.0 : here;
+    const T here = k[LAST];
+    k[LAST] = take ? T(0) : here;
   };
   if constexpr (N > 8) {
     if (topk <= 8) {
@@ -241,6 +269,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   constexpr int TPW = 64 / LPT;                  // tokens a wave takes at a time
   constexpr int KR = LPT == 64 ? 1 : 4;          // slots a lane holds: topk <= min(64, LPT * VPL) <= KR * LPT
   constexpr int W = LPT * VPL;
+  constexpr int SLOTS = W < kGateMaxTopk ? W : kGateMaxTopk;
+  __shared__ int s_slot[GATE ? 256 / LPT * SLOTS : 1];   // the choices' lanes and places, a row a token
   __shared__ int s_cnt[BAL ? W : 1];
   __shared__ __attribute__((aligned(16))) float s_sum[BAL ? 256 * VPL : 1];
   __shared__ int s_n[4];
@@ -275,76 +305,113 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
 #pragma unroll
     for (int r = 0; r < KR; ++r) my_id[r] = -1;
     if constexpr (GATE) {
-      double key[VPL];
-      if (p.bias == nullptr) {
+      const bool biased = p.bias != nullptr;
+      const int last_r = (p.topk - 1) / LPT, last_l = (p.topk - 1) % LPT;
+      bool close = false;
+      {
+        uint32_t key[VPL];
+        if (!biased) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v)
-          key[v] = gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4);
-      } else {
-        float b[VPL];
-        gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
+          for (int v = 0; v < VPL; ++v) key[v] = (sortable(z[v]) & ~15u) | (uint32_t)(15 - v);
+        } else {
+          float b[VPL];
+          gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          const float k = gate_clean((SIGMOID ? s[v] : s[v] * inv) + b[v]);
-          key[v] = gate_key(z[v] > -INFINITY ? k : -INFINITY, 4 * (l + LPT * (v / 4)) + v % 4);
-        }
-      }
-      // One round with fp32 keys; with a bias a second one in 64 bits where they are too close.  Error of an
-      // fp32 key: u = 2^-24; a sigmoid is within 5 u (its exponential's relative error |z| 3 u + 2 u enters
-      // times s (1 - s) <= min(1/4, e^-|z|)), a softmax score within 55 u (exponent e^-x (3 x + 2) u, the sum's
-      // error up to 50 u), the sum with the bias rounds by u |key|.  Two keys can swap below twice that.
-      const float tol = SIGMOID ? 0x1p-20f : 0x1p-17f;
-      for (int round = 0;; ++round) {
-        sort_desc<VPL>(key);
-        const double ninth = key[VPL > 8 ? 8 : 0];
-        double last = 0.0, my_key[KR];   // this lane's choices
-#pragma unroll
-        for (int r = 0; r < KR; ++r) {
-          my_key[r] = 0.0;
-          for (int j = 0; j < LPT; ++j) {
-            if (r * LPT + j >= p.topk) break;   // uniform
-            last = group_max_f64<LPT>(key[0]);
-            if (l == j) my_key[r] = last;
-            move_up<VPL>(key, key[0] == last, p.topk);
+          for (int v = 0; v < VPL; ++v) {
+            const float k = gate_clean((SIGMOID ? s[v] : s[v] * inv) + b[v]);
+            key[v] = (sortable(z[v] > -INFINITY ? k : -INFINITY) & ~15u) | (uint32_t)(15 - v);
           }
         }
-#pragma unroll
-        for (int r = 0; r < KR; ++r) my_id[r] = my_key[r] >= kLeastKey ? gate_index(my_key[r]) : -1;
-        if (p.bias == nullptr || round == 1) break;
-        // Each choice against the next one, the last against the first key left out (move_up keeps eight of a
-        // lane's keys for topk 8: one that gave all eight away and had a ninth cannot tell).
-        auto near = [&](double a, double b) {
-          const float x = gate_key_value(a), y = gate_key_value(b);
-          return b >= kLeastKey && x - y <= tol * (1.0f + fabsf(y));
-        };
-        bool close = near(last, group_max_f64<LPT>(key[0]));
-        if constexpr (VPL > 8) close = close || (p.topk == 8 && key[0] == 0.0 && ninth >= kLeastKey);
+        sort_desc(key);
+        const uint32_t ninth = key[VPL > 8 ? 8 : 0];
+        int* const slot = s_slot + (wave * TPW + g) * SLOTS;
+        for (int j = 0; j < p.topk; ++j) {
+          // the two lowest bits are the place in a chunk: lanes whose heads agree above them hold neighbouring experts
+          const uint32_t head = key[0] & ~3u;
+          const uint32_t best = group_max_u32<LPT>(head);
+          const bool mine = lowest_lane<LPT>(head == best, lane);
+          if (mine) slot[j] = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
+          move_up(key, mine, p.topk);
+        }
+        const uint32_t left = group_max_u32<LPT>(key[0] & ~3u);
+        wave_lds_fence();
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
           if (r * LPT >= p.topk) break;   // uniform
-          // slot r LPT + l - 1: the lane below, or the last lane of the block before
-          const double up = __shfl_up(my_key[r], 1, LPT);
-          const double over = r > 0 ? __shfl(my_key[r > 0 ? r - 1 : 0], LPT - 1, LPT) : 0.0;
-          const double prev = l > 0 ? up : over;
-          close = close || (prev >= kLeastKey && near(prev, my_key[r]));
+          const int raw = r * LPT + l < p.topk ? slot[r * LPT + l] : -1;
+          const int v = 15 - (raw & 15);
+          my_id[r] = raw >= 0 ? 4 * ((raw >> 4) + LPT * (v >> 2)) + (v & 3) : -1;
         }
-        if (__ballot(close) == 0) break;
+        wave_lds_fence();
+        // move_up keeps eight of a lane's keys for topk 8: one that gave all eight away and had a ninth cannot
+        // tell what is left
+        if constexpr (VPL > 8) close = p.topk == 8 && key[0] == 0u && ninth >= kLeast32;
+        // Error of an fp32 key with a bias, u = 2^-24: a sigmoid is within 5 u (its exponential's relative error
+        // |z| 3 u + 2 u enters times s (1 - s) <= min(1/4, e^-|z|)), a softmax score within 55 u (exponent
+        // e^-x (3 x + 2) u, the sum's error up to 50 u), the sum with the bias rounds by u |key|.  Two keys can
+        // swap below twice that.  A key without its low four bits is lower by less than 2^-19 of its value.
+        const float tol = SIGMOID ? 0x1p-20f : 0x1p-17f;
+        float before = 0.0f;   // slot r LPT - 1
+        int before_id = -1;
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+          if (r * LPT >= p.topk) break;   // uniform
+          float x = -INFINITY;
+          if (my_id[r] >= 0) {
+            x = gate_logit<BF16>(p.logits, row + my_id[r]);
+            if (biased) x = gate_clean((SIGMOID ? sigmoid_f32(x) : __expf(x - m) * inv) + p.bias[my_id[r]]);
+          }
+          const float xp = __shfl_up(x, 1, LPT);
+          const int ip = __shfl_up(my_id[r], 1, LPT);
+          const float xb = l > 0 ? xp : before;
+          const int ib = l > 0 ? ip : before_id;
+          if (ib >= 0 && my_id[r] >= 0)
+            close = close || (biased ? xb - x <= tol * (1.0f + fabsf(x)) : !(xb > x || (xb == x && ib < my_id[r])));
+          if (r == last_r && l == last_l && left >= kLeast32) {
+            const float y = sorted_value(left & ~15u);
+            close = close || (biased ? x - y <= tol * (1.0f + fabsf(y)) + 0x1p-18f * fabsf(y)
+                                     : !BF16 && ((sortable(x) ^ left) & ~15u) == 0);
+          }
+          if (r + 1 < KR) {
+            before = __shfl(x, LPT - 1, LPT);
+            before_id = __shfl(my_id[r], LPT - 1, LPT);
+          }
+        }
+      }
+      if (__ballot(close) != 0) {   // second round
         // loaded again: this round is rare, and what it needs would occupy registers through the first one
-        float b[VPL];
+        double key[VPL];
         gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
-        gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
-        double dt = 0.0;
+        if (!biased) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          key[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
-          dt += key[v];
+          for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4);
+        } else {
+          float b[VPL];
+          gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
+          double dt = 0.0;
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) {
+            key[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
+            dt += key[v];
+          }
+          if constexpr (!SIGMOID) dt = group_sum_f64<LPT>(dt);
+#pragma unroll
+          for (int v = 0; v < VPL; ++v) {
+            const double k = (SIGMOID ? key[v] : key[v] / dt) + (double)b[v];
+            const double packed = gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4);
+            key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
+          }
         }
-        if constexpr (!SIGMOID) dt = group_sum_f64<LPT>(dt);
+        sort_desc(key);
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-          const double k = (SIGMOID ? key[v] : key[v] / dt) + (double)b[v];
-          const double packed = gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4);
-          key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
+        for (int r = 0; r < KR; ++r) {
+          my_id[r] = -1;
+          for (int j = 0; j < LPT; ++j) {
+            if (r * LPT + j >= p.topk) break;   // uniform
+            const double best = group_max_f64<LPT>(key[0]);
+            if (l == j) my_id[r] = best >= kLeastKey ? gate_index(best) : -1;
+            move_up(key, key[0] == best, p.topk);
+          }
         }
       }
       float w[KR], ws = 0.0f;
@@ -577,12 +644,6 @@ struct GateBwd {
   const float* dloss;      // null: 1
   void* dlogits;           // [T][E]
 };
-
-// Orders the wave's own LDS accesses for the compiler (the hardware keeps them in order).
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
 
 template <int LPT, int VPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
