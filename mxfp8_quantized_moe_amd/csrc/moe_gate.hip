@@ -58,19 +58,12 @@ __device__ __forceinline__ float gate_logit(const void* __restrict__ logits, int
   else return gate_clean(static_cast<const float*>(logits)[at]);
 }
 
-// A copy the compiler cannot see through: the bounds of the element-wise paths are compared where they are used
-// instead of being kept as one lane mask each (16 spilled mask pairs).
-__device__ __forceinline__ int opaque(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-// The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  vec: E and the row
-// stride are multiples of four and the rows start aligned, so a chunk is one load.
-template <int LPT, int VPL, bool BF16>
-__device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64_t row, int E, int l, bool on, bool vec,
+// The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  VEC: E and the row
+// stride are multiples of four and every array of experts starts aligned, so a chunk is one load.
+template <int LPT, int VPL, bool BF16, bool VEC>
+__device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64_t row, int E, int l, bool on,
                                           float (&z)[VPL]) {
-  if (vec) {
+  if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < VPL / 4; ++c) {
       const int e0 = 4 * (l + LPT * c);
@@ -86,7 +79,7 @@ __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64
       z[4 * c] = w.x; z[4 * c + 1] = w.y; z[4 * c + 2] = w.z; z[4 * c + 3] = w.w;
     }
   } else {
-    const int n = on ? opaque(E) : 0;
+    const int n = on ? E : 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int e = 4 * (l + LPT * (v / 4)) + v % 4;
@@ -102,9 +95,9 @@ __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64
 }
 
 // fp32 vector of the experts (a bias, the loss's derivative), 0 past E.
-template <int LPT, int VPL>
-__device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E, int l, bool vec, float (&out)[VPL]) {
-  if (vec) {
+template <int LPT, int VPL, bool VEC>
+__device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E, int l, float (&out)[VPL]) {
+  if constexpr (VEC) {
 #pragma unroll
     for (int c = 0; c < VPL / 4; ++c) {
       const int e0 = 4 * (l + LPT * c);
@@ -112,11 +105,10 @@ __device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E
       out[4 * c] = w.x; out[4 * c + 1] = w.y; out[4 * c + 2] = w.z; out[4 * c + 3] = w.w;
     }
   } else {
-    const int n = opaque(E);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int e = 4 * (l + LPT * (v / 4)) + v % 4;
-      out[v] = e < n ? x[e] : 0.0f;
+      out[v] = e < E ? x[e] : 0.0f;
     }
   }
 }
@@ -224,6 +216,48 @@ __device__ __forceinline__ void move_up(T (&k)[N], bool take, int topk) {
   shift(std::integral_constant<int, N - 1>{});
 }
 
+// The second round for one token (row, wave-uniform), by a whole wave: chosen[r] of lane l is slot
+// r LPT + l % LPT.  m: the row's largest logit (softmax).
+template <int VPL, int LPT, int KR, bool BF16, bool SIGMOID, bool VEC>
+__device__ __forceinline__ void select_exact(const void* __restrict__ logits, int64_t row, int E,
+                                             const float* __restrict__ bias, float m, int topk, int (&chosen)[KR]) {
+  const int lane = threadIdx.x & 63;
+  float z[VPL];
+  double key[VPL];
+  gate_load<64, VPL, BF16, VEC>(logits, row, E, lane, true, z);
+  if (bias == nullptr) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], 4 * (lane + 64 * (v / 4)) + v % 4);
+  } else {
+    float b[VPL];
+    gate_load_vec<64, VPL, VEC>(bias, E, lane, b);
+    double total = 0.0;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      key[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
+      total += key[v];
+    }
+    if constexpr (!SIGMOID) total = group_sum_f64<64>(total);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      const double k = (SIGMOID ? key[v] : key[v] / total) + (double)b[v];
+      const double packed = gate_key64(k, 4 * (lane + 64 * (v / 4)) + v % 4);
+      key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
+    }
+  }
+  sort_desc(key);
+#pragma unroll
+  for (int r = 0; r < KR; ++r) {
+    chosen[r] = -1;
+    for (int j = 0; j < LPT; ++j) {
+      if (r * LPT + j >= topk) break;   // uniform
+      const double best = group_max_f64<64>(key[0]);
+      if (lane % LPT == j) chosen[r] = best >= kLeastKey ? gate_index(best) : -1;
+      move_up(key, key[0] == best, topk);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- work units
 //
 // A workgroup takes one unit: up to `chunk` tokens of one sequence (or of the
@@ -251,7 +285,6 @@ struct GateFwd {
   const void* logits;
   int64_t ld;
   int T, E, topk, renorm, chunk, S;
-  int vec, vec_bias;       // aligned rows, bias
   const float* bias;
   const uint8_t* mask;
   float route_scale;
@@ -264,7 +297,7 @@ struct GateFwd {
   int32_t* arrived;        // the loss kernel's counter, cleared here
 };
 
-template <int LPT, int VPL, bool BF16, bool SIGMOID, bool GATE, bool BAL>
+template <int LPT, int VPL, bool BF16, bool VEC, bool SIGMOID, bool GATE, bool BAL>
 __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   constexpr int TPW = 64 / LPT;                  // tokens a wave takes at a time
   constexpr int KR = LPT == 64 ? 1 : 4;          // slots a lane holds: topk <= min(64, LPT * VPL) <= KR * LPT
@@ -297,7 +330,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
     const bool on = live && (p.mask == nullptr || p.mask[t] != 0);
     const int64_t row = (int64_t)t * p.ld, slot0 = (int64_t)t * p.topk;
     float z[VPL], s[VPL], m, total;
-    gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
+    gate_load<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, on, z);
     gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);
     const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 
@@ -315,7 +348,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           for (int v = 0; v < VPL; ++v) key[v] = (sortable(z[v]) & ~15u) | (uint32_t)(15 - v);
         } else {
           float b[VPL];
-          gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
+          gate_load_vec<LPT, VPL, VEC>(p.bias, p.E, l, b);
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
             const float k = gate_clean((SIGMOID ? s[v] : s[v] * inv) + b[v]);
@@ -378,41 +411,16 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           }
         }
       }
-      if (__ballot(close) != 0) {   // second round
-        // loaded again: this round is rare, and what it needs would occupy registers through the first one
-        double key[VPL];
-        gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
-        if (!biased) {
+      // Second round: the whole wave takes one token after another of those that need it, so its wide keys
+      // occupy few registers beside the first round's.
+      for (uint64_t todo = __ballot(close); todo != 0;) {
+        const int gc = (__ffsll((unsigned long long)todo) - 1) / LPT;   // wave-uniform
+        todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << (gc * (LPT & 63)));
+        int chosen[KR];
+        select_exact<W <= 256 ? 4 : VPL, LPT, KR, BF16, SIGMOID, VEC>(p.logits, (int64_t)(base + gc) * p.ld, p.E, p.bias,
+                                                                     __shfl(m, gc * LPT, 64), p.topk, chosen);
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], 4 * (l + LPT * (v / 4)) + v % 4);
-        } else {
-          float b[VPL];
-          gate_load_vec<LPT, VPL>(p.bias, p.E, l, p.vec_bias, b);
-          double dt = 0.0;
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) {
-            key[v] = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[v])) : exp((double)z[v] - (double)m);
-            dt += key[v];
-          }
-          if constexpr (!SIGMOID) dt = group_sum_f64<LPT>(dt);
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) {
-            const double k = (SIGMOID ? key[v] : key[v] / dt) + (double)b[v];
-            const double packed = gate_key64(k, 4 * (l + LPT * (v / 4)) + v % 4);
-            key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
-          }
-        }
-        sort_desc(key);
-#pragma unroll
-        for (int r = 0; r < KR; ++r) {
-          my_id[r] = -1;
-          for (int j = 0; j < LPT; ++j) {
-            if (r * LPT + j >= p.topk) break;   // uniform
-            const double best = group_max_f64<LPT>(key[0]);
-            if (l == j) my_id[r] = best >= kLeastKey ? gate_index(best) : -1;
-            move_up(key, key[0] == best, p.topk);
-          }
-        }
+        for (int r = 0; r < KR; ++r) my_id[r] = g == gc ? chosen[r] : my_id[r];
       }
       float w[KR], ws = 0.0f;
 #pragma unroll
@@ -634,7 +642,6 @@ struct GateBwd {
   const void* logits;
   int64_t ld;
   int T, E, topk, renorm, chunk, S;
-  int vec, vec_dprob, vec_out;
   const uint8_t* mask;
   float route_scale;
   const int32_t* ids;
@@ -645,7 +652,7 @@ struct GateBwd {
   void* dlogits;           // [T][E]
 };
 
-template <int LPT, int VPL, bool BF16, bool SIGMOID>
+template <int LPT, int VPL, bool BF16, bool VEC, bool SIGMOID>
 __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
   constexpr int TPW = 64 / LPT, W = LPT * VPL;
   constexpr int KR = LPT == 64 ? 1 : 4;
@@ -664,7 +671,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
   for (int v = 0; v < VPL; ++v) dp[v] = 0.0f;
   if (rg.seq >= 0) {
     const float dl = p.dloss != nullptr ? *p.dloss : 1.0f;
-    gate_load_vec<LPT, VPL>(p.dprob + (int64_t)rg.seq * p.E, p.E, l, p.vec_dprob, dp);
+    gate_load_vec<LPT, VPL, VEC>(p.dprob + (int64_t)rg.seq * p.E, p.E, l, dp);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) dp[v] *= dl;
   }
@@ -674,7 +681,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     const bool on = live && (p.mask == nullptr || p.mask[t] != 0);
     const int64_t row = (int64_t)t * p.ld, slot0 = (int64_t)t * p.topk;
     float z[VPL], s[VPL], ds[VPL], m, total;
-    gate_load<LPT, VPL, BF16>(p.logits, row, p.E, l, on, p.vec, z);
+    gate_load<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, on, z);
     int id[KR];
     float dw[KR];
     if (p.dweights != nullptr) {
@@ -782,7 +789,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         const int e0 = 4 * (l + LPT * c);
         if constexpr (BF16) {
           __bf16* const o = static_cast<__bf16*>(p.dlogits) + out + e0;
-          if (p.vec_out) {
+          if constexpr (VEC) {
             if (e0 < p.E)
               *reinterpret_cast<u32x2*>(o) =
                   u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(gt_f32x2{ds[4 * c], ds[4 * c + 1]}, gt_bf16x2)),
@@ -795,7 +802,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
           }
         } else {
           float* const o = static_cast<float*>(p.dlogits) + out + e0;
-          if (p.vec_out) {
+          if constexpr (VEC) {
             if (e0 < p.E)
               *reinterpret_cast<float4*>(o) = float4{ds[4 * c], ds[4 * c + 1], ds[4 * c + 2], ds[4 * c + 3]};
           } else {
@@ -812,12 +819,15 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 // ---------------------------------------------------------------- launchers
 
 template <typename F>
-static hipError_t gate_dispatch(int E, bool bf16, bool sigmoid, F&& f) {
+static hipError_t gate_dispatch(int E, bool bf16, bool vec, bool sigmoid, F&& f) {
+  using T = std::true_type;
+  using N = std::false_type;
   auto types = [&](auto lpt, auto vpl) -> hipError_t {
-    using T = std::true_type;
-    using N = std::false_type;
-    if (bf16) return sigmoid ? f(lpt, vpl, T{}, T{}) : f(lpt, vpl, T{}, N{});
-    return sigmoid ? f(lpt, vpl, N{}, T{}) : f(lpt, vpl, N{}, N{});
+    auto scored = [&](auto bf, auto ve) -> hipError_t {
+      return sigmoid ? f(lpt, vpl, bf, ve, T{}) : f(lpt, vpl, bf, ve, N{});
+    };
+    if (bf16) return vec ? scored(T{}, T{}) : scored(T{}, N{});
+    return vec ? scored(N{}, T{}) : scored(N{}, N{});
   };
   using std::integral_constant;
   if (E <= 16) return types(integral_constant<int, 4>{}, integral_constant<int, 4>{});
@@ -841,8 +851,7 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   p.renorm = a.renorm;
   p.chunk = bal ? gate_chunk(a.tokens, a.E) : gate_step(a.E);
   p.S = a.S;
-  p.vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16);
-  p.vec_bias = a.E % 4 == 0 && ptr_aligned(a.bias, 16);
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16) && ptr_aligned(a.bias, 16);
   p.bias = a.bias;
   p.mask = a.mask;
   p.route_scale = a.route_scale;
@@ -864,13 +873,13 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
     p.arrived = p.part_n + units;
   }
   if (units > 0) {
-    const hipError_t e = gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto sg) -> hipError_t {
+    const hipError_t e = gate_dispatch(a.E, a.bf16, vec, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto ve, auto sg) -> hipError_t {
       constexpr int L = decltype(lpt)::value, V = decltype(vpl)::value;
-      constexpr bool B = decltype(bf)::value, G = decltype(sg)::value;
+      constexpr bool B = decltype(bf)::value, A = decltype(ve)::value, G = decltype(sg)::value;
       const dim3 grid((unsigned)units), block(256);
-      if (gate && bal) hipLaunchKernelGGL((gate_kernel<L, V, B, G, true, true>), grid, block, 0, st, p);
-      else if (gate) hipLaunchKernelGGL((gate_kernel<L, V, B, G, true, false>), grid, block, 0, st, p);
-      else hipLaunchKernelGGL((gate_kernel<L, V, B, G, false, true>), grid, block, 0, st, p);
+      if (gate && bal) hipLaunchKernelGGL((gate_kernel<L, V, B, A, G, true, true>), grid, block, 0, st, p);
+      else if (gate) hipLaunchKernelGGL((gate_kernel<L, V, B, A, G, true, false>), grid, block, 0, st, p);
+      else hipLaunchKernelGGL((gate_kernel<L, V, B, A, G, false, true>), grid, block, 0, st, p);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
@@ -893,9 +902,8 @@ hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st) {
   p.renorm = a.renorm;
   p.chunk = gate_chunk(a.tokens, a.E);
   p.S = a.S;
-  p.vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16);
-  p.vec_dprob = a.E % 4 == 0 && ptr_aligned(a.dprob, 16);
-  p.vec_out = a.E % 4 == 0 && ptr_aligned(a.dlogits, a.bf16 ? 8 : 16);
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16) &&
+                   ptr_aligned(a.dlogits, a.bf16 ? 8 : 16) && ptr_aligned(a.dprob, 16);
   p.mask = a.mask;
   p.route_scale = a.route_scale;
   p.ids = a.ids;
@@ -906,9 +914,10 @@ hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st) {
   p.dlogits = a.dlogits;
   const int64_t units =
       a.dprob != nullptr ? gate_units(a.tokens, a.E, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
-  return gate_dispatch(a.E, a.bf16, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto sg) -> hipError_t {
-    hipLaunchKernelGGL((gate_bwd_kernel<decltype(lpt)::value, decltype(vpl)::value, decltype(bf)::value, decltype(sg)::value>),
-                       dim3((unsigned)units), dim3(256), 0, st, p);
+  return gate_dispatch(a.E, a.bf16, vec, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto ve, auto sg) -> hipError_t {
+    constexpr int L = decltype(lpt)::value, V = decltype(vpl)::value;
+    constexpr bool B = decltype(bf)::value, A = decltype(ve)::value, G = decltype(sg)::value;
+    hipLaunchKernelGGL((gate_bwd_kernel<L, V, B, A, G>), dim3((unsigned)units), dim3(256), 0, st, p);
     return hipGetLastError();
   });
 }
