@@ -294,7 +294,7 @@ struct GateFwd {
   float* part_p;           // [units][E] sums of normalised scores
   int32_t* part_c;         // [units][E] slots choosing the expert
   int32_t* part_n;         // [units] tokens that count
-  int32_t* arrived;        // the loss kernel's counter, cleared here
+  uint64_t* total;         // the loss kernel's sum and counter, cleared here
 };
 
 template <int LPT, int VPL, bool BF16, bool VEC, bool SIGMOID, bool GATE, bool BAL>
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   TokenRange rg;
   if constexpr (BAL) {
     rg = gate_unit(p.offs, p.S, p.T, blockIdx.x, p.chunk);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0;
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.total[threadIdx.x] = 0;
     for (int e = threadIdx.x; e < p.E; e += 256) s_cnt[e] = 0;
     __syncthreads();
   } else {
@@ -341,6 +341,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       const bool biased = p.bias != nullptr;
       const int last_r = (p.topk - 1) / LPT, last_l = (p.topk - 1) % LPT;
       bool close = false;
+      float chosen_z[KR];   // the chosen logits
       {
         uint32_t key[VPL];
         if (!biased) {
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           if (r * LPT >= p.topk) break;   // uniform
           float x = -INFINITY;
           if (my_id[r] >= 0) {
-            x = gate_logit<BF16>(p.logits, row + my_id[r]);
+            chosen_z[r] = x = gate_logit<BF16>(p.logits, row + my_id[r]);
             if (biased) x = gate_clean((SIGMOID ? sigmoid_f32(x) : __expf(x - m) * inv) + p.bias[my_id[r]]);
           }
           const float xp = __shfl_up(x, 1, LPT);
@@ -413,6 +414,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       }
       // Second round: the whole wave takes one token after another of those that need it, so its wide keys
       // occupy few registers beside the first round's.
+      const bool again = __ballot(close) != 0;
       for (uint64_t todo = __ballot(close); todo != 0;) {
         const int gc = (__ffsll((unsigned long long)todo) - 1) / LPT;   // wave-uniform
         todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << (gc * (LPT & 63)));
@@ -428,8 +430,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
         if (r * LPT >= p.topk) break;   // uniform
         w[r] = 0.0f;
         if (my_id[r] >= 0) {
-          const float zj = gate_logit<BF16>(p.logits, row + my_id[r]);
-          w[r] = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+          if (again) chosen_z[r] = gate_logit<BF16>(p.logits, row + my_id[r]);
+          w[r] = SIGMOID ? sigmoid_f32(chosen_z[r]) : __expf(chosen_z[r] - m);
         }
         ws += w[r];
       }
@@ -487,6 +489,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
 
 // ---------------------------------------------------------------- the loss from the units' sums
 
+constexpr int kLossSlice = 32;   // experts a workgroup of the loss kernel adds up
+
 struct GateLoss {
   int T, E, topk, chunk, S;
   float coef;
@@ -494,8 +498,7 @@ struct GateLoss {
   const float* part_p;
   const int32_t* part_c;
   const int32_t* part_n;
-  double* slice_loss;  // [S][slices]
-  int32_t* arrived;    // 0 on entry
+  uint64_t* total;     // sum over slices in units of 2^-50, slices that added theirs; 0 on entry
   float* loss;
   int32_t* counts;     // [S][E]
   float* dprob;        // [S][E]
@@ -557,75 +560,80 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
   count = s_count;
 }
 
-// One workgroup for 64 experts of a sequence: its 16 waves each add every 16th
-// unit, in 64 bits.  The last workgroup to arrive adds the slices' losses in
-// their order.
+// One workgroup for 32 experts of a sequence: its 32 half-waves each add every 32nd
+// unit, eight loads in flight, in 64 bits.  The sum over slices, sum f P <= E, is
+// kept as a whole number of 2^-50: additions of whole numbers do not depend on their order.
+// Each addition has come back before its slice counts as arrived, so the last one finds them all.
 __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
-  __shared__ double sh_p[16][64];
-  __shared__ int sh_c[16][64], sh_n[16], s_last;
-  __shared__ double red[16];
+  constexpr int B = 8;
+  __shared__ double sh_p[32][kLossSlice];
+  __shared__ int sh_c[32][kLossSlice], sh_n[16];
   const int s = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane;
+  const int i0 = threadIdx.x / kLossSlice, ie = threadIdx.x % kLossSlice;
+  const int e = blockIdx.x * kLossSlice + ie;
   int first, count;
   seq_units<1024>(p.offs, p.S, p.T, s, p.chunk, first, count);
   int n = 0;
   for (int u = threadIdx.x; u < count; u += 1024) n += p.part_n[first + u];
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
-  if (lane == 0) sh_n[wave] = n;
   double sum = 0.0;
   int c = 0;
   if (e < p.E) {
-#pragma unroll 4
-    for (int u = wave; u < count; u += 16) {
-      sum += (double)p.part_p[(int64_t)(first + u) * p.E + e];
-      c += p.part_c[(int64_t)(first + u) * p.E + e];
-    }
-  }
-  sh_p[wave][lane] = sum;
-  sh_c[wave][lane] = c;
-  __syncthreads();
-  if (wave == 0) {
-    n = 0;
-    for (int i = 0; i < 16; ++i) n += sh_n[i];
-    for (int i = 1; i < 16; ++i) {
-      sum += sh_p[i][lane];
-      c += sh_c[i][lane];
-    }
-    const double scale = (double)p.coef / p.S;
-    double loss = 0.0;
-    if (e < p.E) {
-      const double f = n > 0 ? (double)c * p.E / ((double)p.topk * n) : 0.0;
-      loss = n > 0 ? f * sum / n : 0.0;
-      p.counts[(int64_t)s * p.E + e] = c;
-      p.dprob[(int64_t)s * p.E + e] = n > 0 ? (float)(scale * f / n) : 0.0f;
-    }
-    loss = scale * group_sum_f64<64>(loss);
-    const int total = gridDim.x * gridDim.y;
-    if (lane == 0) {
-      if (total == 1) {
-        *p.loss = (float)loss;
-      } else {
-        p.slice_loss[(int64_t)s * gridDim.x + blockIdx.x] = loss;
-        __threadfence();   // before the arrival: the last workgroup reads it
-        s_last = atomicAdd(p.arrived, 1) == total - 1;
+    for (int u0 = i0; u0 < count; u0 += 32 * B) {
+      float q[B];
+      int d[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        // a unit past the last one loads the last one again: no branch between the loads
+        const int64_t at = (int64_t)(first + min(u0 + 32 * i, count - 1)) * p.E + e;
+        q[i] = p.part_p[at];
+        d[i] = p.part_c[at];
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const bool in = u0 + 32 * i < count;
+        sum += in ? (double)q[i] : 0.0;
+        c += in ? d[i] : 0;
       }
     }
   }
-  if (gridDim.x * gridDim.y == 1) return;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+  if (lane == 0) sh_n[wave] = n;
+  sh_p[i0][ie] = sum;
+  sh_c[i0][ie] = c;
   __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  const int total = gridDim.x * gridDim.y;
-  double all = 0.0;
-  for (int i = threadIdx.x; i < total; i += 1024) all += p.slice_loss[i];
-  all = group_sum_f64<64>(all);
-  if (lane == 0) red[wave] = all;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) all += red[i];
-    *p.loss = (float)all;
+  if (wave != 0) return;   // lanes of the upper half of wave 0 repeat the lower half's sums
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) n += sh_n[i];
+  sum = 0.0;
+  c = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    sum += sh_p[i][ie];
+    c += sh_c[i][ie];
   }
+  const double inv_n = n > 0 ? 1.0 / n : 0.0;
+  const double f = (double)c * p.E / p.topk * inv_n;
+  const double scale = (double)p.coef / p.S;
+  if (lane < kLossSlice && e < p.E) {
+    p.counts[(int64_t)s * p.E + e] = c;
+    p.dprob[(int64_t)s * p.E + e] = (float)(scale * f * inv_n);
+  }
+  const double part = group_sum_f64<64>(lane < kLossSlice && e < p.E ? f * sum * inv_n : 0.0);
+  if (lane != 0) return;
+  const unsigned slices = gridDim.x * gridDim.y;
+  if (slices == 1) {
+    *p.loss = (float)(scale * part);
+    return;
+  }
+  auto add = [](uint64_t* at, uint64_t v) {
+    return __hip_atomic_fetch_add(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  uint64_t before = add(p.total, (uint64_t)(part * 0x1p50 + 0.5));
+  asm volatile("s_waitcnt vmcnt(0)" : "+v"(before)::"memory");   // its value is here: the addition is done
+  if (add(p.total + 1, 1) != slices - 1) return;
+  *p.loss = (float)(scale * ((double)add(p.total, 0) * 0x1p-50));
 }
 
 // ---------------------------------------------------------------- backward
@@ -861,16 +869,14 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   p.part_p = nullptr;
   p.part_c = nullptr;
   p.part_n = nullptr;
-  p.arrived = nullptr;
+  p.total = nullptr;
   const int64_t units = bal ? gate_units(a.tokens, a.E, a.S) : (a.tokens + p.chunk - 1) / p.chunk;
-  const int slices = (a.E + 63) / 64;
-  double* slice_loss = nullptr;
+  const int slices = (a.E + kLossSlice - 1) / kLossSlice;
   if (bal) {
-    slice_loss = static_cast<double*>(a.workspace);
-    p.part_p = reinterpret_cast<float*>(slice_loss + (int64_t)a.S * slices);
+    p.total = static_cast<uint64_t*>(a.workspace);
+    p.part_p = reinterpret_cast<float*>(p.total + 2);
     p.part_c = reinterpret_cast<int32_t*>(p.part_p + units * a.E);
     p.part_n = p.part_c + units * a.E;
-    p.arrived = p.part_n + units;
   }
   if (units > 0) {
     const hipError_t e = gate_dispatch(a.E, a.bf16, vec, a.sigmoid, [&](auto lpt, auto vpl, auto bf, auto ve, auto sg) -> hipError_t {
@@ -885,8 +891,8 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (!bal) return hipSuccess;
-  const GateLoss l{p.T,      p.E,      p.topk,     p.chunk,   a.S,    a.coef,   a.seq_offs, p.part_p,
-                   p.part_c, p.part_n, slice_loss, p.arrived, a.loss, a.counts, a.dprob};
+  const GateLoss l{p.T,      p.E,      p.topk,   p.chunk, a.S,    a.coef,   a.seq_offs,
+                   p.part_p, p.part_c, p.part_n, p.total, a.loss, a.counts, a.dprob};
   hipLaunchKernelGGL(gate_loss_kernel, dim3((unsigned)slices, (unsigned)a.S), dim3(1024), 0, st, l);
   return hipGetLastError();
 }

@@ -484,7 +484,7 @@ int64_t gate_units(int64_t tokens, int32_t E, int32_t n_seqs) { return tokens / 
 
 int64_t gate_workspace_bytes(int64_t tokens, int32_t E, int32_t n_seqs) {
   if (tokens < 0 || tokens > kI32Max || E < 1 || E > kGateMaxExperts || n_seqs < 1 || n_seqs > kGateMaxSeqs) return -1;
-  return 8LL * n_seqs * ((E + 63) / 64) + gate_units(tokens, E, n_seqs) * (8LL * E + 4) + 4;
+  return 16 + gate_units(tokens, E, n_seqs) * (8LL * E + 4);
 }
 
 int check_moe_gate_logits(const void* logits, int dtype, int64_t tokens, int32_t E, int64_t ld, int32_t topk, int score,
