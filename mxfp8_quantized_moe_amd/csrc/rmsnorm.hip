@@ -288,13 +288,21 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwd p) {
     const bool valid = row < p.rows;
     const int64_t r = valid ? row : 0;
     const float rstd = valid ? p.rstd[r] : 0.0f;
-    u32x4 dv[ITEMS], sv[ITEMS];
+    u32x4 dv[ITEMS], sv[ITEMS], ev[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = i * TPR + lt;
       const bool in = valid && c < p.nchunk;
       dv[i] = in ? reinterpret_cast<const u32x4*>(p.dh + r * cols)[c] : u32x4{0, 0, 0, 0};
       sv[i] = in ? reinterpret_cast<const u32x4*>(p.s + r * cols)[c] : u32x4{0, 0, 0, 0};
+      ev[i] = u32x4{0, 0, 0, 0};
+    }
+    if (p.dsum != nullptr) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int c = i * TPR + lt;
+        if (valid && c < p.nchunk) ev[i] = reinterpret_cast<const u32x4*>(p.dsum + r * cols)[c];
+      }
     }
     float dot = 0.0f;
 #pragma unroll
@@ -331,12 +339,7 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwd p) {
         unpack8(dv[i], d);
         unpack8(sv[i], n);
         load_gamma<GT>(p.gamma, c, g);
-        if (p.dsum != nullptr) {
-          unpack8(reinterpret_cast<const u32x4*>(p.dsum + r * cols)[c], e);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] = 0.0f;
-        }
+        unpack8(ev[i], e);
 #pragma unroll
         for (int k = 0; k < 8; ++k) e[k] += rstd * (d[k] * g[k] - n[k] * rstd * m);
         reinterpret_cast<u32x4*>(p.dx + r * cols)[c] = pack8(e);
@@ -374,20 +377,33 @@ __global__ __launch_bounds__(256) void rmsnorm_bwd_kernel(NormBwd p) {
   }
 }
 
-// dgamma[c] = the workgroups' shares added in order: 64 columns and 4 row ranges per workgroup.
-__global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* __restrict__ part, int n, int64_t cols,
-                                                             float* __restrict__ dgamma) {
-  __shared__ float sh[4][64];
+// dgamma[c] = the workgroups' shares added in a fixed order: 64 columns a workgroup, whose 16 waves each add every
+// 16th share, eight loads in flight.
+__global__ __launch_bounds__(1024) void rmsnorm_dgamma_kernel(const float* __restrict__ part, int n, int64_t cols,
+                                                              float* __restrict__ dgamma) {
+  constexpr int B = 8;
+  __shared__ float sh[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   float t = 0.0f;
   if (c < cols) {
-#pragma unroll 8
-    for (int i = w; i < n; i += 4) t += part[(int64_t)i * cols + c];
+    for (int i0 = w; i0 < n; i0 += 16 * B) {
+      float v[B];
+      // a share past the last one loads the last one again: no branch between the loads
+#pragma unroll
+      for (int i = 0; i < B; ++i) v[i] = part[(int64_t)min(i0 + 16 * i, n - 1) * cols + c];
+#pragma unroll
+      for (int i = 0; i < B; ++i) t += i0 + 16 * i < n ? v[i] : 0.0f;
+    }
   }
   sh[w][lane] = t;
   __syncthreads();
-  if (w == 0 && c < cols) dgamma[c] = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+  if (w == 0 && c < cols) {
+    t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sh[i][lane];
+    dgamma[c] = t;
+  }
 }
 
 template <int TPR, int ITEMS>
@@ -420,6 +436,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dh, const uint16_t* s, const 
     const int items = (p.nchunk + TPR - 1) / TPR;
     if (items <= 1) return launch_bwd_g<TPR, 1>(p, gt, grid, st);
     if (items <= 2) return launch_bwd_g<TPR, 2>(p, gt, grid, st);
+    if (items <= 3) return launch_bwd_g<TPR, 3>(p, gt, grid, st);
     if constexpr (TPR == 256)
       if (items > 4) return launch_bwd_g<TPR, 8>(p, gt, grid, st);
     return launch_bwd_g<TPR, 4>(p, gt, grid, st);
@@ -431,7 +448,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dh, const uint16_t* s, const 
     else e = pick(std::integral_constant<int, 256>{});
   }
   if (e != hipSuccess || dgamma == nullptr) return e;
-  hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, st, workspace, grid,
+  hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(1024), 0, st, workspace, grid,
                      cols, dgamma);
   return hipGetLastError();
 }

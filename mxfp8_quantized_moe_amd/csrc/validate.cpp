@@ -450,7 +450,7 @@ int check_rmsnorm_mx(int rule, int layout, int64_t rows, int64_t cols, const voi
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
   const int64_t rpb = cols <= 512 ? 16 : cols <= 2048 ? 4 : 1;   // rows a workgroup takes at a time
   const int64_t steps = (rows + rpb - 1) / rpb;
-  return (int)(steps < 1024 ? steps : 1024);
+  return (int)(steps < 512 ? steps : 512);
 }
 
 int64_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
