@@ -70,13 +70,32 @@ struct NormFwd {
   int layout;             // MX scale layout
 };
 
+// Four e4m3fnuz codes of f * s.  A code's value is half the e4m3fn value of the same code, so enc_fnuz(y) =
+// enc_fn(2y) up to 224 (doubling is exact); 2y above the tie 464 is 240 (0x7F: the low bit on top of the clamped
+// 448's 0x7E), and a zero result drops its sign.  On whole words: 24 operations for four codes, where four single
+// codes take over 40.
+__device__ __forceinline__ uint32_t quant4_fnuz(float a, float b, float c, float d, float s) {
+  const float s2 = 2.0f * s;
+  const float y[4] = {a * s2, b * s2, c * s2, d * s2};
+  float k[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k[i] = __builtin_amdgcn_fmed3f(y[i], -448.0f, 448.0f);
+    top |= fabsf(y[i]) > 464.0f ? 1u << (8 * i) : 0u;
+  }
+  const uint32_t w = cvt_fn_pair<true>(k[2], k[3], cvt_fn_pair<false>(k[0], k[1], 0u)) | top;
+  const uint32_t mag = w & 0x7F7F7F7Fu;
+  return mag | (w & (mag + 0x7F7F7F7Fu) & 0x80808080u);   // the sign where the magnitude is not 0
+}
+
 // FMT 0: rowwise e4m3fn, 1: rowwise e4m3fnuz, 2: MX floor rule, 3: MX ceil rule, 4: no codes.
 template <int TPR, int ITEMS, int FMT, int GT>
-__global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
-  constexpr int RPB = 256 / TPR;
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd p) {
+  constexpr int NT = TPR > 256 ? TPR : 256, RPB = NT / TPR, WAVES = TPR / 64;
   constexpr bool MX = FMT == 2 || FMT == 3, ROWWISE = FMT < 2;
-  __shared__ float red_s[4];
-  __shared__ uint32_t red_m[4];
+  __shared__ float red_s[TPR > 64 ? WAVES : 1];
+  __shared__ uint32_t red_m[TPR > 64 ? WAVES : 1];
   const int lt = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool valid = row < p.rows;
@@ -111,26 +130,31 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
     }
   }
   float ss = 0.0f;
-  float am[ITEMS];   // largest |s * gamma| of each chunk
+  float f[ITEMS][8];   // s * gamma
+  float am[ITEMS];     // its largest magnitude in each chunk
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c = i * TPR + lt;
-    float a[8], g[8];
-    unpack8(v[i], a);
+    float g[8];
+    unpack8(v[i], f[i]);
     am[i] = 0.0f;
     if (c < p.nchunk) {
       load_gamma<GT>(p.gamma, c, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        ss += a[k] * a[k];
-        am[i] = fmaxf(am[i], fabsf(a[k] * g[k]));
+        ss += f[i][k] * f[i][k];
+        f[i][k] *= g[k];
+        am[i] = fmaxf(am[i], fabsf(f[i][k]));
       }
     }
   }
-  float rm = 0.0f;
+  uint32_t mb = 0;   // the row's largest magnitude (non-negative: its bits are ordered like the values)
+  if constexpr (ROWWISE) {
+    float rm = 0.0f;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) rm = fmaxf(rm, am[i]);
-  uint32_t mb = __float_as_uint(rm);   // non-negative: ordered like the values
+    for (int i = 0; i < ITEMS; ++i) rm = fmaxf(rm, am[i]);
+    mb = __float_as_uint(rm);
+  }
   if constexpr (TPR <= 64) {
     ss = group_sum_f32<TPR>(ss);
     if constexpr (ROWWISE) mb = group_max_u32<TPR>(mb);
@@ -143,8 +167,18 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
       red_m[w] = mb;
     }
     __syncthreads();
-    ss = (red_s[0] + red_s[1]) + (red_s[2] + red_s[3]);
-    if constexpr (ROWWISE) mb = max(max(red_m[0], red_m[1]), max(red_m[2], red_m[3]));
+    float part[WAVES];
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) part[i] = red_s[i];
+#pragma unroll
+    for (int n = WAVES / 2; n >= 1; n /= 2)
+#pragma unroll
+      for (int i = 0; i < n; ++i) part[i] += part[i + n];
+    ss = part[0];
+    if constexpr (ROWWISE) {
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) mb = max(mb, red_m[i]);
+    }
   }
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ss * p.inv_c + p.eps));
   float scale = 0.0f;
@@ -158,16 +192,16 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
   for (int i = 0; i < ITEMS; ++i) {
     const int c = i * TPR + lt;
     const bool in = valid && c < p.nchunk;
-    float a[8], g[8];
-    unpack8(v[i], a);
-    if (c < p.nchunk) load_gamma<GT>(p.gamma, c, g);
+    float(&a)[8] = f[i];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = c < p.nchunk ? a[k] * g[k] * rstd : 0.0f;
+    for (int k = 0; k < 8; ++k) a[k] *= rstd;
     if (in && p.h != nullptr) reinterpret_cast<u32x4*>(p.h + r * cols)[c] = pack8(a);
     if constexpr (ROWWISE) {
-      if (in)
-        reinterpret_cast<u32x2*>(p.q + r * cols)[c] =
-            u32x2{quant4<FMT>(a[0], a[1], a[2], a[3], scale), quant4<FMT>(a[4], a[5], a[6], a[7], scale)};
+      auto four = [&](int k) {
+        if constexpr (FMT == 0) return quant4<0>(a[k], a[k + 1], a[k + 2], a[k + 3], scale);
+        else return quant4_fnuz(a[k], a[k + 1], a[k + 2], a[k + 3], scale);
+      };
+      if (in) reinterpret_cast<u32x2*>(p.q + r * cols)[c] = u32x2{four(0), four(4)};
     }
     if constexpr (MX) {
       // four lanes hold one block (chunks 4b .. 4b+3; TPR is a multiple of four)
@@ -195,8 +229,8 @@ __global__ __launch_bounds__(256) void rmsnorm_kernel(NormFwd p) {
 
 template <int TPR, int ITEMS, int FMT>
 static hipError_t launch_fwd_g(const NormFwd& p, int gt, hipStream_t st) {
-  constexpr int RPB = 256 / TPR;
-  const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(256);
+  constexpr int NT = TPR > 256 ? TPR : 256, RPB = NT / TPR;
+  const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(NT);
   if (gt == 0) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 0>), grid, block, 0, st, p);
   else if (gt == 1) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 1>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 2>), grid, block, 0, st, p);
@@ -205,18 +239,22 @@ static hipError_t launch_fwd_g(const NormFwd& p, int gt, hipStream_t st) {
 
 template <int FMT>
 static hipError_t launch_fwd(const NormFwd& p, int gt, hipStream_t st) {
-  auto pick = [&](auto tpr_tag) -> hipError_t {
-    constexpr int TPR = decltype(tpr_tag)::value;
-    const int items = (p.nchunk + TPR - 1) / TPR;
-    if (items <= 1) return launch_fwd_g<TPR, 1, FMT>(p, gt, st);
-    if (items <= 2) return launch_fwd_g<TPR, 2, FMT>(p, gt, st);
-    if constexpr (TPR == 256)
-      if (items > 4) return launch_fwd_g<TPR, 8, FMT>(p, gt, st);   // cols <= kNormMaxCols
-    return launch_fwd_g<TPR, 4, FMT>(p, gt, st);
-  };
-  if (p.nchunk <= 64) return pick(std::integral_constant<int, 16>{});
-  if (p.nchunk <= 256) return pick(std::integral_constant<int, 64>{});
-  return pick(std::integral_constant<int, 256>{});
+  const int n = p.nchunk;   // <= 2048
+  if (n <= 16) return launch_fwd_g<16, 1, FMT>(p, gt, st);
+  if (n <= 32) return launch_fwd_g<16, 2, FMT>(p, gt, st);
+  if (n <= 64) return launch_fwd_g<16, 4, FMT>(p, gt, st);
+  if (n <= 128) return launch_fwd_g<64, 2, FMT>(p, gt, st);
+  if (n <= 256) return launch_fwd_g<64, 4, FMT>(p, gt, st);
+  // Few long rows (at most two workgroups a compute unit): a row's latency counts.
+  if (p.rows <= 512) {
+    if (n <= 1024) return launch_fwd_g<1024, 1, FMT>(p, gt, st);
+    return launch_fwd_g<1024, 2, FMT>(p, gt, st);
+  }
+  if (n <= 320) return launch_fwd_g<64, 5, FMT>(p, gt, st);   // 256 threads would leave the second chunk mostly empty
+  if (n <= 512) return launch_fwd_g<256, 2, FMT>(p, gt, st);
+  if (n <= 768) return launch_fwd_g<256, 3, FMT>(p, gt, st);
+  if (n <= 1024) return launch_fwd_g<256, 4, FMT>(p, gt, st);
+  return launch_fwd_g<256, 8, FMT>(p, gt, st);
 }
 
 static_assert(kNormMaxCols == 256 * 8 * 8, "256 threads hold eight chunks of eight columns each");
