@@ -10,15 +10,20 @@
 
 namespace fp8moe {
 
+// (bound_ctrl set: no lane reads outside its row here, and the compiler then folds the exchange into the operation.)
+template <int CTL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTL, 0xF, 0xF, true);
+}
 template <int CTL>
 __device__ __forceinline__ float dpp_f32(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTL, 0xF, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTL, 0xF, 0xF, true));
 }
 template <int CTL>
 __device__ __forceinline__ double dpp_f64(double v) {
   const int64_t b = __double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTL, 0xF, 0xF, false);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTL, 0xF, 0xF, true);
   return __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
 }
 
@@ -38,6 +43,26 @@ __device__ __forceinline__ float group_reduce_f32(float v, Op op) {
       v = op(__uint_as_float(a[0]), __uint_as_float(a[1]));
       const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
       v = op(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    }
+    return v;
+  }
+}
+template <int N>
+__device__ __forceinline__ uint32_t group_most_u32(uint32_t v) {
+  static_assert(N == 4 || N == 16 || N == 64, "group size");
+  if constexpr (N == 4) {
+    v = max(v, dpp_u32<0xB1>(v));
+    return max(v, dpp_u32<0x4E>(v));
+  } else {
+    v = max(v, dpp_u32<0x128>(v));
+    v = max(v, dpp_u32<0x124>(v));
+    v = max(v, dpp_u32<0x122>(v));
+    v = max(v, dpp_u32<0x121>(v));
+    if constexpr (N == 64) {
+      const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      v = max(a[0], a[1]);
+      const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+      v = max(b[0], b[1]);
     }
     return v;
   }

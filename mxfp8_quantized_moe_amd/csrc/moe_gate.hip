@@ -194,26 +194,28 @@ __device__ __forceinline__ bool lowest_lane(bool is, int lane) {
   }
 }
 
-// The list without its head where `take`: of a sorted list only the first topk keys can be chosen.
-template <typename T, int N>
-__device__ __forceinline__ void move_up(T (&k)[N], bool take, int topk) {
-  auto shift = [&](auto last_tag) {
-    constexpr int LAST = decltype(last_tag)::value;
+// The list without its head where `take`: of a sorted list only the first KEEP keys are needed.
+template <int KEEP, typename T, int N>
+__device__ __forceinline__ void move_up(T (&k)[N], bool take) {
 #pragma unroll
-    for (int v = 0; v < LAST; ++v) {
-      const T here = k[v], next = k[v + 1];
-      k[v] = take ? next : here;
-    }
-    const T here = k[LAST];
-    k[LAST] = take ? T(0) : here;
-  };
+  for (int v = 0; v < KEEP - 1; ++v) {
+    const T here = k[v], next = k[v + 1];
+    k[v] = take ? next : here;
+  }
+  const T here = k[KEEP - 1];
+  k[KEEP - 1] = take ? T(0) : here;
+}
+
+// f(KEEP) with the keys a lane can lose to topk choices (the loop over the choices is picked once, not each step of it).
+template <int N, typename F>
+__device__ __forceinline__ void with_keep(int topk, F&& f) {
   if constexpr (N > 8) {
     if (topk <= 8) {
-      shift(std::integral_constant<int, 7>{});
+      f(std::integral_constant<int, 8>{});
       return;
     }
   }
-  shift(std::integral_constant<int, N - 1>{});
+  f(std::integral_constant<int, N>{});
 }
 
 // The second round for one token (row, wave-uniform), by a whole wave: chosen[r] of lane l is slot
@@ -246,16 +248,18 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
     }
   }
   sort_desc(key);
+  with_keep<VPL>(topk, [&](auto keep) {
 #pragma unroll
-  for (int r = 0; r < KR; ++r) {
-    chosen[r] = -1;
-    for (int j = 0; j < LPT; ++j) {
-      if (r * LPT + j >= topk) break;   // uniform
-      const double best = group_max_f64<64>(key[0]);
-      if (lane % LPT == j) chosen[r] = best >= kLeastKey ? gate_index(best) : -1;
-      move_up(key, key[0] == best, topk);
+    for (int r = 0; r < KR; ++r) {
+      chosen[r] = -1;
+      for (int j = 0; j < LPT; ++j) {
+        if (r * LPT + j >= topk) break;   // uniform
+        const double best = group_max_f64<64>(key[0]);
+        if (lane % LPT == j) chosen[r] = best >= kLeastKey ? gate_index(best) : -1;
+        move_up<decltype(keep)::value>(key, key[0] == best);
+      }
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------- work units
@@ -359,15 +363,17 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
         sort_desc(key);
         const uint32_t ninth = key[VPL > 8 ? 8 : 0];
         int* const slot = s_slot + (wave * TPW + g) * SLOTS;
-        for (int j = 0; j < p.topk; ++j) {
-          // the two lowest bits are the place in a chunk: lanes whose heads agree above them hold neighbouring experts
-          const uint32_t head = key[0] & ~3u;
-          const uint32_t best = group_max_u32<LPT>(head);
-          const bool mine = lowest_lane<LPT>(head == best, lane);
-          if (mine) slot[j] = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
-          move_up(key, mine, p.topk);
-        }
-        const uint32_t left = group_max_u32<LPT>(key[0] & ~3u);
+        with_keep<VPL>(p.topk, [&](auto keep) {
+          for (int j = 0; j < p.topk; ++j) {
+            // the two lowest bits are the place in a chunk: lanes whose heads agree above them hold the same chunk
+            const uint32_t head = key[0] & ~3u;
+            const uint32_t best = group_most_u32<LPT>(head);
+            const bool mine = lowest_lane<LPT>(head == best, lane);
+            if (mine) slot[j] = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
+            move_up<decltype(keep)::value>(key, mine);
+          }
+        });
+        const uint32_t left = group_most_u32<LPT>(key[0] & ~3u);
         wave_lds_fence();
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
@@ -377,7 +383,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           my_id[r] = raw >= 0 ? 4 * ((raw >> 4) + LPT * (v >> 2)) + (v & 3) : -1;
         }
         wave_lds_fence();
-        // move_up keeps eight of a lane's keys for topk 8: one that gave all eight away and had a ninth cannot
+        // with_keep keeps eight of a lane's keys for topk 8: one that gave all eight away and had a ninth cannot
         // tell what is left
         if constexpr (VPL > 8) close = p.topk == 8 && key[0] == 0u && ninth >= kLeast32;
         // Error of an fp32 key with a bias, u = 2^-24: a sigmoid is within 5 u (its exponential's relative error
