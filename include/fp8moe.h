@@ -728,7 +728,8 @@ int rmsnorm_quantize_mx(const void *x_bf16, const void *residual_bf16, const voi
  *           zeros without rows), or NULL: not computed
  *   workspace  device memory of rmsnorm_backward_workspace_bytes(rows, cols) bytes,
  *           16-byte aligned, owned by the caller (not needed without dgamma);
- *           contents on entry do not matter
+ *           contents on entry do not matter.  Calls that may overlap (other streams,
+ *           graphs replayed side by side) need one each
  *   Requires: cols as in the forward; bf16 and gamma pointers 16-byte aligned.  Two
  *   kernels (one without dgamma), no allocation.
  */
@@ -788,9 +789,10 @@ int moe_gate(const void *logits, int logit_dtype, int64_t tokens, int32_t n_expe
  *   dprob     f32 [n_seqs][n_experts]  the loss's derivative by one token's normalised score
  *             of expert i: coef / n_seqs * f / n[s], what moe_gate_backward takes (written)
  *   workspace device memory of moe_balance_workspace_bytes(...) bytes, 16-byte aligned,
- *             owned by the caller; contents on entry do not matter
- *   Sums over tokens are fp32 over at most 128 tokens, then in 64 bits, all in a fixed
- *   order.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), 1 <= n_seqs <= 65535.
+ *             owned by the caller; contents on entry do not matter.  Calls that may overlap
+ *             (other streams, graphs replayed side by side) need one each
+ *   Sums over tokens are fp32 over at most 128 tokens (up to 2^27 tokens in all), then in
+ *   64 bits; no result depends on the order of arrival.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), 1 <= n_seqs <= 65535.
  *   Two kernels, no allocation.
  */
 int moe_balance_loss(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,

@@ -782,6 +782,10 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       }
       wave_lds_fence();
     }
+    if (!on) {   // whatever the loss's gradient holds
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) ds[v] = 0.0f;
+    }
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] *= s[v] * (1.0f - s[v]);
@@ -863,7 +867,7 @@ hipError_t launch_moe_gate(const GateArgs& a, hipStream_t st) {
   p.E = a.E;
   p.topk = a.topk;
   p.renorm = a.renorm;
-  p.chunk = bal ? gate_chunk(a.tokens, a.E) : gate_step(a.E);
+  p.chunk = bal ? gate_chunk(a.tokens, a.E) : gate_tile(a.tokens, a.E);
   p.S = a.S;
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && ptr_aligned(a.logits, a.bf16 ? 8 : 16) && ptr_aligned(a.bias, 16);
   p.bias = a.bias;

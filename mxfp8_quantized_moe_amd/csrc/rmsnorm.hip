@@ -59,6 +59,7 @@ struct NormFwd {
   const uint16_t* res;    // or null
   const void* gamma;      // or null
   int64_t rows, ld_x, ld_r;
+  int64_t row0;           // first row of this launch
   int nchunk;             // cols / 8
   float inv_c, eps;
   uint16_t* sum;          // [rows][cols], written with a residual
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
   __shared__ float red_s[TPR > 64 ? WAVES : 1];
   __shared__ uint32_t red_m[TPR > 64 ? WAVES : 1];
   const int lt = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int64_t row = p.row0 + (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool valid = row < p.rows;
   const int64_t r = valid ? row : 0;
   const int64_t cols = (int64_t)p.nchunk * 8;
@@ -227,10 +228,14 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
   }
 }
 
+// Rows of one launch: 2^23 workgroups of 256 threads stay within the 32 bits of a grid's thread count.
+constexpr int64_t kNormLaunchRows = 1 << 23;
+
 template <int TPR, int ITEMS, int FMT>
 static hipError_t launch_fwd_g(const NormFwd& p, int gt, hipStream_t st) {
   constexpr int NT = TPR > 256 ? TPR : 256, RPB = NT / TPR;
-  const dim3 grid((unsigned)((p.rows + RPB - 1) / RPB)), block(NT);
+  const int64_t rows = p.rows - p.row0 < kNormLaunchRows ? p.rows - p.row0 : kNormLaunchRows;
+  const dim3 grid((unsigned)((rows + RPB - 1) / RPB)), block(NT);
   if (gt == 0) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 0>), grid, block, 0, st, p);
   else if (gt == 1) hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 1>), grid, block, 0, st, p);
   else hipLaunchKernelGGL((rmsnorm_kernel<TPR, ITEMS, FMT, 2>), grid, block, 0, st, p);
@@ -279,13 +284,18 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
   p.rstd = a.rstd;
   p.layout = a.layout;
   const int gt = a.gamma == nullptr ? 0 : (a.gamma_bf16 ? 2 : 1);
-  switch (a.fmt) {
-    case 0: return launch_fwd<0>(p, gt, st);
-    case 1: return launch_fwd<1>(p, gt, st);
-    case 2: return launch_fwd<2>(p, gt, st);
-    case 3: return launch_fwd<3>(p, gt, st);
-    default: return launch_fwd<4>(p, gt, st);
+  for (p.row0 = 0; p.row0 < a.rows; p.row0 += kNormLaunchRows) {
+    hipError_t e;
+    switch (a.fmt) {
+      case 0: e = launch_fwd<0>(p, gt, st); break;
+      case 1: e = launch_fwd<1>(p, gt, st); break;
+      case 2: e = launch_fwd<2>(p, gt, st); break;
+      case 3: e = launch_fwd<3>(p, gt, st); break;
+      default: e = launch_fwd<4>(p, gt, st); break;
+    }
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------------------- backward

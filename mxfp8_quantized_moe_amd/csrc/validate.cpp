@@ -474,8 +474,15 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
 
 int gate_step(int32_t E) { return E <= 16 ? 64 : E <= 256 ? 16 : 4; }
 
-int gate_chunk(int64_t tokens, int32_t E) {
+// Never more than 2^20 workgroups (and their threads within 32 bits).
+int gate_tile(int64_t tokens, int32_t E) {
   int c = gate_step(E);
+  while (tokens / c > 1 << 20) c *= 2;
+  return c;
+}
+
+int gate_chunk(int64_t tokens, int32_t E) {
+  int c = gate_tile(tokens, E);
   while (c < 128 && tokens / c > 1024) c *= 2;
   return c;
 }

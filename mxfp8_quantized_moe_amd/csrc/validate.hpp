@@ -103,12 +103,14 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
                            const void* dsum, int64_t rows, int64_t cols, const void* dx, const void* dgamma,
                            const void* workspace);
 
-// Router gate and balance loss.  A workgroup takes gate_step tokens at a time and, with the loss, a chunk of them
-// of one sequence: at most gate_units chunks (one more for each sequence and for the tokens behind the last one).
+// Router gate and balance loss.  A workgroup takes gate_step tokens at a time: gate_tile of them in all without the
+// loss and with it gate_chunk, of one sequence: at most gate_units chunks (one more for each sequence and for the
+// tokens behind the last one).
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxTopk = 64;
 constexpr int kGateMaxSeqs = 65535;   // a grid dimension of the loss kernel
 int gate_step(int32_t E);
+int gate_tile(int64_t tokens, int32_t E);
 int gate_chunk(int64_t tokens, int32_t E);
 int64_t gate_units(int64_t tokens, int32_t E, int32_t n_seqs);
 int64_t gate_workspace_bytes(int64_t tokens, int32_t E, int32_t n_seqs);

@@ -83,7 +83,8 @@ def check_loss(got, z, ids, coef, offs, sigmoid, mask, what):
 
 # tokens, experts, topk
 SHAPES = [(1, 1, 1), (1, 16, 1), (3, 2, 2), (5, 7, 7), (33, 16, 1), (64, 64, 6), (17, 63, 5), (129, 65, 8), (40, 128, 4),
-          (31, 200, 12), (50, 256, 8), (9, 257, 3), (21, 512, 10), (7, 777, 64), (12, 1024, 16), (700, 60, 4), (3000, 8, 2)]
+          (31, 200, 12), (50, 256, 8), (9, 257, 3), (21, 512, 10), (7, 777, 64), (12, 1024, 16), (700, 60, 4), (3000, 8, 2),
+          (9, 64, 64), (5, 200, 40), (6, 16, 16), (4, 300, 17)]
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
@@ -129,6 +130,33 @@ def test_bias_decides_in_64_bits():
         for sigmoid in (False, True):
             got = fm.moe_gate(dev(z), k, int(sigmoid), dev(bias))
             np.testing.assert_array_equal(host(got[0]), og.gate(z.astype(np.float64), k, sigmoid, bias)[0])
+
+
+def test_order_below_the_truncated_keys():
+    """Logits that differ in their last four bits only, and ties of them."""
+    note("moe_gate last bits")
+    rng = np.random.default_rng(15)
+    for E, k in ((16, 3), (64, 8), (256, 8), (200, 12), (1000, 20)):
+        z = (rng.choice([1.0, -1.0, 3.0], size=(200, 1)) * (1 + rng.integers(0, 16, size=(200, E)) * 2.0 ** -23)).astype(np.float32)
+        z[::3, E // 2:] = -5.0
+        got = fm.moe_gate(dev(z), k)
+        np.testing.assert_array_equal(host(got[0]), og.gate(z.astype(np.float64), k, False)[0])
+
+
+def test_one_lane_gives_all_choices():
+    """All of a row's largest logits in one lane (experts 4 l + 0..3 of each chunk of 64, of 256 beyond 256 experts): more
+    than eight, so that what the lane keeps runs out."""
+    note("moe_gate one lane")
+    rng = np.random.default_rng(16)
+    for E, step in ((256, 64), (1024, 256), (128, 64)):
+        mine = [e for e in range(E) if (e % step) // 4 == 5]
+        z = rng.standard_normal((40, E)).astype(np.float32)
+        z[:, mine] = 10 + rng.standard_normal((40, len(mine))).astype(np.float32)
+        z[::2, mine] = np.float32(10) + np.float32(2.0 ** -20) * rng.integers(0, 16, size=(20, len(mine)))
+        for bias in (None, np.zeros(E, np.float32)):
+            for k in (7, 8, 9, 16):
+                got = fm.moe_gate(dev(z), k, fm.GATE_SIGMOID, dev(bias))
+                np.testing.assert_array_equal(host(got[0]), og.gate(z.astype(np.float64), k, True, bias)[0])
 
 
 def test_infinite_bias():
@@ -222,6 +250,22 @@ def test_backward(case, sigmoid):
             assert np.all(np.abs(g - dz) <= tol), f"{what}: {np.max(np.abs(g - dz) - tol)}"
             if mask is not None:
                 assert np.all(g[~mask] == 0)
+
+
+def test_masked_tokens_stay_zero():
+    """An overflowed loss gradient and NaN weights' gradients do not reach masked or uncounted tokens."""
+    note("moe_gate_backward masked")
+    z = torch.randn(100, 24, device=DEV)
+    mask = torch.arange(100, device=DEV) % 3 != 0
+    ids, _, _, _, dprob = fm.moe_gate_balance(z, 4, 0.1, i32_dev([60]), token_mask=mask)
+    dw = torch.randn(100, 4, device=DEV)
+    dw[~mask] = float("nan")
+    for bad in (float("inf"), float("nan")):
+        for score in (0, 1):
+            dz = fm.moe_gate_backward(z, ids, dw, score, mask, dprob=dprob, dloss=torch.full((1,), bad, device=DEV),
+                                      seq_offs=i32_dev([60]))
+            assert torch.count_nonzero(dz[~mask]) == 0
+            assert torch.isfinite(dz[60:]).all()
 
 
 def test_single_renormalised_choice_passes_nothing():

@@ -126,6 +126,20 @@ def test_mx(R, C, rule):
     assert_bytes_equal(host(k4[2]), e8m0_rows_to_k4(code), "K4 scales")
 
 
+def test_more_rows_than_one_launch():
+    """2^23 + 5 rows take two launches: the rows around their border against a call on those rows alone."""
+    R, C = (1 << 23) + 5, 32
+    note("rmsnorm 2^23 + 5 rows")
+    x = torch.randn(R, C, device=DEV).to(torch.bfloat16)
+    h, q, sc, rs, _ = fm.rmsnorm_quantize_rowwise(x)
+    m = fm.rmsnorm_quantize_mx(x, layout=fm.MX_LAYOUT_K4, keep_bf16=False)
+    for part in (slice(0, 40), slice((1 << 23) - 20, R)):
+        a = fm.rmsnorm_quantize_rowwise(x[part])
+        assert all(torch.equal(u[part], v) for u, v in zip((h, q, sc, rs), a))
+        b = fm.rmsnorm_quantize_mx(x[part], layout=fm.MX_LAYOUT_K4)
+        assert torch.equal(m[1][part], b[1]) and torch.equal(m[2][:, part], b[2])
+
+
 def test_forms_agree_and_optional_outputs():
     """codes=False / keep_bf16=False change nothing else; the sum may be written over x or the residual."""
     rng = np.random.default_rng(3)
@@ -214,9 +228,10 @@ def test_backward(R, C):
     # without dgamma, and in place
     only, none = fm.rmsnorm_backward(dd, sd, rd, gd, dsum=None if ds is None else bf16_dev(ds_bits), want_dgamma=False)
     assert none is None and torch.equal(only, got)
-    place = dd.clone()
-    fm.rmsnorm_backward(place, sd, rd, gd, dsum=None if ds is None else bf16_dev(ds_bits), dx=place)
-    assert torch.equal(place, got)
+    for which in ("dh", "s", "dsum")[: 2 if ds is None else 3]:
+        a = dict(dh=dd.clone(), s=sd.clone(), dsum=None if ds is None else bf16_dev(ds_bits))
+        place, dg2 = fm.rmsnorm_backward(rstd=rd, gamma=gd, dx=a[which], **a)
+        assert place is a[which] and torch.equal(place, got) and torch.equal(dg2, gg)
 
 
 def test_backward_repeats_bit_for_bit():
