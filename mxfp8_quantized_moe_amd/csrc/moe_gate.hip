@@ -649,6 +649,10 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
 // ds of a chosen expert: route_scale dw, or with renormalisation
 // (route_scale dw - sum over slots of route_scale dw u) / (chosen scores' sum), u the
 // normalised weights; plus the loss's dloss * dprob on the normalised scores.
+// Renormalised softmax weights do not depend on the other experts: their part of dz,
+// u (route_scale dw - sum ...), is added to the chosen experts as it is, so that the
+// rounding of sum p ds, zero for it, does not reach the other experts' (the loss's)
+// gradients, which are often far smaller.
 // The slots' values reach the lanes that hold their experts through one LDS row a
 // token (the wave's own, so no barrier).
 
@@ -734,10 +738,9 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 #pragma unroll
         for (int r = 0; r < KR; ++r) mean += ws > 0.0f ? dw[r] * __fdiv_rn(w[r], ws) : 0.0f;
         mean = group_sum_f32<LPT>(mean);
-        // the softmax's denominator cancels between the chosen scores and their sum
-        const float f = ws > 0.0f ? __fdiv_rn(SIGMOID ? 1.0f : total, ws) : 0.0f;
+        const float f = ws > 0.0f ? __fdiv_rn(1.0f, ws) : 0.0f;
 #pragma unroll
-        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * f;
+        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * (SIGMOID ? f : w[r] * f);
       }
       // Slot values into the token's row.  Each slot first leaves its number at its expert: a slot that reads
       // another's shares its expert with it, and then the slots add up one after another, in their order.
@@ -772,6 +775,8 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
           }
       }
       wave_lds_fence();
+    }
+    auto add_slots = [&] {
 #pragma unroll
       for (int c = 0; c < VPL / 4; ++c) {
         const float4 d = *reinterpret_cast<const float4*>(mine + 4 * (l + LPT * c));
@@ -781,7 +786,9 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         ds[4 * c + 3] += d.w;
       }
       wave_lds_fence();
-    }
+    };
+    const bool direct = !SIGMOID && p.renorm;   // the slots hold their part of dz, not of ds
+    if (p.dweights != nullptr && !direct) add_slots();
     if (!on) {   // whatever the loss's gradient holds
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = 0.0f;
@@ -799,6 +806,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       dot = group_sum_f32<LPT>(dot);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
+      if (p.dweights != nullptr && direct) add_slots();
     }
     if (live) {
       const int64_t out = (int64_t)t * p.E;
