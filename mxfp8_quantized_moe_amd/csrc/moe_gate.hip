@@ -11,10 +11,12 @@
 // A logit that is NaN or -inf makes its expert ineligible for the token; +inf
 // counts as the largest finite value.
 //
-// Layout: LPT lanes (4, 16 or 64) share a token, so a wave takes up to 16 tokens;
-// lane l of the group holds VPL logits in chunks of four, experts
-// 4 (l + LPT c) + 0..3, which are 16-byte loads and stores.  Sums and maxima over a
-// token then take 2, 4 or 6 VALU lane steps, shared by the wave's tokens.
+// Layout: LPT lanes (4, 16 or 64) share a token, so a wave takes up to 16 tokens.
+// Lane l of the group holds VPL logits: where rows are aligned (VEC), in chunks of
+// four, experts 4 (l + LPT c) + 0..3, which are 16-byte loads and stores; else
+// experts l + LPT v, so that the lanes of each 4-byte access are neighbours.  Sums
+// and maxima over a token then take 2, 4 or 6 VALU lane steps, shared by the wave's
+// tokens.
 //
 // Selection, first round: a key is an fp32 value (the logit, or score + bias) made
 // sortable as an unsigned integer, its low four bits replaced by the complement of
@@ -58,6 +60,12 @@ __device__ __forceinline__ float gate_logit(const void* __restrict__ logits, int
   else return gate_clean(static_cast<const float*>(logits)[at]);
 }
 
+// The expert of the lane's value v.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int expert_at(int l, int v) {
+  return VEC ? 4 * (l + LPT * (v >> 2)) + (v & 3) : l + LPT * v;
+}
+
 // The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  VEC: E and the row
 // stride are multiples of four and every array of experts starts aligned, so a chunk is one load.
 template <int LPT, int VPL, bool BF16, bool VEC>
@@ -82,7 +90,7 @@ __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64
     const int n = on ? E : 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int e = 4 * (l + LPT * (v / 4)) + v % 4;
+      const int e = expert_at<LPT, VEC>(l, v);
       z[v] = -INFINITY;
       if (e < n) {
         if constexpr (BF16) z[v] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[row + e] << 16);
@@ -107,7 +115,7 @@ __device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E
   } else {
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int e = 4 * (l + LPT * (v / 4)) + v % 4;
+      const int e = expert_at<LPT, VEC>(l, v);
       out[v] = e < E ? x[e] : 0.0f;
     }
   }
@@ -229,7 +237,7 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
   gate_load<64, VPL, BF16, VEC>(logits, row, E, lane, true, z);
   if (bias == nullptr) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], 4 * (lane + 64 * (v / 4)) + v % 4);
+    for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], expert_at<64, VEC>(lane, v));
   } else {
     float b[VPL];
     gate_load_vec<64, VPL, VEC>(bias, E, lane, b);
@@ -243,7 +251,7 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const double k = (SIGMOID ? key[v] : key[v] / total) + (double)b[v];
-      const double packed = gate_key64(k, 4 * (lane + 64 * (v / 4)) + v % 4);
+      const double packed = gate_key64(k, expert_at<64, VEC>(lane, v));
       key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
     }
   }
@@ -306,6 +314,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   constexpr int TPW = 64 / LPT;                  // tokens a wave takes at a time
   constexpr int KR = LPT == 64 ? 1 : 4;          // slots a lane holds: topk <= min(64, LPT * VPL) <= KR * LPT
   constexpr int W = LPT * VPL;
+  // Places that different lanes' experts of equal value are ordered by, before the lane: all of them, or (a lane's four
+  // in a chunk come before the next lane's) the chunks.
+  constexpr uint32_t kCompare = VEC ? ~3u : ~0u;
   constexpr int SLOTS = W < kGateMaxTopk ? W : kGateMaxTopk;
   __shared__ int s_slot[GATE ? 256 / LPT * SLOTS : 1];   // the choices' lanes and places, a row a token
   __shared__ int s_cnt[BAL ? W : 1];
@@ -365,22 +376,20 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
         int* const slot = s_slot + (wave * TPW + g) * SLOTS;
         with_keep<VPL>(p.topk, [&](auto keep) {
           for (int j = 0; j < p.topk; ++j) {
-            // the two lowest bits are the place in a chunk: lanes whose heads agree above them hold the same chunk
-            const uint32_t head = key[0] & ~3u;
+            const uint32_t head = key[0] & kCompare;
             const uint32_t best = group_most_u32<LPT>(head);
             const bool mine = lowest_lane<LPT>(head == best, lane);
             if (mine) slot[j] = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
             move_up<decltype(keep)::value>(key, mine);
           }
         });
-        const uint32_t left = group_most_u32<LPT>(key[0] & ~3u);
+        const uint32_t left = group_most_u32<LPT>(key[0] & kCompare);
         wave_lds_fence();
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
           if (r * LPT >= p.topk) break;   // uniform
           const int raw = r * LPT + l < p.topk ? slot[r * LPT + l] : -1;
-          const int v = 15 - (raw & 15);
-          my_id[r] = raw >= 0 ? 4 * ((raw >> 4) + LPT * (v >> 2)) + (v & 3) : -1;
+          my_id[r] = raw >= 0 ? expert_at<LPT, VEC>(raw >> 4, 15 - (raw & 15)) : -1;
         }
         wave_lds_fence();
         // with_keep keeps eight of a lane's keys for topk 8: one that gave all eight away and had a ninth cannot
@@ -473,9 +482,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   if constexpr (BAL) {
     constexpr int NG = 256 / LPT;   // token groups of the workgroup, each with its share of the sums
 #pragma unroll
-    for (int c = 0; c < VPL / 4; ++c)
-      *reinterpret_cast<float4*>(&s_sum[(wave * TPW + g) * W + 4 * (l + LPT * c)]) =
-          float4{acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]};
+    for (int v = 0; v < VPL; ++v) s_sum[(wave * TPW + g) * W + expert_at<LPT, VEC>(l, v)] = acc[v];
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
     if (lane == 0) s_n[wave] = n;
@@ -745,8 +752,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       // Slot values into the token's row.  Each slot first leaves its number at its expert: a slot that reads
       // another's shares its expert with it, and then the slots add up one after another, in their order.
 #pragma unroll
-      for (int c = 0; c < VPL / 4; ++c)
-        *reinterpret_cast<float4*>(mine + 4 * (l + LPT * c)) = float4{0.f, 0.f, 0.f, 0.f};
+      for (int v = 0; v < VPL; ++v) mine[expert_at<LPT, VEC>(l, v)] = 0.0f;
       wave_lds_fence();
 #pragma unroll
       for (int r = 0; r < KR; ++r)
@@ -778,13 +784,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     }
     auto add_slots = [&] {
 #pragma unroll
-      for (int c = 0; c < VPL / 4; ++c) {
-        const float4 d = *reinterpret_cast<const float4*>(mine + 4 * (l + LPT * c));
-        ds[4 * c] += d.x;
-        ds[4 * c + 1] += d.y;
-        ds[4 * c + 2] += d.z;
-        ds[4 * c + 3] += d.w;
-      }
+      for (int v = 0; v < VPL; ++v) ds[v] += mine[expert_at<LPT, VEC>(l, v)];
       wave_lds_fence();
     };
     const bool direct = !SIGMOID && p.renorm;   // the slots hold their part of dz, not of ds
@@ -810,32 +810,27 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     }
     if (live) {
       const int64_t out = (int64_t)t * p.E;
+      if constexpr (VEC) {
 #pragma unroll
-      for (int c = 0; c < VPL / 4; ++c) {
-        const int e0 = 4 * (l + LPT * c);
-        if constexpr (BF16) {
-          __bf16* const o = static_cast<__bf16*>(p.dlogits) + out + e0;
-          if constexpr (VEC) {
-            if (e0 < p.E)
-              *reinterpret_cast<u32x2*>(o) =
-                  u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(gt_f32x2{ds[4 * c], ds[4 * c + 1]}, gt_bf16x2)),
-                        __builtin_bit_cast(uint32_t,
-                                           __builtin_convertvector(gt_f32x2{ds[4 * c + 2], ds[4 * c + 3]}, gt_bf16x2))};
-          } else {
+        for (int c = 0; c < VPL / 4; ++c) {
+          const int e0 = 4 * (l + LPT * c);
+          if (e0 >= p.E) continue;
+          if constexpr (BF16)
+            *reinterpret_cast<u32x2*>(static_cast<__bf16*>(p.dlogits) + out + e0) =
+                u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(gt_f32x2{ds[4 * c], ds[4 * c + 1]}, gt_bf16x2)),
+                      __builtin_bit_cast(uint32_t,
+                                         __builtin_convertvector(gt_f32x2{ds[4 * c + 2], ds[4 * c + 3]}, gt_bf16x2))};
+          else
+            *reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + out + e0) =
+                float4{ds[4 * c], ds[4 * c + 1], ds[4 * c + 2], ds[4 * c + 3]};
+        }
+      } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (e0 + r < p.E) o[r] = (__bf16)ds[4 * c + r];
-          }
-        } else {
-          float* const o = static_cast<float*>(p.dlogits) + out + e0;
-          if constexpr (VEC) {
-            if (e0 < p.E)
-              *reinterpret_cast<float4*>(o) = float4{ds[4 * c], ds[4 * c + 1], ds[4 * c + 2], ds[4 * c + 3]};
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (e0 + r < p.E) o[r] = ds[4 * c + r];
-          }
+        for (int v = 0; v < VPL; ++v) {
+          const int e = expert_at<LPT, VEC>(l, v);
+          if (e >= p.E) continue;
+          if constexpr (BF16) static_cast<__bf16*>(p.dlogits)[out + e] = (__bf16)ds[v];
+          else static_cast<float*>(p.dlogits)[out + e] = ds[v];
         }
       }
     }
