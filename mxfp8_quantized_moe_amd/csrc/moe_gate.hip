@@ -51,8 +51,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // ---------------------------------------------------------------- logits
 
-// NaN as -inf, at most the largest finite value.
-__device__ __forceinline__ float gate_clean(float v) { return v > -INFINITY ? fminf(v, kFltMax) : -INFINITY; }
+// NaN as -inf (the maximum of a NaN and a number is the number), at most the largest finite value.
+__device__ __forceinline__ float gate_clean(float v) { return fminf(fmaxf(v, -INFINITY), kFltMax); }
 
 template <bool BF16>
 __device__ __forceinline__ float gate_logit(const void* __restrict__ logits, int64_t at) {
@@ -98,6 +98,9 @@ __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64
       }
     }
   }
+  // All loads have left before the first is cleaned (the compiler would clean each in its own branch, one wait a load).
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) asm volatile("" : "+v"(z[v]));
 #pragma unroll
   for (int v = 0; v < VPL; ++v) z[v] = gate_clean(z[v]);
 }

@@ -159,6 +159,26 @@ def test_one_lane_gives_all_choices():
                 np.testing.assert_array_equal(host(got[0]), og.gate(z.astype(np.float64), k, True, bias)[0])
 
 
+def test_nan_patterns():
+    """Quiet and signalling NaN of either sign, and -inf, are no expert; +inf comes first."""
+    note("moe_gate NaN patterns")
+    z = np.random.default_rng(17).standard_normal((8, 32)).astype(np.float32)
+    bits = z.view(np.uint32).copy()
+    for e, b in ((0, 0x7FC00000), (3, 0x7F800001), (9, 0xFFC00000), (17, 0xFF800001), (30, 0x7FFFFFFF), (31, 0xFF800000)):
+        bits[:, e] = b
+    bits[4:, 12] = 0x7F800000
+    zd, z = torch.from_numpy(bits.view(np.int32)).to(DEV).view(torch.float32), bits.view(np.float32)
+    half = torch.from_numpy((bits >> 16).astype(np.uint16).view(np.int16)).to(DEV).view(torch.bfloat16)
+    zh = ((bits >> 16) << 16).view(np.float32)   # 0x7F800001 is +inf and 0xFF800001 -inf in bf16; 0x7FFF is a NaN
+    for t, v in ((zd, z), (half, zh)):
+        for sigmoid in (False, True):
+            for bias in (None, np.full(32, 0.25, np.float32)):
+                ids, w = fm.moe_gate(t, 32, int(sigmoid), dev(bias))
+                want, ww = og.gate(v.astype(np.float64), 32, sigmoid, bias)
+                np.testing.assert_array_equal(host(ids), want)
+                assert np.all(np.abs(host(w) - ww) <= 1e-5 * ww + 4 * TINY)
+
+
 def test_infinite_bias():
     note("moe_gate infinite bias")
     z = np.random.default_rng(6).standard_normal((9, 12)).astype(np.float32)
