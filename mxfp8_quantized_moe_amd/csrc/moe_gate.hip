@@ -229,11 +229,11 @@ __device__ __forceinline__ void with_keep(int topk, F&& f) {
   f(std::integral_constant<int, N>{});
 }
 
-// The second round for one token (row, wave-uniform), by a whole wave: chosen[r] of lane l is slot
-// r LPT + l % LPT.  m: the row's largest logit (softmax).
-template <int VPL, int LPT, int KR, bool BF16, bool SIGMOID, bool VEC>
+// The second round for one token (row, wave-uniform), by a whole wave: its choices go to slot[0 .. topk).
+// m: the row's largest logit (softmax).
+template <int VPL, bool BF16, bool SIGMOID, bool VEC>
 __device__ __forceinline__ void select_exact(const void* __restrict__ logits, int64_t row, int E,
-                                             const float* __restrict__ bias, float m, int topk, int (&chosen)[KR]) {
+                                             const float* __restrict__ bias, float m, int topk, int* slot) {
   const int lane = threadIdx.x & 63;
   float z[VPL];
   double key[VPL];
@@ -260,15 +260,10 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
   }
   sort_desc(key);
   with_keep<VPL>(topk, [&](auto keep) {
-#pragma unroll
-    for (int r = 0; r < KR; ++r) {
-      chosen[r] = -1;
-      for (int j = 0; j < LPT; ++j) {
-        if (r * LPT + j >= topk) break;   // uniform
-        const double best = group_max_f64<64>(key[0]);
-        if (lane % LPT == j) chosen[r] = best >= kLeastKey ? gate_index(best) : -1;
-        move_up<decltype(keep)::value>(key, key[0] == best);
-      }
+    for (int j = 0; j < topk; ++j) {
+      const double best = group_max_f64<64>(key[0]);
+      if (lane == 0) slot[j] = best >= kLeastKey ? gate_index(best) : -1;
+      move_up<decltype(keep)::value>(key, key[0] == best);
     }
   });
 }
@@ -315,13 +310,15 @@ struct GateFwd {
 template <int LPT, int VPL, bool BF16, bool VEC, bool SIGMOID, bool GATE, bool BAL>
 __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
   constexpr int TPW = 64 / LPT;                  // tokens a wave takes at a time
-  constexpr int KR = LPT == 64 ? 1 : 4;          // slots a lane holds: topk <= min(64, LPT * VPL) <= KR * LPT
   constexpr int W = LPT * VPL;
   // Places that different lanes' experts of equal value are ordered by, before the lane: all of them, or (a lane's four
   // in a chunk come before the next lane's) the chunks.
   constexpr uint32_t kCompare = VEC ? ~3u : ~0u;
   constexpr int SLOTS = W < kGateMaxTopk ? W : kGateMaxTopk;
-  __shared__ int s_slot[GATE ? 256 / LPT * SLOTS : 1];   // the choices' lanes and places, a row a token
+  // A token's choices: lane and place, then the expert; its logit's bits, then its score's.  (A wave's rows hold at least
+  // 64 of each.)
+  __shared__ int s_slot[GATE ? 256 / LPT * SLOTS : 1];
+  __shared__ int s_val[GATE ? 256 / LPT * SLOTS : 1];
   __shared__ int s_cnt[BAL ? W : 1];
   __shared__ __attribute__((aligned(16))) float s_sum[BAL ? 256 * VPL : 1];
   __shared__ int s_n[4];
@@ -352,14 +349,11 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
     gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);
     const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 
-    int my_id[KR];   // slot r * LPT + l
-#pragma unroll
-    for (int r = 0; r < KR; ++r) my_id[r] = -1;
     if constexpr (GATE) {
       const bool biased = p.bias != nullptr;
-      const int last_r = (p.topk - 1) / LPT, last_l = (p.topk - 1) % LPT;
+      int* const slot = s_slot + (wave * TPW + g) * SLOTS;
+      int* const val = s_val + (wave * TPW + g) * SLOTS;
       bool close = false;
-      float chosen_z[KR];   // the chosen logits
       {
         uint32_t key[VPL];
         if (!biased) {
@@ -376,111 +370,102 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
         }
         sort_desc(key);
         const uint32_t ninth = key[VPL > 8 ? 8 : 0];
-        int* const slot = s_slot + (wave * TPW + g) * SLOTS;
+        // The lane that owns a choice writes it; the others write beside it (a place of their own among the wave's
+        // values, which are not in use yet): without a branch the lists move by selects.
+        int* const aside = s_val + wave * TPW * SLOTS + lane;
         with_keep<VPL>(p.topk, [&](auto keep) {
           for (int j = 0; j < p.topk; ++j) {
             const uint32_t head = key[0] & kCompare;
             const uint32_t best = group_most_u32<LPT>(head);
             const bool mine = lowest_lane<LPT>(head == best, lane);
-            if (mine) slot[j] = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
+            *(mine ? slot + j : aside) = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
             move_up<decltype(keep)::value>(key, mine);
           }
         });
         const uint32_t left = group_most_u32<LPT>(key[0] & kCompare);
-        wave_lds_fence();
-#pragma unroll
-        for (int r = 0; r < KR; ++r) {
-          if (r * LPT >= p.topk) break;   // uniform
-          const int raw = r * LPT + l < p.topk ? slot[r * LPT + l] : -1;
-          my_id[r] = raw >= 0 ? expert_at<LPT, VEC>(raw >> 4, 15 - (raw & 15)) : -1;
-        }
-        wave_lds_fence();
         // with_keep keeps eight of a lane's keys for topk 8: one that gave all eight away and had a ninth cannot
         // tell what is left
         if constexpr (VPL > 8) close = p.topk == 8 && key[0] == 0u && ninth >= kLeast32;
+        wave_lds_fence();
         // Error of an fp32 key with a bias, u = 2^-24: a sigmoid is within 5 u (its exponential's relative error
         // |z| 3 u + 2 u enters times s (1 - s) <= min(1/4, e^-|z|)), a softmax score within 55 u (exponent
         // e^-x (3 x + 2) u, the sum's error up to 50 u), the sum with the bias rounds by u |key|.  Two keys can
         // swap below twice that.  A key without its low four bits is lower by less than 2^-19 of its value.
         const float tol = SIGMOID ? 0x1p-20f : 0x1p-17f;
-        float before = 0.0f;   // slot r LPT - 1
+        float before = 0.0f;   // slot j0 - 1
         int before_id = -1;
-#pragma unroll
-        for (int r = 0; r < KR; ++r) {
-          if (r * LPT >= p.topk) break;   // uniform
+        for (int j0 = 0; j0 < p.topk; j0 += LPT) {
+          const int j = j0 + l;
+          const int raw = j < p.topk ? slot[j] : -1;
+          const int id = raw >= 0 ? expert_at<LPT, VEC>(raw >> 4, 15 - (raw & 15)) : -1;
           float x = -INFINITY;
-          if (my_id[r] >= 0) {
-            chosen_z[r] = x = gate_logit<BF16>(p.logits, row + my_id[r]);
-            if (biased) x = gate_clean((SIGMOID ? sigmoid_f32(x) : __expf(x - m) * inv) + p.bias[my_id[r]]);
+          if (id >= 0) {
+            x = gate_logit<BF16>(p.logits, row + id);
+            slot[j] = id;
+            val[j] = __float_as_int(x);
+            if (biased) x = gate_clean((SIGMOID ? sigmoid_f32(x) : __expf(x - m) * inv) + p.bias[id]);
           }
           const float xp = __shfl_up(x, 1, LPT);
-          const int ip = __shfl_up(my_id[r], 1, LPT);
+          const int ip = __shfl_up(id, 1, LPT);
           const float xb = l > 0 ? xp : before;
           const int ib = l > 0 ? ip : before_id;
-          if (ib >= 0 && my_id[r] >= 0)
-            close = close || (biased ? xb - x <= tol * (1.0f + fabsf(x)) : !(xb > x || (xb == x && ib < my_id[r])));
-          if (r == last_r && l == last_l && left >= kLeast32) {
+          if (ib >= 0 && id >= 0)
+            close = close || (biased ? xb - x <= tol * (1.0f + fabsf(x)) : !(xb > x || (xb == x && ib < id)));
+          if (j == p.topk - 1 && left >= kLeast32) {
             const float y = sorted_value(left & ~15u);
             close = close || (biased ? x - y <= tol * (1.0f + fabsf(y)) + 0x1p-18f * fabsf(y)
                                      : !BF16 && ((sortable(x) ^ left) & ~15u) == 0);
           }
-          if (r + 1 < KR) {
-            before = __shfl(x, LPT - 1, LPT);
-            before_id = __shfl(my_id[r], LPT - 1, LPT);
-          }
+          before = __shfl(x, LPT - 1, LPT);
+          before_id = __shfl(id, LPT - 1, LPT);
         }
       }
       // Second round: the whole wave takes one token after another of those that need it, so its wide keys
       // occupy few registers beside the first round's.
-      const bool again = __ballot(close) != 0;
       for (uint64_t todo = __ballot(close); todo != 0;) {
         const int gc = (__ffsll((unsigned long long)todo) - 1) / LPT;   // wave-uniform
         todo &= ~(LPT == 64 ? ~0ull : ((1ull << (LPT & 63)) - 1) << (gc * (LPT & 63)));
-        int chosen[KR];
-        select_exact<W <= 256 ? 4 : VPL, LPT, KR, BF16, SIGMOID, VEC>(p.logits, (int64_t)(base + gc) * p.ld, p.E, p.bias,
-                                                                     __shfl(m, gc * LPT, 64), p.topk, chosen);
-#pragma unroll
-        for (int r = 0; r < KR; ++r) my_id[r] = g == gc ? chosen[r] : my_id[r];
+        select_exact<W <= 256 ? 4 : VPL, BF16, SIGMOID, VEC>(p.logits, (int64_t)(base + gc) * p.ld, p.E, p.bias,
+                                                             __shfl(m, gc * LPT, 64), p.topk,
+                                                             s_slot + (wave * TPW + gc) * SLOTS);
+        wave_lds_fence();
+        if (g == gc)
+          for (int j = l; j < p.topk; j += LPT)
+            if (slot[j] >= 0) val[j] = __float_as_int(gate_logit<BF16>(p.logits, row + slot[j]));
       }
-      float w[KR], ws = 0.0f;
-#pragma unroll
-      for (int r = 0; r < KR; ++r) {
-        if (r * LPT >= p.topk) break;   // uniform
-        w[r] = 0.0f;
-        if (my_id[r] >= 0) {
-          if (again) chosen_z[r] = gate_logit<BF16>(p.logits, row + my_id[r]);
-          w[r] = SIGMOID ? sigmoid_f32(chosen_z[r]) : __expf(chosen_z[r] - m);
-        }
-        ws += w[r];
+      wave_lds_fence();
+      float ws = 0.0f;
+      for (int j = l; j < p.topk; j += LPT) {
+        const float zj = __int_as_float(val[j]);
+        const float w = slot[j] < 0 ? 0.0f : SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+        val[j] = __float_as_int(w);
+        ws += w;
       }
       if (p.renorm) ws = group_sum_f32<LPT>(ws);
-#pragma unroll
-      for (int r = 0; r < KR; ++r) {
-        if (r * LPT >= p.topk) break;   // uniform
-        const int j = r * LPT + l;
-        if (live && j < p.topk) {
-          if (p.renorm) w[r] = ws > 0.0f ? __fdiv_rn(w[r], ws) : 0.0f;   // exactly 1 for a single choice
-          else if constexpr (!SIGMOID) w[r] *= inv;
-          p.ids[slot0 + j] = my_id[r];
-          p.weights[slot0 + j] = w[r] * p.route_scale;
+      for (int j = l; j < p.topk; j += LPT) {
+        float w = __int_as_float(val[j]);
+        if (p.renorm) w = ws > 0.0f ? __fdiv_rn(w, ws) : 0.0f;   // exactly 1 for a single choice
+        else if constexpr (!SIGMOID) w *= inv;
+        if (live) {
+          p.ids[slot0 + j] = slot[j];
+          p.weights[slot0 + j] = w * p.route_scale;
         }
       }
     }
     if constexpr (BAL) {
       if (counted && on) {
-        if constexpr (!GATE) {
-#pragma unroll
-          for (int r = 0; r < KR; ++r)
-            if (r * LPT + l < p.topk) my_id[r] = p.ids[slot0 + r * LPT + l];
+        for (int j = l; j < p.topk; j += LPT) {
+          int id;
+          if constexpr (GATE) id = s_slot[(wave * TPW + g) * SLOTS + j];
+          else id = p.ids[slot0 + j];
+          if (id >= 0 && id < p.E) atomicAdd(&s_cnt[id], 1);
         }
-#pragma unroll
-        for (int r = 0; r < KR; ++r)
-          if (my_id[r] >= 0 && my_id[r] < p.E) atomicAdd(&s_cnt[my_id[r]], 1);
         if (l == 0) ++n;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) acc[v] += s[v] * inv;
       }
     }
+    if constexpr (GATE) wave_lds_fence();   // before the next token's choices
   }
   if constexpr (BAL) {
     constexpr int NG = 256 / LPT;   // token groups of the workgroup, each with its share of the sums
