@@ -30,6 +30,13 @@
 // wave selects again in a second round over keys that hold everything: the exact
 // fp32 logit, or score + bias formed in 64 bits, above the expert's index, as a
 // positive double.
+//
+// Measured on the GPU, fp32 logits (copy rate 5.2 TB/s).  Choice, 65536 x 256 top 8: 20
+// us without and 25-27 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
+// busy 92% of the time (746 operations a wave of four tokens: 320 for scores and keys,
+// 126 for the sorting network, 23 a choice).  A wave a token took 120 us, 64-bit keys
+// from the start 47 us.  With the loss 31 us + 9 us for its sums; 8192 x 64 top 6: 6.4 +
+// 5 us.  Backward, 65536 x 256: 30 us (140 MB: 27 us), bound by HBM; 8192 x 64: 5.7 us.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "lane_groups.hpp"
@@ -839,6 +846,8 @@ static hipError_t gate_dispatch(int E, bool bf16, bool vec, bool sigmoid, F&& f)
     return vec ? scored(N{}, T{}) : scored(N{}, N{});
   };
   using std::integral_constant;
+  // The fewest lanes a token that hold its logits in at most 16 registers each: lane steps are shared by the
+  // wave's tokens (65536 x 256: a wave a token 120 us, 16 lanes 25 us).
   if (E <= 16) return types(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   if (E <= 64) return types(integral_constant<int, 16>{}, integral_constant<int, 4>{});
   if (E <= 128) return types(integral_constant<int, 16>{}, integral_constant<int, 8>{});
