@@ -792,7 +792,8 @@ int moe_gate(const void *logits, int logit_dtype, int64_t tokens, int32_t n_expe
  *             owned by the caller; contents on entry do not matter.  Calls that may overlap
  *             (other streams, graphs replayed side by side) need one each
  *   Sums over tokens are fp32 over at most 128 tokens (up to 2^27 tokens in all), then in
- *   64 bits; no result depends on the order of arrival.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), 1 <= n_seqs <= 65535.
+ *   64 bits, the loss over sequences to |coef| * 2^-33; no result depends on the order of
+ *   arrival.  Requires: as moe_gate; coef finite (else FP8MOE_ERR_VALUE), 1 <= n_seqs <= 65535.
  *   Two kernels, no allocation.
  */
 int moe_balance_loss(const void *logits, int logit_dtype, int64_t tokens, int32_t n_experts, int64_t ld_logits,

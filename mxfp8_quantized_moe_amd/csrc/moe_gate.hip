@@ -33,9 +33,10 @@
 //
 // Measured on the GPU, fp32 logits (copy rate 5.2 TB/s).  Choice, 65536 x 256 top 8: 20
 // us without and 25-27 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
-// busy 92% of the time (746 operations a wave of four tokens: 320 for scores and keys,
-// 126 for the sorting network, 23 a choice).  A wave a token took 120 us, 64-bit keys
-// from the start 47 us.  With the loss 31 us + 9 us for its sums; 8192 x 64 top 6: 6.4 +
+// busy 92% of the time (746 vector operations a wave of four tokens: about 320 for scores
+// and keys, 126 for the sorting network, 23 a choice).  A wave a token took 120 us,
+// looking for close choices once instead of after each choice 71 -> 47 us, the place in
+// the key 47 -> 41 us, a second round that takes a token at a time 41 -> 31 us.  With the loss 31 us + 9 us for its sums; 8192 x 64 top 6: 6.4 +
 // 5 us.  Backward, 65536 x 256: 30 us (140 MB: 27 us), bound by HBM; 8192 x 64: 5.7 us.
 #include "device_common.hpp"
 #include "kernels.hpp"
@@ -506,7 +507,7 @@ struct GateLoss {
   const float* part_p;
   const int32_t* part_c;
   const int32_t* part_n;
-  uint64_t* total;     // sum over slices in units of 2^-50, slices that added theirs; 0 on entry
+  uint64_t* total;     // sum over slices in units of 2^-53, slices that added theirs; 0 on entry
   float* loss;
   int32_t* counts;     // [S][E]
   float* dprob;        // [S][E]
@@ -569,8 +570,9 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
 }
 
 // One workgroup for 32 experts of a sequence: its 32 half-waves each add every 32nd
-// unit, eight loads in flight, in 64 bits.  The sum over slices, sum f P <= E, is
-// kept as a whole number of 2^-50: additions of whole numbers do not depend on their order.
+// unit, eight loads in flight, in 64 bits.  The sum over slices and sequences of
+// f P / S, at most E <= 2^10, is kept as a whole number of 2^-53 (the at most 2^21
+// terms' roundings are 2^-33 together): additions of whole numbers do not depend on their order.
 // Each addition has come back before its slice counts as arrived, so the last one finds them all.
 __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
   constexpr int B = 8;
@@ -638,10 +640,10 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
   auto add = [](uint64_t* at, uint64_t v) {
     return __hip_atomic_fetch_add(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  uint64_t before = add(p.total, (uint64_t)(part * 0x1p50 + 0.5));
+  uint64_t before = add(p.total, (uint64_t)(part / p.S * 0x1p53 + 0.5));
   asm volatile("s_waitcnt vmcnt(0)" : "+v"(before)::"memory");   // its value is here: the addition is done
   if (add(p.total + 1, 1) != slices - 1) return;
-  *p.loss = (float)(scale * ((double)add(p.total, 0) * 0x1p-50));
+  *p.loss = (float)((double)p.coef * ((double)add(p.total, 0) * 0x1p-53));
 }
 
 // ---------------------------------------------------------------- backward

@@ -223,6 +223,26 @@ def test_balance_loss(case, sigmoid):
         assert abs(host(got[0])[0] - loss) <= (6 * spread(z, sigmoid) + 70) * U * abs(loss) + TINY
 
 
+@pytest.mark.parametrize("S,E,n", [(64, 256, 2), (400, 1024, 1), (3, 1024, 50), (65535, 16, 1)])
+def test_loss_of_collapsed_routing(S, E, n):
+    """Every token on one expert: a sequence adds E f P = E, the most there is, S times over.  The sum over sequences
+    and slices of experts rounds each by 2^-54, far below the tolerance."""
+    note(f"moe_gate_balance collapsed {S} sequences of {n} x {E}")
+    z = np.zeros((S * n, E))
+    z[:, 3] = 40.0
+    offs = [n * (s + 1) for s in range(S)]
+    zd = dev(z.astype(np.float32))
+    for sigmoid in (0, 1):
+        ids, w, *rest = fm.moe_gate_balance(zd, 1, 0.5, i32_dev(offs), sigmoid)
+        assert bool((ids == 3).all())
+        loss, counts, dprob = og.balance(z, host(ids), 0.5, offs, bool(sigmoid))
+        if not sigmoid:
+            assert abs(loss - 0.5 * E) < 1e-9 * E
+        np.testing.assert_array_equal(host(rest[1]), counts)
+        assert np.all(np.abs(host(rest[2]) - dprob) <= 2 * U * np.abs(dprob))
+        assert abs(host(rest[0])[0] - loss) <= (6 * spread(z, bool(sigmoid)) + 70) * U * abs(loss) + TINY
+
+
 def test_counts_agree_with_the_routing():
     rng = np.random.default_rng(12)
     zd, z = make_logits(rng, 1000, 64, "f32")
