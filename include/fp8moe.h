@@ -684,7 +684,8 @@ int grouped_mm_scaled(int mode, const void *a, int a_fmt, const void *a_scale,
  *   a residual), rstd = 1 / sqrt(sum(s^2) / cols + eps) and f = (s * gamma) * rstd,
  *   each an fp32 operation and the sum in fp32:
  *   sum       bf16 [rows][cols]  s, the new residual stream (written with a
- *             residual; ignored without one).  It may be x or the residual itself.
+ *             residual; ignored without one).  It may be x or the residual itself
+ *             where that one's ld is cols.
  *   h         bf16 [rows][cols]  bf16(f) (written), or NULL
  *   q, scale  u8 [rows][cols], f32 [rows]: the rowwise recipe over the fp32 values f
  *             (not over their bf16 copy h), or NULL together: no codes (written)

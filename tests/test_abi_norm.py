@@ -46,6 +46,10 @@ def test_forward_rejections(lib):
         assert refused(f, ok, ld_r=68) == L.ERR_ALIGN
         for p in ("x", "res", "gamma", "sum", "h", "q", "rstd"):
             assert refused(f, ok, **{p: MIS}) == L.ERR_ALIGN, p
+        # in place only where rows lie as the sum's do: else a row's sum would land in rows not read yet
+        assert refused(f, ok, ld=72) == L.ERR_SHAPE
+        assert refused(f, ok, ld=72, x=2 * P, sum=2 * P, res=3 * P) == L.ERR_SHAPE
+        assert refused(f, ok, x=2 * P, ld_r=72) == L.ERR_SHAPE
         assert refused(f, ok, rows=0, x=None, res=None, sum=None, h=None, q=None, scale=None, rstd=None) == L.OK
     assert refused(lib.rmsnorm_quantize_rowwise, rw, codec=2) == L.ERR_ENUM
     assert refused(lib.rmsnorm_quantize_rowwise, rw, scale=P + 2) == L.ERR_ALIGN
