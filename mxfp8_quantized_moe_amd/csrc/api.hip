@@ -291,6 +291,7 @@ int rmsnorm_quantize_rowwise(const void* x_bf16, const void* residual_bf16, cons
   int st = check_rmsnorm(x_bf16, residual_bf16, gamma, gamma_dtype, rows, cols, ld_x, ld_residual, eps, sum_bf16,
                          h_bf16, q, scale, rstd);
   if (!st) st = check_rmsnorm_rowwise(codec, q, scale);
+  if (!st) st = check_rmsnorm_in_place(x_bf16, residual_bf16, rows, cols, ld_x, ld_residual, sum_bf16);
   if (st) return st;
   const NormArgs a{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16), gamma,
                    gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps, q ? codec : 4, 0,
@@ -306,6 +307,7 @@ int rmsnorm_quantize_mx(const void* x_bf16, const void* residual_bf16, const voi
   int st = check_rmsnorm(x_bf16, residual_bf16, gamma, gamma_dtype, rows, cols, ld_x, ld_residual, eps, sum_bf16,
                          h_bf16, q, scale_e8m0, rstd);
   if (!st) st = check_rmsnorm_mx(rule, scale_layout, rows, cols, q, scale_e8m0);
+  if (!st) st = check_rmsnorm_in_place(x_bf16, residual_bf16, rows, cols, ld_x, ld_residual, sum_bf16);
   if (st) return st;
   const NormArgs a{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16), gamma,
                    gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps, 2 + rule, scale_layout,

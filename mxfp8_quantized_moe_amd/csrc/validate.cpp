@@ -430,7 +430,12 @@ int check_rmsnorm(const void* x, const void* res, const void* gamma, int gamma_d
   if (cols % 8 || ld_x % 8 || (res && ld_r % 8) || !aligned(x, 16) || !aligned(res, 16) || !aligned(gamma, 16) ||
       !aligned(sum, 16) || !aligned(h, 16) || !aligned(q, 16) || !aligned(rstd, 4))
     return FP8MOE_ERR_ALIGN;
-  // In place only where the input's rows lie as the sum's do: else a row's sum lands in rows that are not read yet.
+  return FP8MOE_OK;
+}
+
+// In place only where the input's rows lie as the sum's do: else a row's sum lands in rows that are not read yet.
+int check_rmsnorm_in_place(const void* x, const void* res, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r,
+                           const void* sum) {
   if (res && rows > 1 && ((sum == x && ld_x != cols) || (sum == res && ld_r != cols))) return FP8MOE_ERR_SHAPE;
   return FP8MOE_OK;
 }

@@ -94,6 +94,8 @@ constexpr int64_t kNormMaxCols = 16384;
 int check_rmsnorm(const void* x, const void* res, const void* gamma, int gamma_dtype, int64_t rows, int64_t cols,
                   int64_t ld_x, int64_t ld_r, float eps, const void* sum, const void* h, const void* q,
                   const void* scale, const void* rstd);
+int check_rmsnorm_in_place(const void* x, const void* res, int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_r,
+                           const void* sum);
 int check_rmsnorm_rowwise(int codec, const void* q, const void* scale);
 int check_rmsnorm_mx(int rule, int layout, int64_t rows, int64_t cols, const void* q, const void* sc);
 // Workgroups of the backward, each with one row of dgamma shares in the workspace.
