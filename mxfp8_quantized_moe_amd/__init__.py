@@ -584,6 +584,16 @@ def _vec(fn, name, t, n, dtypes):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
+def _workspace(fn, workspace, need, dev):
+    """A caller's workspace, checked, or a new one."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if (workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous() or
+            workspace.device != dev):
+        raise ValueError(f"{fn}: a contiguous workspace of {need} bytes needed on {dev}")
+    return workspace
+
+
 _BF16, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
 
@@ -667,11 +677,8 @@ def rmsnorm_backward(dh, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, w
         dev = dh.device
         dx = _out(fn, "dx", dx, (R, C), torch.bfloat16, dev)
         dgamma = _out(fn, "dgamma", dgamma, (C,), torch.float32, dev) if want_dgamma else None
-        need = max(rmsnorm_backward_workspace_bytes(R, C), 16) if want_dgamma else 0
-        if want_dgamma and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif want_dgamma and workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"{fn}: workspace of {need} bytes needed")
+        if want_dgamma:
+            workspace = _workspace(fn, workspace, max(rmsnorm_backward_workspace_bytes(R, C), 16), dev)
         _lib.check(fn, _lib.lib().rmsnorm_backward(
             _ptr(dh), _ptr(s), _ptr(rstd), _ptr(gamma),
             OUT_BF16 if gamma is not None and gamma.dtype == torch.bfloat16 else OUT_F32, _ptr(dsum), R, C, _ptr(dx),
@@ -681,8 +688,8 @@ def rmsnorm_backward(dh, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, w
 
 def _gate_inputs(fn, logits, token_mask):
     T, E, ld = _rows2d(fn, "logits", logits, _BF16_F32)
-    if E < 1:
-        raise ValueError(f"{fn}: logits need at least one expert")
+    if not 1 <= E < 2**31:   # an int32 argument
+        raise ValueError(f"{fn}: logits need at least one expert, fewer than 2^31, got {E}")
     _vec(fn, "token_mask", token_mask, T, (torch.uint8, torch.bool))
     return T, E, ld, OUT_F32 if logits.dtype == torch.float32 else OUT_BF16
 
@@ -703,8 +710,8 @@ def _gate_slots(fn, name, t, T, dtypes):
 def _gate_seqs(fn, seq_offs):
     if seq_offs is None:
         return 1
-    if seq_offs.numel() < 1:
-        raise ValueError(f"{fn}: seq_offs needs at least one sequence")
+    if not 1 <= seq_offs.numel() < 2**31:   # an int32 argument
+        raise ValueError(f"{fn}: seq_offs needs at least one sequence, fewer than 2^31, got {seq_offs.numel()}")
     _vec(fn, "seq_offs", seq_offs, seq_offs.numel(), _I32)
     return seq_offs.numel()
 
@@ -735,10 +742,7 @@ def _balance_outputs(fn, T, E, S, loss, counts, dprob, workspace, dev):
     need = moe_balance_workspace_bytes(T, E, S)
     if need < 0:
         raise ValueError(f"{fn}: invalid sizes tokens={T} experts={E} sequences={S}")
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.numel() * workspace.element_size() < need or workspace.device != dev:
-        raise ValueError(f"{fn}: workspace of {need} bytes needed on {dev}")
+    workspace = _workspace(fn, workspace, need, dev)
     return (_out(fn, "loss", loss, (1,), torch.float32, dev), _out(fn, "counts", counts, (S, E), torch.int32, dev),
             _out(fn, "dprob", dprob, (S, E), torch.float32, dev), workspace)
 

@@ -139,3 +139,10 @@ def test_binding_refusals():
             calls["lossback"](dprob=bad)
     with pytest.raises(ValueError, match="dloss"):
         calls["lossback"](dloss=torch.ones(2))
+
+
+def test_more_experts_than_an_int32_counts():
+    """2^32 + 5 experts are not taken for five."""
+    z = torch.empty((0, 2**32 + 5), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="fewer than"):
+        fm.moe_gate(z, 2)

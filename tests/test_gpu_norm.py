@@ -195,6 +195,28 @@ def test_empty_and_refused():
         fm.rmsnorm_quantize_rowwise(wide[:, :64], torch.ones(64))
 
 
+def test_workspaces_that_do_not_hold_their_bytes():
+    note("rmsnorm_backward, moe_balance_loss workspaces")
+    x = torch.ones(40, 64, dtype=torch.bfloat16, device=DEV)
+    one = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    for bad in (one, one.expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            fm.rmsnorm_backward(x, x, torch.ones(40, device=DEV), workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            fm.moe_gate_balance(x, 2, 0.1, workspace=bad)
+
+
+def test_smallest_epsilon():
+    """Rows of zeros with an epsilon below the normal fp32 range: rstd stays finite, codes zero."""
+    note("rmsnorm smallest epsilon")
+    x = torch.zeros(3, 64, dtype=torch.bfloat16, device=DEV)
+    for eps in (2.0 ** -149, 2.0 ** -130):
+        h, q, sc, rs, _ = fm.rmsnorm_quantize_rowwise(x, eps=eps)
+        want = 1.0 / np.sqrt(eps)
+        assert np.all(np.abs(host(rs) - want) <= 4 * 2.0 ** -24 * want)   # a root and a quotient, each rounded once
+        assert not h.any() and not q.any() and bool(torch.isfinite(sc).all())
+
+
 BWD = [(1, 8), (2, 48), (17, 64), (5, 200), (70, 512), (7, 520), (33, 2048), (9, 2056), (3, 4104), (2, 8200), (5, 16384),
        (2500, 64), (5000, 600), (1500, 2304)]
 
