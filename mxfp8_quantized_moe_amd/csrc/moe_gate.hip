@@ -75,8 +75,8 @@ __device__ __forceinline__ int expert_at(int l, int v) {
 }
 
 // The lane's VPL logits of a row starting at element `row` (-inf past E or when off).  VEC: E and the row
-// stride are multiples of four and every array of experts starts aligned, so a chunk is one load.
-template <int LPT, int VPL, bool BF16, bool VEC>
+// stride are multiples of four and every array of experts starts aligned, so a chunk is one load.  RAW: not cleaned.
+template <int LPT, int VPL, bool BF16, bool VEC, bool RAW = false>
 __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64_t row, int E, int l, bool on,
                                           float (&z)[VPL]) {
   if constexpr (VEC) {
@@ -109,8 +109,10 @@ __device__ __forceinline__ void gate_load(const void* __restrict__ logits, int64
   // All loads have left before the first is cleaned (the compiler would clean each in its own branch, one wait a load).
 #pragma unroll
   for (int v = 0; v < VPL; ++v) asm volatile("" : "+v"(z[v]));
+  if constexpr (!RAW) {
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) z[v] = gate_clean(z[v]);
+    for (int v = 0; v < VPL; ++v) z[v] = gate_clean(z[v]);
+  }
 }
 
 // fp32 vector of the experts (a bias, the loss's derivative), 0 past E.
@@ -155,10 +157,12 @@ __device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VP
 
 // ---------------------------------------------------------------- keys
 
-__device__ __forceinline__ uint32_t sortable(float v) {
-  const uint32_t b = __float_as_uint(v + 0.0f);   // -0 -> +0
+// A value that is not -0.
+__device__ __forceinline__ uint32_t sortable_nz(float v) {
+  const uint32_t b = __float_as_uint(v);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t sortable(float v) { return sortable_nz(v + 0.0f); }   // -0 -> +0
 __device__ __forceinline__ float sorted_value(uint32_t s) {
   return __uint_as_float(s ^ ((int32_t)s < 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
@@ -353,7 +357,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
     const bool on = live && (p.mask == nullptr || p.mask[t] != 0);
     const int64_t row = (int64_t)t * p.ld, slot0 = (int64_t)t * p.topk;
     float z[VPL], s[VPL], m, total;
-    gate_load<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, on, z);
+    // Sigmoid keys with a bias take the logits as they are, a sixth fewer operations a logit.
+    constexpr bool RAW = SIGMOID && GATE && !BAL;
+    gate_load<LPT, VPL, BF16, VEC, RAW>(p.logits, row, p.E, l, on, z);
     gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);
     const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 
@@ -366,14 +372,16 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
         uint32_t key[VPL];
         if (!biased) {
 #pragma unroll
-          for (int v = 0; v < VPL; ++v) key[v] = (sortable(z[v]) & ~15u) | (uint32_t)(15 - v);
+          for (int v = 0; v < VPL; ++v) key[v] = (sortable(RAW ? gate_clean(z[v]) : z[v]) & ~15u) | (uint32_t)(15 - v);
         } else {
           float b[VPL];
           gate_load_vec<LPT, VPL, VEC>(p.bias, p.E, l, b);
 #pragma unroll
           for (int v = 0; v < VPL; ++v) {
-            const float k = gate_clean((SIGMOID ? s[v] : s[v] * inv) + b[v]);
-            key[v] = (sortable(z[v] > -INFINITY ? k : -INFINITY) & ~15u) | (uint32_t)(15 - v);
+            // NaN (of the bias) is below all; +inf stays, the checks below see it as close to the largest finite
+            // value; a sum of a score, which is not -0, is not -0
+            const float k = fmaxf((SIGMOID ? s[v] : s[v] * inv) + b[v], -INFINITY);
+            key[v] = (sortable_nz(z[v] > -INFINITY ? k : -INFINITY) & ~15u) | (uint32_t)(15 - v);
           }
         }
         sort_desc(key);

@@ -189,6 +189,24 @@ def test_infinite_bias():
     assert np.all(ids[:, :2] == [2, 5]) and np.all(ids[:, 10:] == -1) and not np.any((ids == 7) | (ids == 0))
 
 
+def test_largest_keys():
+    """Infinite biases go before the largest finite one, which swallows the scores: each kind's ties to the lower index,
+    chosen or left out."""
+    note("moe_gate largest keys")
+    big = np.finfo(np.float32).max
+    z = np.random.default_rng(8).standard_normal((70, 40)).astype(np.float32)
+    z[1, :] = -np.inf
+    z[2, ::2] = np.nan
+    z[3, 5], z[3, 30] = np.inf, -big
+    bias = np.zeros(40, np.float32)
+    bias[[5, 21, 39]], bias[[2, 20, 30]], bias[11], bias[12], bias[13] = np.inf, big, -big, -0.0, -np.inf
+    for sigmoid in (0, 1):
+        for k in (1, 2, 3, 5, 6, 7, 40):
+            ids, w = fm.moe_gate(dev(z), k, sigmoid, dev(bias))
+            want, _ = og.gate(z.astype(np.float64), k, bool(sigmoid), bias)
+            np.testing.assert_array_equal(host(ids), want)
+
+
 # tokens, experts, topk, sequence ends (None: no offsets)
 LOSSES = [(1, 4, 1, None), (0, 8, 2, None), (0, 8, 2, [0, 0]), (64, 16, 1, [64]), (100, 16, 1, [10, 10, 50, 90]),
           (333, 64, 6, [1, 2, 3, 333]), (50, 256, 8, [20, 5, 70, 50]), (2000, 30, 3, None), (40, 1000, 5, [0, 40]),
