@@ -205,16 +205,14 @@ __device__ __forceinline__ void sort_desc(T (&k)[N]) {
           }
 }
 
-// Whether this is the lowest lane of its group of LPT for which `is` holds.
+// Whether this is the lowest lane of its group of LPT for which `is` holds; it holds somewhere in every group, and all
+// lanes are here.  On the wave's mask, by scalar operations: one taken from each group's bits clears its lowest set
+// one and, as no group is empty, borrows nothing from the next group.
 template <int LPT>
-__device__ __forceinline__ bool lowest_lane(bool is, int lane) {
+__device__ __forceinline__ bool lowest_lane(bool is) {
+  constexpr uint64_t kOnes = LPT == 64 ? 1u : LPT == 16 ? 0x0001000100010001u : 0x1111111111111111u;
   const uint64_t all = __ballot(is);
-  if constexpr (LPT == 64) {
-    return lane == __ffsll((unsigned long long)all) - 1;
-  } else {
-    const uint32_t m = (uint32_t)(all >> (lane & ~(LPT - 1))) & ((1u << LPT) - 1u);
-    return (m & (0u - m)) == 1u << (lane & (LPT - 1));
-  }
+  return __builtin_amdgcn_inverse_ballot_w64(all & ~(all - kOnes));
 }
 
 // The list without its head where `take`: of a sorted list only the first KEEP keys are needed.
@@ -393,7 +391,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           for (int j = 0; j < p.topk; ++j) {
             const uint32_t head = key[0] & kCompare;
             const uint32_t best = group_most_u32<LPT>(head);
-            const bool mine = lowest_lane<LPT>(head == best, lane);
+            const bool mine = lowest_lane<LPT>(head == best);
             *(mine ? slot + j : aside) = best >= kLeast32 ? (int)((key[0] & 15u) | (uint32_t)(l << 4)) : -1;
             move_up<decltype(keep)::value>(key, mine);
           }
