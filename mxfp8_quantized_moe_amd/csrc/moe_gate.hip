@@ -32,9 +32,9 @@
 // positive double.
 //
 // Measured on the GPU, fp32 logits (copy rate 5.2 TB/s).  Choice, 65536 x 256 top 8: 20
-// us without and 25-27 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
-// busy 92% of the time (746 vector operations a wave of four tokens: about 320 for scores
-// and keys, 126 for the sorting network, 23 a choice).  A wave a token took 120 us,
+// us without and 23-26 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
+// busy 89% of the time (664 vector operations a wave of four tokens: about 260 for scores
+// and keys, 126 for the sorting network, 17 a choice).  A wave a token took 120 us,
 // looking for close choices once instead of after each choice 71 -> 47 us, the place in
 // the key 47 -> 41 us, a second round that takes a token at a time 41 -> 31 us.  With the loss 31 us + 9 us for its sums; 8192 x 64 top 6: 6.4 +
 // 5 us.  Backward, 65536 x 256: 30 us (140 MB: 27 us), bound by HBM; 8192 x 64: 5.7 us.

@@ -312,7 +312,7 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
 // A workgroup walks rows with a stride of the grid and keeps its columns' share of
 // dgamma in registers (fp32); the shares go to the workspace, one row per
 // workgroup, and a second kernel adds them in a fixed order.  Bound by HBM: 8 bytes
-// an element with dsum.  512 workgroups: 16384 x 5120 takes 136 us (4.9 TB/s) + 5 us for
+// an element with dsum.  512 workgroups: 16384 x 5120 takes 135 us (5.0 TB/s) + 5 us for
 // the shares; 1024 take 132 + 14, and where only 768 fit (8192 x 7168) 119 instead of
 // 97.  Loading dsum with the other rows instead of after the row's sum, and three
 // chunks a thread instead of four, brought both kernels together from 195 us to 141.

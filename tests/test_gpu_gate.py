@@ -311,6 +311,42 @@ def test_backward(case, sigmoid):
                 assert np.all(g[~mask] == 0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("odd", ["logits", "bias", "dprob", "dlogits"])
+def test_arrays_one_element_off(dtype, odd):
+    """Each array starting one element past an aligned place, 256 experts: what aligned copies give (ids equal, sums of
+    another order within the tolerances' roundings), and nothing is written beside the outputs."""
+    note(f"moe_gate {odd} one element off {dtype}")
+
+    def place(name, t):
+        if name != odd:
+            return t
+        flat = torch.full((t.numel() + 9,), 7.0, dtype=t.dtype, device=DEV)
+        flat[1:1 + t.numel()] = t.view(-1)
+        return flat[1:1 + t.numel()].view(t.shape)
+
+    g = torch.Generator(device=DEV).manual_seed(11)
+    T, E, k = 37, 256, 8
+    z = torch.randn(T, E, generator=g, device=DEV).to(dtype)
+    bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+    dw = torch.randn(T, k, generator=g, device=DEV)
+    ids, w, loss, counts, dprob = fm.moe_gate_balance(z, k, 0.1, None, 1, bias, renormalize=True)
+    got = fm.moe_gate_balance(place("logits", z), k, 0.1, None, 1, place("bias", bias), renormalize=True)
+    assert torch.equal(got[0], ids) and torch.equal(got[3], counts) and torch.equal(got[4], dprob)
+    assert bool(((got[1] - w).abs() <= 16 * U * w.abs()).all())       # eight positive scores summed, one division
+    assert bool(((got[2] - loss).abs() <= 300 * U * loss).all())      # 256 positive scores, then the units' sums
+    want = fm.moe_gate_backward(z, ids, dw, 1, renormalize=True, dprob=dprob)
+    out = place("dlogits", torch.zeros(T, E, dtype=dtype, device=DEV))
+    back = fm.moe_gate_backward(place("logits", z), ids, dw, 1, renormalize=True, dprob=place("dprob", dprob), dlogits=out)
+    assert back is out
+    # sums of at most 256 terms of the size of dw (at most 5) over the chosen scores (at least 8 / 2): both rounded
+    size = 300 * U * 5 + (2.0 ** -7 * want.float().abs() if dtype == torch.bfloat16 else 0)
+    assert bool(((back.float() - want.float()).abs() <= size).all())
+    if odd == "dlogits":
+        whole = out.as_strided((T * E + 9,), (1,), out.storage_offset() - 1)
+        assert float(whole[0]) == 7.0 and bool((whole[T * E + 1:] == 7.0).all())
+
+
 def test_masked_tokens_stay_zero():
     """An overflowed loss gradient and NaN weights' gradients do not reach masked or uncounted tokens."""
     note("moe_gate_backward masked")
