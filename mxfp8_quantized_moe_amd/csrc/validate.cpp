@@ -479,6 +479,7 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
   return FP8MOE_OK;
 }
 
+// Without the loss a workgroup takes a single step (65536 x 256 top 8 with a bias: 25.7 us, two steps 26.2, four 28.1).
 int gate_step(int32_t E) { return E <= 16 ? 64 : E <= 256 ? 16 : 4; }
 
 // Never more than 2^20 workgroups (and their threads within 32 bits).
