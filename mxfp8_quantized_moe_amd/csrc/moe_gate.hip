@@ -288,12 +288,12 @@ struct TokenRange {
   int t0, t1;
 };
 __device__ __forceinline__ TokenRange gate_unit(const int32_t* __restrict__ offs, int S, int T, int u, int chunk) {
-  auto chunks = [chunk](int lo, int hi) { return (hi - lo + chunk - 1) / chunk; };
+  auto chunks = [chunk](int lo, int hi) { return gate_chunks(lo, hi, chunk); };
   auto len = [](int lo, int hi) { return hi - lo; };
   const Unit un = find_unit_quant<256>(offs, S, T, u, chunks, len);
   if (un.e >= 0) {
     const int t0 = un.lo + un.j * chunk;
-    return TokenRange{un.e, t0, min(t0 + chunk, un.hi)};
+    return TokenRange{un.e, t0, gate_chunk_end(t0, un.hi, chunk)};
   }
   const int64_t t0 = un.pbase + (int64_t)un.j * chunk;   // pbase: the end of the last sequence
   return t0 < T ? TokenRange{-1, (int)t0, (int)min(t0 + chunk, (int64_t)T)} : TokenRange{-1, 0, 0};
@@ -525,7 +525,7 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
                                           int& count) {
   if (offs == nullptr) {
     first = 0;
-    count = (T + chunk - 1) / chunk;
+    count = gate_chunks(0, T, chunk);
     return;
   }
   if (S <= 64) {   // every wave on its own, no barrier
@@ -538,7 +538,7 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
     }
     int lo = __shfl_up(hi, 1, 64);
     if (lane == 0) lo = 0;
-    const int cnt = lane < S ? (hi - lo + chunk - 1) / chunk : 0;
+    const int cnt = lane < S ? gate_chunks(lo, hi, chunk) : 0;
     int incl = cnt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -559,7 +559,7 @@ __device__ __forceinline__ void seq_units(const int32_t* __restrict__ offs, int 
     s_hi[t] = hi;
     __syncthreads();
     const int lo = t == 0 ? carry : s_hi[t - 1];
-    const int cnt = e < S ? (hi - lo + chunk - 1) / chunk : 0;
+    const int cnt = e < S ? gate_chunks(lo, hi, chunk) : 0;
     const int incl = block_scan_sum<NT>(cnt, tmp) + base;
     if (e == s) {
       s_first = incl - cnt;

@@ -510,7 +510,7 @@ int check_moe_gate_logits(const void* logits, int dtype, int64_t tokens, int32_t
   if (score != FP8MOE_GATE_SOFTMAX && score != FP8MOE_GATE_SIGMOID) return FP8MOE_ERR_ENUM;
   if (tokens < 0 || E < 1 || ld < E || topk < 1 || topk > E) return FP8MOE_ERR_SHAPE;
   if (E > kGateMaxExperts || topk > kGateMaxTopk) return FP8MOE_ERR_UNSUPPORTED;
-  if (tokens > kI32Max - 1024 || mul(tokens, topk) > kI32Max || mul(tokens, ld) < 0) return FP8MOE_ERR_SHAPE;
+  if (tokens > kGateMaxTokens || mul(tokens, topk) > kI32Max || mul(tokens, ld) < 0) return FP8MOE_ERR_SHAPE;
   if (!need(logits, tokens)) return FP8MOE_ERR_NULL;
   if (!aligned(logits, dtype == FP8MOE_OUT_F32 ? 4 : 2)) return FP8MOE_ERR_ALIGN;
   return FP8MOE_OK;

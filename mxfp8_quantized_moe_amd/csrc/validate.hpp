@@ -111,6 +111,14 @@ int check_rmsnorm_backward(const void* dh, const void* s, const void* rstd, cons
 constexpr int kGateMaxExperts = 1024;
 constexpr int kGateMaxTopk = 64;
 constexpr int kGateMaxSeqs = 65535;   // a grid dimension of the loss kernel
+constexpr int64_t kGateMaxTokens = 2147483647 - 1024;   // a wave's next step stays within 32 bits
+// Chunks of tokens [lo, hi), and where the chunk starting at t0 < hi ends.  No sum passes hi, whatever the chunk (for
+// kGateMaxTokens tokens it is 2048).
+constexpr int gate_chunks(int lo, int hi, int chunk) { return hi > lo ? (hi - lo - 1) / chunk + 1 : 0; }
+constexpr int gate_chunk_end(int t0, int hi, int chunk) { return hi - t0 < chunk ? hi : t0 + chunk; }
+static_assert(gate_chunks(0, kGateMaxTokens, 2048) == 1 << 20, "all tokens in chunks");
+static_assert(gate_chunk_end(2048 * ((1 << 20) - 1), kGateMaxTokens, 2048) == kGateMaxTokens, "the last chunk ends with them");
+static_assert(gate_chunks(5, 5, 128) == 0 && gate_chunks(5, 133, 128) == 1 && gate_chunks(5, 134, 128) == 2, "partial chunks");
 int gate_step(int32_t E);
 int gate_tile(int64_t tokens, int32_t E);
 int gate_chunk(int64_t tokens, int32_t E);
