@@ -757,8 +757,7 @@ int64_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *            the logits decide
  *   token_mask  u8 [tokens] or NULL: a token of value 0 chooses nothing
  *   ids      int32 [tokens][topk]  the experts of largest key, in decreasing order, equal
- *            keys to the lower index (with a bias, keys within 2^-42 of each other count
- *            as equal); -1 where no eligible expert is left (written)
+ *            keys to the lower index; -1 where no eligible expert is left (written)
  *   weights  f32 [tokens][topk]  route_scale * score, the scores divided by their sum over
  *            the token's choices when renormalize is non-zero; 0 where ids is -1, and for
  *            choices whose scores sum to 0 (written)

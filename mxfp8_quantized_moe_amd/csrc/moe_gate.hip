@@ -27,9 +27,8 @@
 // exact values are formed anyway, for the weights: where two consecutive choices
 // are in the wrong order or, with a bias, closer than the rounding of fp32 keys
 // allows, or where the first key left out may be as large as the last choice, the
-// wave selects again in a second round over keys that hold everything: the exact
-// fp32 logit, or score + bias formed in 64 bits, above the expert's index, as a
-// positive double.
+// wave selects again in a second round over whole keys: the exact logit, or
+// score + bias formed in 64 bits, equal keys to the lower expert.
 //
 // Measured on the GPU, fp32 logits (copy rate 5.2 TB/s).  Choice, 65536 x 256 top 8: 20
 // us without and 23-26 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
@@ -45,7 +44,7 @@
 
 namespace fp8moe {
 
-static_assert(kGateMaxExperts == 1024, "a key's index has ten bits; 64 lanes hold 16 logits each");
+static_assert(kGateMaxExperts == 1024, "64 lanes hold 16 logits each");
 
 constexpr float kFltMax = 3.402823466e38f;
 typedef float gt_f32x2 __attribute__((ext_vector_type(2)));
@@ -168,24 +167,7 @@ __device__ __forceinline__ float sorted_value(uint32_t s) {
 }
 constexpr uint32_t kLeast32 = 0x00800000u;   // -FLT_MAX; -inf (no eligible expert) and 0 (an emptied list) are below
 
-// Keys of the second round: positive doubles, the expert's complemented index in the low ten bits.  The fp32
-// range maps to the high words 0x00400000 .. 0x7FBFFFFF, below the patterns of infinity and NaN.
-constexpr double kLeastKey = 0x1p-1019;      // high word 0x00400000
-__device__ __forceinline__ double gate_key(float v, int idx) {
-  const uint32_t s = sortable(v);
-  return __longlong_as_double((int64_t)(((uint64_t)(s >> 1) << 32) | (s << 31) | (uint32_t)(1023 - idx)));
-}
-// The same of a 64-bit value (1e300 and more count as equal; the low 11 bits give way to the index).
-__device__ __forceinline__ double gate_key64(double v, int idx) {
-  const uint64_t b = (uint64_t)__double_as_longlong(fmin(fmax(v, -1e300), 1e300) + 0.0);
-  const uint64_t s = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
-  return __longlong_as_double((int64_t)(((s >> 1) & ~1023ull) | (uint32_t)(1023 - idx)));
-}
-__device__ __forceinline__ int gate_index(double key) { return 1023 - (int)(__double_as_longlong(key) & 1023); }
-
 // Descending order by Batcher's odd-even merge network.
-__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
-__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 __device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
 template <typename T, int N>
@@ -240,17 +222,19 @@ __device__ __forceinline__ void with_keep(int topk, F&& f) {
 }
 
 // The second round for one token (row, wave-uniform), by a whole wave: its choices go to slot[0 .. topk).
-// m: the row's largest logit (softmax).
+// m: the row's largest logit (softmax).  A key is the logit, or score + bias in 64 bits, all of them: the wave takes the
+// largest and then the lowest expert that holds it, an exchange of its own (an index in the key's low bits would make
+// keys equal that are 2^-41 of their value apart).
 template <int VPL, bool BF16, bool SIGMOID, bool VEC>
 __device__ __forceinline__ void select_exact(const void* __restrict__ logits, int64_t row, int E,
                                              const float* __restrict__ bias, float m, int topk, int* slot) {
   const int lane = threadIdx.x & 63;
   float z[VPL];
-  double key[VPL];
+  double key[VPL];   // -inf: not eligible, or chosen before
   gate_load<64, VPL, BF16, VEC>(logits, row, E, lane, true, z);
   if (bias == nullptr) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) key[v] = gate_key(z[v], expert_at<64, VEC>(lane, v));
+    for (int v = 0; v < VPL; ++v) key[v] = (double)z[v];
   } else {
     float b[VPL];
     gate_load_vec<64, VPL, VEC>(bias, E, lane, b);
@@ -264,18 +248,22 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const double k = (SIGMOID ? key[v] : key[v] / total) + (double)b[v];
-      const double packed = gate_key64(k, expert_at<64, VEC>(lane, v));
-      key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? packed : 0.0;
+      key[v] = z[v] > -INFINITY && b[v] > -INFINITY ? k : -(double)INFINITY;   // a NaN of the bias is not above -inf
     }
   }
-  sort_desc(key);
-  with_keep<VPL>(topk, [&](auto keep) {
-    for (int j = 0; j < topk; ++j) {
-      const double best = group_max_f64<64>(key[0]);
-      if (lane == 0) slot[j] = best >= kLeastKey ? gate_index(best) : -1;
-      move_up<decltype(keep)::value>(key, key[0] == best);
-    }
-  });
+  for (int j = 0; j < topk; ++j) {
+    double best = key[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) best = fmax(best, key[v]);
+    best = group_max_f64<64>(best);
+    uint32_t at = 0;   // the lowest expert that holds it, counted down from the most there are; 0: none here
+#pragma unroll
+    for (int v = VPL - 1; v >= 0; --v) at = key[v] == best ? kGateMaxExperts - expert_at<64, VEC>(lane, v) : at;
+    const int id = kGateMaxExperts - (int)group_most_u32<64>(at);
+    if (lane == 0) slot[j] = best > -(double)INFINITY ? id : -1;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) key[v] = expert_at<64, VEC>(lane, v) == id ? -(double)INFINITY : key[v];
+  }
 }
 
 // ---------------------------------------------------------------- work units
