@@ -135,6 +135,15 @@ __device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
+// A sigmoid score and its complement 1 - s = sigmoid(-z), each to a few roundings of itself (1 - s formed from a rounded s
+// has no digits left from a logit of 17 on).
+__device__ __forceinline__ void sigmoid_pair(float z, float& s, float& comp) {
+  const float e = __expf(-fabsf(z));   // 0 for infinities
+  const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+  s = z >= 0.0f ? big : small;
+  comp = z >= 0.0f ? small : big;
+}
+
 // Scores of the lane's logits, the softmax's before its division: m is the row's maximum, total their sum
 // over the token.
 template <int LPT, int VPL, bool SIGMOID>
@@ -643,14 +652,15 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
 // ---------------------------------------------------------------- backward
 //
 // With p the scores, ds the gradient reaching them:
-//   softmax  dz = p (ds - sum p ds),    sigmoid  dz = ds p (1 - p).
-// ds of a chosen expert: route_scale dw, or with renormalisation
-// (route_scale dw - sum over slots of route_scale dw u) / (chosen scores' sum), u the
-// normalised weights; plus the loss's dloss * dprob on the normalised scores.
-// Renormalised softmax weights do not depend on the other experts: their part of dz,
-// u (route_scale dw - sum ...), is added to the chosen experts as it is, so that the
-// rounding of sum p ds, zero for it, does not reach the other experts' (the loss's)
-// gradients, which are often far smaller.
+//   softmax  dz = p (ds - sum p ds),    sigmoid  dz = (1 - p) (ds p), 1 - p = sigmoid(-z).
+// What reaches the scores: the loss's dloss * dprob, on the normalised scores q (a
+// sigmoid's are p / sum p: q (d - sum q d) takes the place of ds p), and at a chosen
+// expert route_scale dw, or with renormalisation u (route_scale dw - sum over slots of
+// route_scale dw u) in the place of ds p, u the normalised weights.
+// Renormalised softmax weights do not depend on the other experts: their part of dz
+// is added to the chosen experts as it is, so that the rounding of sum p ds, zero for
+// it, does not reach the other experts' (the loss's) gradients, which are often far
+// smaller.  A sigmoid's slots hold their part of ds p.
 // The slots' values reach the lanes that hold their experts through one LDS row a
 // token (the wave's own, so no barrier).
 
@@ -709,16 +719,28 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         dw[r] = id[r] >= 0 ? p.dweights[slot0 + j] * p.route_scale : 0.0f;
       }
     }
-    gate_scores<LPT, VPL, SIGMOID>(z, s, m, total);   // all scores 0 when the token is off
+    if constexpr (SIGMOID) {   // z becomes the complements
+      total = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        sigmoid_pair(z[v], s[v], z[v]);
+        total += s[v];
+      }
+      total = group_sum_f32<LPT>(total);
+    } else {
+      gate_scores<LPT, VPL, false>(z, s, m, total);   // all scores 0 when the token is off
+    }
     const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) s[v] *= inv;   // the normalised scores
     float dot = 0.0f;
     if constexpr (SIGMOID) {   // the loss's part through the division by the scores' sum
 #pragma unroll
       for (int v = 0; v < VPL; ++v) dot += dp[v] * s[v];
-      dot = group_sum_f32<LPT>(dot) * inv;
+      dot = group_sum_f32<LPT>(dot);
     }
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? (dp[v] - dot) * inv : dp[v];
+    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? s[v] * (dp[v] - dot) : dp[v];
 
     if (p.dweights != nullptr) {
       if (p.renorm) {
@@ -738,7 +760,11 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         mean = group_sum_f32<LPT>(mean);
         const float f = ws > 0.0f ? __fdiv_rn(1.0f, ws) : 0.0f;
 #pragma unroll
-        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * (SIGMOID ? f : w[r] * f);
+        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * (w[r] * f);
+      } else if constexpr (SIGMOID) {
+#pragma unroll
+        for (int r = 0; r < KR; ++r)
+          if (id[r] >= 0) dw[r] *= sigmoid_f32(gate_logit<BF16>(p.logits, row + id[r]));
       }
       // Slot values into the token's row.  Each slot first leaves its number at its expert: a slot that reads
       // another's shares its expert with it, and then the slots add up one after another, in their order.
@@ -778,7 +804,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       for (int v = 0; v < VPL; ++v) ds[v] += mine[expert_at<LPT, VEC>(l, v)];
       wave_lds_fence();
     };
-    const bool direct = !SIGMOID && p.renorm;   // the slots hold their part of dz, not of ds
+    const bool direct = !SIGMOID && p.renorm;   // the slots hold their part of dz
     if (p.dweights != nullptr && !direct) add_slots();
     if (!on) {   // whatever the loss's gradient holds
 #pragma unroll
@@ -786,14 +812,11 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     }
     if constexpr (SIGMOID) {
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) ds[v] *= s[v] * (1.0f - s[v]);
+      for (int v = 0; v < VPL; ++v) ds[v] *= z[v];
     } else {
       dot = 0.0f;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        s[v] *= inv;
-        dot += s[v] * ds[v];
-      }
+      for (int v = 0; v < VPL; ++v) dot += s[v] * ds[v];
       dot = group_sum_f32<LPT>(dot);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);

@@ -132,3 +132,73 @@ def backward(logits, ids, dweights, sigmoid: bool, mask=None, renorm: bool = Fal
         dz = s * (ds - (ds * s).sum(axis=1, keepdims=True))
         mag = s * (mag + (mag * s).sum(axis=1, keepdims=True))
     return np.where(on[:, None], dz, 0.0), np.where(on[:, None], mag, 0.0)
+
+
+# ---------------------------------------------------------------- the same gradient by differences
+#
+# A softmax's (or a quotient's) gradient is u_i (x_i - sum u x) with sum u = 1, which is u_i times the sum over the others
+# j of u_j (x_i - x_j): no digits are lost where one u is close to 1.  Scores are kept on the scale of the largest one, and
+# a sigmoid's complement is sigmoid(-z).
+
+
+def sigmoid_parts(z: np.ndarray):
+    """(s exp(-min(row maximum, 0)), 1 - s) of logits z [T, N]; (0, 1) for -inf."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        c = np.minimum(np.max(z, axis=1, keepdims=True, initial=-FLT_MAX), 0.0)
+        e = np.exp(-np.abs(z))
+        return np.exp(np.minimum(z, 0.0) - c) / (1 + e), np.where(z >= 0, e, 1.0) / (1 + e)
+
+
+def parts_of_one(z: np.ndarray, sigmoid: bool) -> np.ndarray:
+    """Scores over their sum along the rows [T, N], on the scale of the largest (rows of -inf: zeros)."""
+    w = sigmoid_parts(z)[0] if sigmoid else np.exp(z - np.max(z, axis=1, keepdims=True, initial=-FLT_MAX))
+    tot = w.sum(axis=1, keepdims=True)
+    return np.divide(w, tot, out=np.zeros_like(w), where=tot > 0)
+
+
+def quotient_gradient(u: np.ndarray, x: np.ndarray, size: np.ndarray):
+    """u_i sum over the others j of u_j (x_i - x_j), and the same sum of magnitudes, size standing for |x|."""
+    n = u.shape[1]
+    rest = np.ones((n, n)) - np.eye(n)
+    g = u * ((u @ rest) * x - (u * x) @ rest)
+    return g, u * ((u @ rest) * size + (u * size) @ rest)
+
+
+def backward_by_differences(logits, ids, dweights, sigmoid: bool, mask=None, renorm: bool = False, route_scale: float = 1.0,
+                            dprob=None, dloss: float = 1.0, seq_offs=None):
+    """backward() for eligible choices, with every term to its own digits -> (dlogits, size), size the sum of the magnitudes
+    of the terms that remain (after a sigmoid's complement, and the others' share of a quotient)."""
+    z = eligible_logits(logits)
+    T, E = z.shape
+    on = np.ones(T, bool) if mask is None else np.asarray(mask).astype(bool)
+    p = parts_of_one(z, sigmoid)
+    comp = sigmoid_parts(z)[1] if sigmoid else np.ones((T, E))
+    ds, mag = np.zeros((T, E)), np.zeros((T, E))     # through the scores' own quotient
+    dz, size = np.zeros((T, E)), np.zeros((T, E))    # past it
+    if dprob is not None:
+        for i, (lo, hi) in enumerate(sequences(seq_offs, T)):
+            ds[lo:hi] = dloss * np.asarray(dprob, np.float64)[i]
+    mag += np.abs(ds)
+    if dweights is not None:
+        for t in range(T):
+            j = [j for j in range(ids.shape[1]) if 0 <= ids[t, j] < E]
+            if not j:
+                continue
+            i = ids[t, j]
+            dw = np.asarray(dweights, np.float64)[t, j] * route_scale
+            if renorm:
+                u = parts_of_one(z[t, i][None], sigmoid)
+                g, m = quotient_gradient(u, dw[None], np.abs(dw)[None])
+                np.add.at(dz[t], i, g[0])
+                np.add.at(size[t], i, m[0])
+            elif sigmoid:
+                with np.errstate(over="ignore"):
+                    s = 1.0 / (1.0 + np.exp(-z[t, i]))
+                np.add.at(dz[t], i, s * dw)
+                np.add.at(size[t], i, s * np.abs(dw))
+            else:
+                np.add.at(ds[t], i, dw)
+                np.add.at(mag[t], i, np.abs(dw))
+    g, m = quotient_gradient(p, ds, mag)
+    ok = on[:, None] & (z > -np.inf)
+    return np.where(ok, (dz + g) * comp, 0.0), np.where(ok, (size + m) * comp, 0.0)
