@@ -759,8 +759,8 @@ int64_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *   ids      int32 [tokens][topk]  the experts of largest key, in decreasing order, equal
  *            keys to the lower index; -1 where no eligible expert is left (written)
  *   weights  f32 [tokens][topk]  route_scale * score, the scores divided by their sum over
- *            the token's choices when renormalize is non-zero; 0 where ids is -1, and for
- *            choices whose scores sum to 0 (written)
+ *            the token's choices when renormalize is non-zero (their ratios, also where each
+ *            of them is below the fp32 range); 0 where ids is -1 (written)
  *   ids and weights are what moe_route and moe_combine take (moe_route drops id -1).
  *   Requires: 1 <= topk <= n_experts, ld_logits >= n_experts, tokens*topk within int32;
  *   route_scale finite (else FP8MOE_ERR_VALUE); n_experts <= 1024 and topk <= 64 (else

@@ -144,6 +144,15 @@ __device__ __forceinline__ void sigmoid_pair(float z, float& s, float& comp) {
   comp = z >= 0.0f ? small : big;
 }
 
+// A chosen expert's score for the renormalised weights, on the scale of the token's choices: without the factor exp(c),
+// c the largest chosen logit (a sigmoid's at most 0).  The largest is at least a half, so the sum cannot vanish and the
+// ratios hold where every score of the choices is below the fp32 range (a bias can choose experts 100 below the others).
+template <bool SIGMOID>
+__device__ __forceinline__ float scaled_score(float z, float c) {
+  if constexpr (SIGMOID) return __expf(fminf(z, 0.0f) - c) * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(z)));
+  else return __expf(z - c);
+}
+
 // Scores of the lane's logits, the softmax's before its division: m is the row's maximum, total their sum
 // over the token.
 template <int LPT, int VPL, bool SIGMOID>
@@ -445,10 +454,18 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
             if (slot[j] >= 0) val[j] = __float_as_int(gate_logit<BF16>(p.logits, row + slot[j]));
       }
       wave_lds_fence();
-      float ws = 0.0f;
+      float ws = 0.0f, c = -INFINITY;
+      if (p.renorm) {
+        for (int j = l; j < p.topk; j += LPT) c = slot[j] < 0 ? c : fmaxf(c, __int_as_float(val[j]));
+        c = group_max_f32<LPT>(c);
+        if constexpr (SIGMOID) c = fminf(c, 0.0f);
+      }
       for (int j = l; j < p.topk; j += LPT) {
         const float zj = __int_as_float(val[j]);
-        const float w = slot[j] < 0 ? 0.0f : SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+        const float w = slot[j] < 0 ? 0.0f
+                        : p.renorm  ? scaled_score<SIGMOID>(zj, c)
+                        : SIGMOID   ? sigmoid_f32(zj)
+                                    : __expf(zj - m);
         val[j] = __float_as_int(w);
         ws += w;
       }
@@ -744,14 +761,18 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 
     if (p.dweights != nullptr) {
       if (p.renorm) {
-        float w[KR], ws = 0.0f, mean = 0.0f;
+        float w[KR], ws = 0.0f, mean = 0.0f, c = -INFINITY;
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
-          w[r] = 0.0f;
-          if (id[r] >= 0) {
-            const float zj = gate_logit<BF16>(p.logits, row + id[r]);
-            w[r] = SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
-          }
+          w[r] = id[r] >= 0 ? gate_logit<BF16>(p.logits, row + id[r]) : -INFINITY;
+          c = fmaxf(c, w[r]);
+        }
+        c = group_max_f32<LPT>(c);
+        if constexpr (SIGMOID) c = fminf(c, 0.0f);
+        c = fmaxf(c, -kFltMax);   // no eligible expert among the choices
+#pragma unroll
+        for (int r = 0; r < KR; ++r) {
+          w[r] = scaled_score<SIGMOID>(w[r], c);   // 0 for -inf
           ws += w[r];
         }
         ws = group_sum_f32<LPT>(ws);
