@@ -785,7 +785,8 @@ int moe_gate(const void *logits, int logit_dtype, int64_t tokens, int32_t n_expe
  *   loss      f32 [1]  coef / n_seqs * sum over s and i of f[s][i] * P[s][i], with n[s] the
  *             unmasked tokens of s, f = c * n_experts / (topk * n[s]) and P the mean over
  *             those tokens of the scores divided by their sum over the experts (softmax
- *             scores as they are); a sequence without tokens adds 0 (written)
+ *             scores as they are; sigmoid logits all below -709.78, scores of 0 even in 64
+ *             bits, have no share); a sequence without tokens adds 0 (written)
  *   dprob     f32 [n_seqs][n_experts]  the loss's derivative by one token's normalised score
  *             of expert i: coef / n_seqs * f / n[s], what moe_gate_backward takes (written)
  *   workspace device memory of moe_balance_workspace_bytes(...) bytes, 16-byte aligned,

@@ -172,6 +172,33 @@ __device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VP
   total = group_sum_f32<LPT>(total);
 }
 
+// A sigmoid token's scores over their sum, where the sum is below kLowTotal, on the scale of the row's largest logit m:
+// exp(z - m) / (1 + exp(z)), every logit being negative (the scores themselves fall below the fp32 range from -87 on).
+// With a sum of kLowTotal and more a score below the range is below 2^-125 of it.  A row whose sigmoids are 0 in 64 bits
+// (all logits below kLeastSigmoid, as those of a row masked by the type's lowest value are) has none.
+constexpr float kLowTotal = 0.5f;
+constexpr float kLeastSigmoid = -709.78f;
+template <int LPT, int VPL, bool BF16, bool VEC>
+__device__ __forceinline__ void low_sigmoid_scores(const void* __restrict__ logits, int64_t row, int E, int l, bool low,
+                                                   float (&s)[VPL], float& inv) {
+  float z[VPL], m = -kFltMax, total = 0.0f;
+  gate_load<LPT, VPL, BF16, VEC>(logits, row, E, l, low, z);
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) m = fmaxf(m, z[v]);
+  m = group_max_f32<LPT>(m);
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    z[v] = __expf(z[v] - m) * __builtin_amdgcn_rcpf(1.0f + __expf(z[v]));   // 0 for -inf
+    total += z[v];
+  }
+  total = group_sum_f32<LPT>(total);
+  if (low) {
+    inv = total > 0.0f && m >= kLeastSigmoid ? __fdiv_rn(1.0f, total) : 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) s[v] = z[v];
+  }
+}
+
 // ---------------------------------------------------------------- keys
 
 // A value that is not -0.
@@ -489,8 +516,16 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
           if (id >= 0 && id < p.E) atomicAdd(&s_cnt[id], 1);
         }
         if (l == 0) ++n;
+      }
+      float share = inv;
+      if constexpr (SIGMOID) {
+        const bool low = on && total < kLowTotal;
+        if (counted && __ballot(low) != 0)   // wave-uniform
+          low_sigmoid_scores<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, low, s, share);
+      }
+      if (counted && on) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) acc[v] += s[v] * inv;
+        for (int v = 0; v < VPL; ++v) acc[v] += s[v] * share;
       }
     }
     if constexpr (GATE) wave_lds_fence();   // before the next token's choices
@@ -747,7 +782,12 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     } else {
       gate_scores<LPT, VPL, false>(z, s, m, total);   // all scores 0 when the token is off
     }
-    const float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+    float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+    if constexpr (SIGMOID) {
+      const bool low = on && total < kLowTotal;
+      if (rg.seq >= 0 && __ballot(low) != 0)   // wave-uniform
+        low_sigmoid_scores<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, low, s, inv);
+    }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) s[v] *= inv;   // the normalised scores
     float dot = 0.0f;

@@ -156,6 +156,17 @@ def parts_of_one(z: np.ndarray, sigmoid: bool) -> np.ndarray:
     return np.divide(w, tot, out=np.zeros_like(w), where=tot > 0)
 
 
+LEAST_SIGMOID = -709.78   # 1 / (1 + exp(-z)) is 0 in 64 bits below
+
+
+def loss_shares(z: np.ndarray, sigmoid: bool) -> np.ndarray:
+    """What the loss averages: none for a token whose sigmoids are 0 in 64 bits."""
+    p = parts_of_one(z, sigmoid)
+    if sigmoid:
+        p[np.max(z, axis=1, initial=-FLT_MAX) < LEAST_SIGMOID] = 0.0
+    return p
+
+
 def quotient_gradient(u: np.ndarray, x: np.ndarray, size: np.ndarray):
     """u_i sum over the others j of u_j (x_i - x_j), and the same sum of magnitudes, size standing for |x|."""
     n = u.shape[1]
@@ -171,7 +182,7 @@ def backward_by_differences(logits, ids, dweights, sigmoid: bool, mask=None, ren
     z = eligible_logits(logits)
     T, E = z.shape
     on = np.ones(T, bool) if mask is None else np.asarray(mask).astype(bool)
-    p = parts_of_one(z, sigmoid)
+    p = loss_shares(z, sigmoid)
     comp = sigmoid_parts(z)[1] if sigmoid else np.ones((T, E))
     ds, mag = np.zeros((T, E)), np.zeros((T, E))     # through the scores' own quotient
     dz, size = np.zeros((T, E)), np.zeros((T, E))    # past it

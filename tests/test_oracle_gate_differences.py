@@ -69,3 +69,12 @@ def test_keeps_its_digits(row, sigmoid, renorm):
         got, size = og.backward_by_differences(z, ids, d, sigmoid, None, renorm, 1.0, p)
         want = decimal_gradient(row, ids[0], None if d is None else d[0], sigmoid, renorm, None if p is None else p[0])
         assert np.all(np.abs(got[0] - want) <= 1e-13 * size[0] + 1e-300), (got, want)
+
+
+def test_shares():
+    """On the scale of the row's largest score; none where the sigmoids are 0 in 64 bits, which the formulas give as well."""
+    z = np.array([[-100.0, -101.0], [-700.0, -700.0], [-750.0, -750.0], [0.0, -800.0], [-np.inf, -np.inf], [-np.inf, -3.0]])
+    a = 1 / (1 + np.exp(-1.0))
+    np.testing.assert_allclose(og.loss_shares(z, True), [[a, 1 - a], [0.5, 0.5], [0, 0], [1, 0], [0, 0], [0, 1]])
+    np.testing.assert_allclose(og.shares(z, True), og.loss_shares(z, True))
+    np.testing.assert_allclose(og.loss_shares(z, False), og.shares(z, False))
