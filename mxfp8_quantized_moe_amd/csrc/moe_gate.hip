@@ -716,6 +716,20 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
 // The slots' values reach the lanes that hold their experts through one LDS row a
 // token (the wave's own, so no barrier).
 
+// A quotient's gradient u_i (x_i - sum u x), sum u = 1, does not change when one number is taken from every x.  Where one
+// u is above a half, that x is taken: its own difference is then exactly 0, and what is left of a confident token, the
+// others' u_j (x_j - x), is not the rounding of two nearly equal numbers (at 1 - u = 2^-24 nothing else was left).  With
+// no u above a half nothing cancels, and 0 is taken.
+
+// The x whose u is above a half, else 0 (in every lane of the token's group).
+template <int LPT, int N>
+__device__ __forceinline__ float dominant(const float (&u)[N], const float (&x)[N]) {
+  float c = 0.0f;
+#pragma unroll
+  for (int v = 0; v < N; ++v) c += u[v] > 0.5f ? x[v] : 0.0f;
+  return group_sum_f32<LPT>(c);
+}
+
 struct GateBwd {
   const void* logits;
   int64_t ld;
@@ -790,14 +804,18 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     }
 #pragma unroll
     for (int v = 0; v < VPL; ++v) s[v] *= inv;   // the normalised scores
-    float dot = 0.0f;
+    float dot = 0.0f, top = 0.0f;
+    // a sigmoid is at most 1: a score above half their sum needs a sum below 2
+    if (SIGMOID && rg.seq >= 0 && __ballot(on && total < 2.0f) != 0) top = dominant<LPT>(s, dp);   // wave-uniform
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? dp[v] - top : dp[v];
     if constexpr (SIGMOID) {   // the loss's part through the division by the scores' sum
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) dot += dp[v] * s[v];
+      for (int v = 0; v < VPL; ++v) dot += ds[v] * s[v];
       dot = group_sum_f32<LPT>(dot);
-    }
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? s[v] * (dp[v] - dot) : dp[v];
+      for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
+    }
 
     if (p.dweights != nullptr) {
       if (p.renorm) {
@@ -817,11 +835,16 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         }
         ws = group_sum_f32<LPT>(ws);
 #pragma unroll
-        for (int r = 0; r < KR; ++r) mean += ws > 0.0f ? dw[r] * __fdiv_rn(w[r], ws) : 0.0f;
-        mean = group_sum_f32<LPT>(mean);
-        const float f = ws > 0.0f ? __fdiv_rn(1.0f, ws) : 0.0f;
+        for (int r = 0; r < KR; ++r) w[r] = ws > 0.0f ? __fdiv_rn(w[r], ws) : 0.0f;
+        const float first = dominant<LPT>(w, dw);
 #pragma unroll
-        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * (w[r] * f);
+        for (int r = 0; r < KR; ++r) {
+          dw[r] -= first;
+          mean += dw[r] * w[r];
+        }
+        mean = group_sum_f32<LPT>(mean);
+#pragma unroll
+        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * w[r];
       } else if constexpr (SIGMOID) {
 #pragma unroll
         for (int r = 0; r < KR; ++r)
@@ -876,6 +899,11 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       for (int v = 0; v < VPL; ++v) ds[v] *= z[v];
     } else {
       dot = 0.0f;
+      if (__ballot(inv > 0.5f) != 0) {   // the largest softmax score is exp(0) inv; wave-uniform
+        top = dominant<LPT>(s, ds);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) ds[v] -= top;
+      }
 #pragma unroll
       for (int v = 0; v < VPL; ++v) dot += s[v] * ds[v];
       dot = group_sum_f32<LPT>(dot);
