@@ -823,6 +823,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
           w[r] = id[r] >= 0 ? gate_logit<BF16>(p.logits, row + id[r]) : -INFINITY;
+          if (!(w[r] > -INFINITY)) id[r] = -1, dw[r] = 0.0f;   // an ineligible expert passes nothing
           c = fmaxf(c, w[r]);
         }
         c = group_max_f32<LPT>(c);
@@ -848,7 +849,11 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       } else if constexpr (SIGMOID) {
 #pragma unroll
         for (int r = 0; r < KR; ++r)
-          if (id[r] >= 0) dw[r] *= sigmoid_f32(gate_logit<BF16>(p.logits, row + id[r]));
+          if (id[r] >= 0) {
+            const float zj = gate_logit<BF16>(p.logits, row + id[r]);
+            dw[r] *= sigmoid_f32(zj);
+            if (!(zj > -INFINITY)) id[r] = -1;   // an ineligible expert passes nothing
+          }
       }
       // Slot values into the token's row.  Each slot first leaves its number at its expert: a slot that reads
       // another's shares its expert with it, and then the slots add up one after another, in their order.
@@ -910,6 +915,12 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
       if (p.dweights != nullptr && direct) add_slots();
+    }
+    // A score of 0 times an overflowed gradient is no 0: the ineligible experts' are set (wave-uniform, rare).
+    if (__ballot(on && !(fabsf(dot) <= kFltMax)) != 0) {
+      gate_load<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, on, z);
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) ds[v] = z[v] > -INFINITY ? ds[v] : 0.0f;
     }
     if (live) {
       const int64_t out = (int64_t)t * p.E;
