@@ -107,7 +107,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
   const bool valid = row < p.rows;
   const int64_t r = valid ? row : 0;
   const int64_t cols = (int64_t)p.nchunk * 8;
-  const u32x4* __restrict__ xr = reinterpret_cast<const u32x4*>(p.x + r * p.ld_x);
+  const u32x4* xr = reinterpret_cast<const u32x4*>(p.x + r * p.ld_x);   // the sum may be written over it
   u32x4 v[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
@@ -115,8 +115,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
     v[i] = valid && c < p.nchunk ? xr[c] : u32x4{0, 0, 0, 0};
   }
   if (p.res != nullptr) {
-    const u32x4* __restrict__ rr = reinterpret_cast<const u32x4*>(p.res + r * p.ld_r);
-    u32x4* __restrict__ so = reinterpret_cast<u32x4*>(p.sum + r * cols);
+    const u32x4* rr = reinterpret_cast<const u32x4*>(p.res + r * p.ld_r);
+    u32x4* so = reinterpret_cast<u32x4*>(p.sum + r * cols);   // may be x's rows or the residual's
     u32x4 w[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
