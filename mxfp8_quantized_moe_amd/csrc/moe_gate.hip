@@ -135,23 +135,28 @@ __device__ __forceinline__ void gate_load_vec(const float* __restrict__ x, int E
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
-// A sigmoid score and its complement 1 - s = sigmoid(-z), each to a few roundings of itself (1 - s formed from a rounded s
-// has no digits left from a logit of 17 on).
-__device__ __forceinline__ void sigmoid_pair(float z, float& s, float& comp) {
+// A sigmoid score s, its complement 1 - s = sigmoid(-z) and its derivative s (1 - s), each to a few roundings of itself (1 - s
+// formed from a rounded s has no digits left from a logit of 17 on).
+struct Sigmoid {
+  float s, comp, slope;
+};
+__device__ __forceinline__ Sigmoid sigmoid_parts(float z) {
   const float e = __expf(-fabsf(z));   // 0 for infinities
   const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
-  s = z >= 0.0f ? big : small;
-  comp = z >= 0.0f ? small : big;
+  return z >= 0.0f ? Sigmoid{big, small, small * big} : Sigmoid{small, big, small * big};
 }
 
-// A chosen expert's score for the renormalised weights, on the scale of the token's choices: without the factor exp(c),
-// c the largest chosen logit (a sigmoid's at most 0).  The largest is at least a half, so the sum cannot vanish and the
-// ratios hold where every score of the choices is below the fp32 range (a bias can choose experts 100 below the others).
+// A score on the scale of the largest of its kind: without the factor exp(c), c the largest logit (a sigmoid's at most 0).
+// The largest is at least a half, so their sum cannot vanish and their ratios hold where every score is below the fp32
+// range: chosen experts' where a bias chooses 100 below the others, a sigmoid row's from logits of -87 on.
 template <bool SIGMOID>
 __device__ __forceinline__ float scaled_score(float z, float c) {
   if constexpr (SIGMOID) return __expf(fminf(z, 0.0f) - c) * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(z)));
   else return __expf(z - c);
 }
+// Renormalised weights are taken on that scale where the chosen scores' sum is below this.  With a larger sum, a score that
+// falls below the fp32 range is below 2^-102 of it.
+constexpr float kLowChosen = 0x1p-24f;
 
 // Scores of the lane's logits, the softmax's before its division: m is the row's maximum, total their sum
 // over the token.
@@ -172,31 +177,41 @@ __device__ __forceinline__ void gate_scores(const float (&z)[VPL], float (&s)[VP
   total = group_sum_f32<LPT>(total);
 }
 
-// A sigmoid token's scores over their sum, where the sum is below kLowTotal, on the scale of the row's largest logit m:
-// exp(z - m) / (1 + exp(z)), every logit being negative (the scores themselves fall below the fp32 range from -87 on).
-// With a sum of kLowTotal and more a score below the range is below 2^-125 of it.  A row whose sigmoids are 0 in 64 bits
-// (all logits below kLeastSigmoid, as those of a row masked by the type's lowest value are) has none.
+// A sigmoid token's scores and one over their sum where the sum is below kLowTotal, on the scale of the row's largest logit
+// (all are negative).  With a sum of kLowTotal and more a score below the fp32 range is below 2^-125 of it.  A row whose
+// sigmoids are 0 in 64 bits (all logits below kLeastSigmoid, as those of a row masked by the type's lowest value are) has no
+// share of the loss.
 constexpr float kLowTotal = 0.5f;
 constexpr float kLeastSigmoid = -709.78f;
+// The path is rare: it reads the logits again, one at a time, and passes the scores through the token's LDS row `mine`
+// (W floats), so that the kernels around it keep their registers.
 template <int LPT, int VPL, bool BF16, bool VEC>
 __device__ __forceinline__ void low_sigmoid_scores(const void* __restrict__ logits, int64_t row, int E, int l, bool low,
-                                                   float (&s)[VPL], float& inv) {
-  float z[VPL], m = -kFltMax, total = 0.0f;
-  gate_load<LPT, VPL, BF16, VEC>(logits, row, E, l, low, z);
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) m = fmaxf(m, z[v]);
-  m = group_max_f32<LPT>(m);
-#pragma unroll
+                                                   float* mine, float (&s)[VPL], float& inv) {
+  const int n = low ? E : 0;
+  float m = -kFltMax, total = 0.0f;
+#pragma unroll 1
   for (int v = 0; v < VPL; ++v) {
-    z[v] = __expf(z[v] - m) * __builtin_amdgcn_rcpf(1.0f + __expf(z[v]));   // 0 for -inf
-    total += z[v];
+    const int e = expert_at<LPT, VEC>(l, v);
+    if (e < n) m = fmaxf(m, gate_logit<BF16>(logits, row + e));
+  }
+  m = group_max_f32<LPT>(m);
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) {
+    const int e = expert_at<LPT, VEC>(l, v);
+    const float z = e < n ? gate_logit<BF16>(logits, row + e) : -INFINITY;
+    const float w = scaled_score<true>(z, m);   // 0 for -inf
+    mine[e] = w;
+    total += w;
   }
   total = group_sum_f32<LPT>(total);
+  wave_lds_fence();
   if (low) {
     inv = total > 0.0f && m >= kLeastSigmoid ? __fdiv_rn(1.0f, total) : 0.0f;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) s[v] = z[v];
+    for (int v = 0; v < VPL; ++v) s[v] = mine[expert_at<LPT, VEC>(l, v)];
   }
+  wave_lds_fence();
 }
 
 // ---------------------------------------------------------------- keys
@@ -273,7 +288,7 @@ __device__ __forceinline__ void with_keep(int topk, F&& f) {
 template <int VPL, bool BF16, bool SIGMOID, bool VEC>
 __device__ __forceinline__ void select_exact(const void* __restrict__ logits, int64_t row, int E,
                                              const float* __restrict__ bias, float m, int topk, int* slot) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, first = expert_at<64, VEC>(lane, 0);   // the lane's experts lie at the same distances
   float z[VPL];
   double key[VPL];   // -inf: not eligible, or chosen before
   gate_load<64, VPL, BF16, VEC>(logits, row, E, lane, true, z);
@@ -301,13 +316,13 @@ __device__ __forceinline__ void select_exact(const void* __restrict__ logits, in
 #pragma unroll
     for (int v = 1; v < VPL; ++v) best = fmax(best, key[v]);
     best = group_max_f64<64>(best);
-    uint32_t at = 0;   // the lowest expert that holds it, counted down from the most there are; 0: none here
+    int at = kGateMaxExperts - first;   // the lane's lowest expert that holds it, from its first; none: past the last there is
 #pragma unroll
-    for (int v = VPL - 1; v >= 0; --v) at = key[v] == best ? kGateMaxExperts - expert_at<64, VEC>(lane, v) : at;
-    const int id = kGateMaxExperts - (int)group_most_u32<64>(at);
+    for (int v = VPL - 1; v >= 0; --v) at = key[v] == best ? expert_at<64, VEC>(0, v) : at;
+    const int id = kGateMaxExperts - (int)group_most_u32<64>((uint32_t)(kGateMaxExperts - first - at));
     if (lane == 0) slot[j] = best > -(double)INFINITY ? id : -1;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) key[v] = expert_at<64, VEC>(lane, v) == id ? -(double)INFINITY : key[v];
+    for (int v = 0; v < VPL; ++v) key[v] = expert_at<64, VEC>(0, v) == id - first ? -(double)INFINITY : key[v];
   }
 }
 
@@ -481,22 +496,31 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
             if (slot[j] >= 0) val[j] = __float_as_int(gate_logit<BF16>(p.logits, row + slot[j]));
       }
       wave_lds_fence();
-      float ws = 0.0f, c = -INFINITY;
-      if (p.renorm) {
-        for (int j = l; j < p.topk; j += LPT) c = slot[j] < 0 ? c : fmaxf(c, __int_as_float(val[j]));
-        c = group_max_f32<LPT>(c);
-        if constexpr (SIGMOID) c = fminf(c, 0.0f);
-      }
+      float ws = 0.0f, c = -INFINITY;   // c: the lane's largest chosen logit, where a score of it is small
       for (int j = l; j < p.topk; j += LPT) {
         const float zj = __int_as_float(val[j]);
-        const float w = slot[j] < 0 ? 0.0f
-                        : p.renorm  ? scaled_score<SIGMOID>(zj, c)
-                        : SIGMOID   ? sigmoid_f32(zj)
-                                    : __expf(zj - m);
+        const float w = slot[j] < 0 ? 0.0f : SIGMOID ? sigmoid_f32(zj) : __expf(zj - m);
+        c = slot[j] < 0 ? c : fmaxf(c, zj);
         val[j] = __float_as_int(w);
         ws += w;
       }
-      if (p.renorm) ws = group_sum_f32<LPT>(ws);
+      if (p.renorm) {
+        ws = group_sum_f32<LPT>(ws);
+        if (__ballot(ws < kLowChosen && c > -INFINITY) != 0) {   // wave-uniform, rare
+          c = group_max_f32<LPT>(c);
+          if constexpr (SIGMOID) c = fminf(c, 0.0f);
+          float scaled = 0.0f;
+          if (ws < kLowChosen) {
+            for (int j = l; j < p.topk; j += LPT) {
+              const float w = slot[j] < 0 ? 0.0f : scaled_score<SIGMOID>(gate_logit<BF16>(p.logits, row + slot[j]), c);
+              val[j] = __float_as_int(w);
+              scaled += w;
+            }
+          }
+          scaled = group_sum_f32<LPT>(scaled);
+          ws = ws < kLowChosen ? scaled : ws;
+        }
+      }
       for (int j = l; j < p.topk; j += LPT) {
         float w = __int_as_float(val[j]);
         if (p.renorm) w = ws > 0.0f ? __fdiv_rn(w, ws) : 0.0f;   // exactly 1 for a single choice
@@ -521,7 +545,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateFwd p) {
       if constexpr (SIGMOID) {
         const bool low = on && total < kLowTotal;
         if (counted && __ballot(low) != 0)   // wave-uniform
-          low_sigmoid_scores<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, low, s, share);
+          low_sigmoid_scores<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, low, s_sum + (wave * TPW + g) * W, s, share);
       }
       if (counted && on) {
 #pragma unroll
@@ -712,7 +736,7 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
 // Renormalised softmax weights do not depend on the other experts: their part of dz
 // is added to the chosen experts as it is, so that the rounding of sum p ds, zero for
 // it, does not reach the other experts' (the loss's) gradients, which are often far
-// smaller.  A sigmoid's slots hold their part of ds p.
+// smaller.  A sigmoid's slots hold their part of dz too.
 // The slots' values reach the lanes that hold their experts through one LDS row a
 // token (the wave's own, so no barrier).
 
@@ -721,6 +745,12 @@ __global__ __launch_bounds__(1024) void gate_loss_kernel(GateLoss p) {
 // others' u_j (x_j - x), is not the rounding of two nearly equal numbers (at 1 - u = 2^-24 nothing else was left).  With
 // no u above a half nothing cancels, and 0 is taken.
 
+// A product as it is rounded: fused into a difference from itself, it would leave its rounding there instead of 0.
+__device__ __forceinline__ float rounded(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 // The x whose u is above a half, else 0 (in every lane of the token's group).
 template <int LPT, int N>
 __device__ __forceinline__ float dominant(const float (&u)[N], const float (&x)[N]) {
@@ -728,6 +758,62 @@ __device__ __forceinline__ float dominant(const float (&u)[N], const float (&x)[
 #pragma unroll
   for (int v = 0; v < N; ++v) c += u[v] > 0.5f ? x[v] : 0.0f;
   return group_sum_f32<LPT>(c);
+}
+
+// A sigmoid token's sums for the loss's gradient where the scores' sum is below kSmallTotal, the only ones of which a score can
+// hold more than half (a score is at most 1) or whose scores can be below the fp32 range: on the scale of the largest, and by
+// differences from the dominant expert.  d: s (1 - s) on that scale; inv: one over the scores' sum on it; top and dot: the
+// dominant expert's derivative and the mean of the differences from it.  Rare: the logits and the loss's derivative are read
+// again, one at a time, through the token's LDS row `mine`, so that the kernel keeps its registers.
+constexpr float kSmallTotal = 2.0f;
+template <int LPT, int VPL, bool BF16, bool VEC>
+__device__ __forceinline__ void small_sigmoid_sums(const void* __restrict__ logits, int64_t row,
+                                                   const float* __restrict__ dprob, const float* __restrict__ dloss, int E,
+                                                   int l, bool small, float* mine, float (&d)[VPL], float& inv, float& top,
+                                                   float& dot) {
+  const int n = small ? E : 0;
+  const float dl = dloss != nullptr ? *dloss : 1.0f;
+  float m = -kFltMax, total = 0.0f, most = 0.0f, of = 0.0f, sum = 0.0f;
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) {
+    const int e = expert_at<LPT, VEC>(l, v);
+    if (e < n) m = fmaxf(m, gate_logit<BF16>(logits, row + e));
+  }
+  m = group_max_f32<LPT>(m);
+  const float c = fminf(m, 0.0f);
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) {
+    const int e = expert_at<LPT, VEC>(l, v);
+    if (e < n) {
+      const float w = scaled_score<true>(gate_logit<BF16>(logits, row + e), c);   // 0 for -inf
+      total += w;
+      of = w > most ? rounded(dprob[e] * dl) : of;
+      most = fmaxf(most, w);
+    }
+  }
+  total = group_sum_f32<LPT>(total);
+  const float x = group_sum_f32<LPT>(most > 0.5f * total ? of : 0.0f);
+#pragma unroll 1
+  for (int v = 0; v < VPL; ++v) {
+    const int e = expert_at<LPT, VEC>(l, v);
+    if (e < n) {
+      const float z = gate_logit<BF16>(logits, row + e), w = scaled_score<true>(z, c);
+      sum += w * (rounded(dprob[e] * dl) - x);
+      mine[e] = w * sigmoid_parts(z).comp;
+    } else {
+      mine[e] = 0.0f;
+    }
+  }
+  sum = group_sum_f32<LPT>(sum);
+  wave_lds_fence();
+  if (small) {
+    inv = total > 0.0f && m >= kLeastSigmoid ? __fdiv_rn(1.0f, total) : 0.0f;
+    top = x;
+    dot = sum * inv;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) d[v] = mine[expert_at<LPT, VEC>(l, v)];
+  }
+  wave_lds_fence();
 }
 
 struct GateBwd {
@@ -765,7 +851,7 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
     const float dl = p.dloss != nullptr ? *p.dloss : 1.0f;
     gate_load_vec<LPT, VPL, VEC>(p.dprob + (int64_t)rg.seq * p.E, p.E, l, dp);
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) dp[v] *= dl;
+    for (int v = 0; v < VPL; ++v) dp[v] = rounded(dp[v] * dl);
   }
   for (int base = rg.t0 + wave * TPW; base < rg.t1; base += 4 * TPW) {   // wave-uniform
     const int t = base + g;
@@ -782,59 +868,74 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         const int j = r * LPT + l;
         id[r] = on && j < p.topk ? p.ids[slot0 + j] : -1;
         if (id[r] < 0 || id[r] >= p.E) id[r] = -1;
-        dw[r] = id[r] >= 0 ? p.dweights[slot0 + j] * p.route_scale : 0.0f;
+        dw[r] = id[r] >= 0 ? rounded(p.dweights[slot0 + j] * p.route_scale) : 0.0f;
       }
     }
-    if constexpr (SIGMOID) {   // z becomes the complements
+    float dot = 0.0f, top = 0.0f, inv;
+    if constexpr (SIGMOID) {   // the loss's part, through the division by the scores' sum
       total = 0.0f;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        sigmoid_pair(z[v], s[v], z[v]);
-        total += s[v];
+        const Sigmoid q = sigmoid_parts(z[v]);
+        total += q.s;
+        dot += dp[v] * q.s;
+        ds[v] = q.slope;
       }
       total = group_sum_f32<LPT>(total);
+      inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
+      dot = group_sum_f32<LPT>(dot) * inv;
+      const bool small = rg.seq >= 0 && on && total < kSmallTotal;
+      if (__ballot(small) != 0) {   // wave-uniform
+        small_sigmoid_sums<LPT, VPL, BF16, VEC>(p.logits, row, p.dprob + (int64_t)rg.seq * p.E, p.dloss, p.E, l, small, mine, ds,
+                                                inv, top, dot);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) ds[v] = ds[v] * inv * ((dp[v] - top) - dot);
+      } else {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) ds[v] = ds[v] * inv * (dp[v] - dot);
+      }
     } else {
       gate_scores<LPT, VPL, false>(z, s, m, total);   // all scores 0 when the token is off
-    }
-    float inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
-    if constexpr (SIGMOID) {
-      const bool low = on && total < kLowTotal;
-      if (rg.seq >= 0 && __ballot(low) != 0)   // wave-uniform
-        low_sigmoid_scores<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, low, s, inv);
-    }
+      inv = total > 0.0f ? __fdiv_rn(1.0f, total) : 0.0f;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) s[v] *= inv;   // the normalised scores
-    float dot = 0.0f, top = 0.0f;
-    // a sigmoid is at most 1: a score above half their sum needs a sum below 2
-    if (SIGMOID && rg.seq >= 0 && __ballot(on && total < 2.0f) != 0) top = dominant<LPT>(s, dp);   // wave-uniform
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) ds[v] = SIGMOID ? dp[v] - top : dp[v];
-    if constexpr (SIGMOID) {   // the loss's part through the division by the scores' sum
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) dot += ds[v] * s[v];
-      dot = group_sum_f32<LPT>(dot);
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
+      for (int v = 0; v < VPL; ++v) {
+        s[v] *= inv;
+        ds[v] = dp[v];
+      }
     }
 
     if (p.dweights != nullptr) {
       if (p.renorm) {
-        float w[KR], ws = 0.0f, mean = 0.0f, c = -INFINITY;
+        float w[KR], comp[KR], ws = 0.0f, mean = 0.0f, c = -INFINITY;   // c: the lane's largest chosen logit
 #pragma unroll
         for (int r = 0; r < KR; ++r) {
-          w[r] = id[r] >= 0 ? gate_logit<BF16>(p.logits, row + id[r]) : -INFINITY;
-          if (!(w[r] > -INFINITY)) id[r] = -1, dw[r] = 0.0f;   // an ineligible expert passes nothing
-          c = fmaxf(c, w[r]);
-        }
-        c = group_max_f32<LPT>(c);
-        if constexpr (SIGMOID) c = fminf(c, 0.0f);
-        c = fmaxf(c, -kFltMax);   // no eligible expert among the choices
-#pragma unroll
-        for (int r = 0; r < KR; ++r) {
-          w[r] = scaled_score<SIGMOID>(w[r], c);   // 0 for -inf
+          w[r] = comp[r] = 0.0f;
+          if (r * LPT >= p.topk) continue;   // uniform
+          const float zj = id[r] >= 0 ? gate_logit<BF16>(p.logits, row + id[r]) : -INFINITY;
+          if (!(zj > -INFINITY)) id[r] = -1, dw[r] = 0.0f;   // an ineligible expert passes nothing
+          c = fmaxf(c, zj);
+          if constexpr (SIGMOID) {
+            const Sigmoid q = sigmoid_parts(zj);
+            w[r] = q.s;
+            comp[r] = q.comp;
+          } else {
+            w[r] = __expf(zj - m);
+          }
           ws += w[r];
         }
         ws = group_sum_f32<LPT>(ws);
+        if (__ballot(ws < kLowChosen && c > -INFINITY) != 0) {   // wave-uniform, rare: as the forward
+          c = fmaxf(group_max_f32<LPT>(c), -kFltMax);
+          if constexpr (SIGMOID) c = fminf(c, 0.0f);
+          float scaled = 0.0f;
+#pragma unroll
+          for (int r = 0; r < KR; ++r) {
+            const float zj = id[r] >= 0 ? gate_logit<BF16>(p.logits, row + id[r]) : -INFINITY;
+            w[r] = ws < kLowChosen ? scaled_score<SIGMOID>(zj, c) : w[r];
+            scaled += w[r];
+          }
+          ws = group_sum_f32<LPT>(scaled);
+        }
 #pragma unroll
         for (int r = 0; r < KR; ++r) w[r] = ws > 0.0f ? __fdiv_rn(w[r], ws) : 0.0f;
         const float first = dominant<LPT>(w, dw);
@@ -845,13 +946,13 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
         }
         mean = group_sum_f32<LPT>(mean);
 #pragma unroll
-        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * w[r];
+        for (int r = 0; r < KR; ++r) dw[r] = (dw[r] - mean) * w[r] * (SIGMOID ? comp[r] : 1.0f);
       } else if constexpr (SIGMOID) {
 #pragma unroll
         for (int r = 0; r < KR; ++r)
           if (id[r] >= 0) {
             const float zj = gate_logit<BF16>(p.logits, row + id[r]);
-            dw[r] *= sigmoid_f32(zj);
+            dw[r] *= sigmoid_parts(zj).slope;
             if (!(zj > -INFINITY)) id[r] = -1;   // an ineligible expert passes nothing
           }
       }
@@ -893,16 +994,13 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       for (int v = 0; v < VPL; ++v) ds[v] += mine[expert_at<LPT, VEC>(l, v)];
       wave_lds_fence();
     };
-    const bool direct = !SIGMOID && p.renorm;   // the slots hold their part of dz
+    const bool direct = SIGMOID || p.renorm;   // the slots hold their part of dz
     if (p.dweights != nullptr && !direct) add_slots();
     if (!on) {   // whatever the loss's gradient holds
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = 0.0f;
     }
-    if constexpr (SIGMOID) {
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) ds[v] *= z[v];
-    } else {
+    if constexpr (!SIGMOID) {
       dot = 0.0f;
       if (__ballot(inv > 0.5f) != 0) {   // the largest softmax score is exp(0) inv; wave-uniform
         top = dominant<LPT>(s, ds);
@@ -914,13 +1012,19 @@ __global__ __launch_bounds__(256) void gate_bwd_kernel(GateBwd p) {
       dot = group_sum_f32<LPT>(dot);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) ds[v] = s[v] * (ds[v] - dot);
-      if (p.dweights != nullptr && direct) add_slots();
     }
+    if (p.dweights != nullptr && direct) add_slots();
     // A score of 0 times an overflowed gradient is no 0: the ineligible experts' are set (wave-uniform, rare).
     if (__ballot(on && !(fabsf(dot) <= kFltMax)) != 0) {
-      gate_load<LPT, VPL, BF16, VEC>(p.logits, row, p.E, l, on, z);
+#pragma unroll 1
+      for (int v = 0; v < VPL; ++v) {
+        const int e = expert_at<LPT, VEC>(l, v);
+        mine[e] = e < (on ? p.E : 0) ? gate_logit<BF16>(p.logits, row + e) : -INFINITY;
+      }
+      wave_lds_fence();
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) ds[v] = z[v] > -INFINITY ? ds[v] : 0.0f;
+      for (int v = 0; v < VPL; ++v) ds[v] = mine[expert_at<LPT, VEC>(l, v)] > -INFINITY ? ds[v] : 0.0f;
+      wave_lds_fence();
     }
     if (live) {
       const int64_t out = (int64_t)t * p.E;
