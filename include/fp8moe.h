@@ -718,7 +718,7 @@ int rmsnorm_quantize_mx(const void *x_bf16, const void *residual_bf16, const voi
  * for the gradient dh of its output (codes pass gradients straight through).
  *   dh      bf16 [rows][cols]
  *   s       bf16 [rows][cols], rstd f32 [rows]: as the forward wrote them (s = x
- *           without a residual)
+ *           without a residual, whose rows lie cols apart here)
  *   gamma   as in the forward
  *   dsum    bf16 [rows][cols]  gradient that reaches s past the norm (the residual
  *           stream's), or NULL

@@ -659,7 +659,8 @@ def rmsnorm_backward(dh, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, w
                      stream=None):
     """dh bf16 [R, C] (the gradient of h), s bf16 [R, C] and rstd f32 [R] from the forward (s = x without a residual),
     gamma as there, dsum bf16 [R, C] or None (the gradient that reaches the residual stream past the norm) ->
-    (dx bf16 [R, C], the gradient of x and of the residual, dgamma f32 [C] or None).  dx may be dh, s or dsum."""
+    (dx bf16 [R, C], the gradient of x and of the residual, dgamma f32 [C] or None).  dx may be dh, s or dsum.  dh, s and
+    dsum are contiguous: an x whose rows lie further apart is refused here, not copied."""
     fn = "rmsnorm_backward"
     dims = []
     for name, t in (("dh", dh), ("s", s), ("dsum", dsum)):

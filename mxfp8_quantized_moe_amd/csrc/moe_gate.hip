@@ -30,13 +30,19 @@
 // wave selects again in a second round over whole keys: the exact logit, or
 // score + bias formed in 64 bits, equal keys to the lower expert.
 //
-// Measured on the GPU, fp32 logits (copy rate 5.2 TB/s).  Choice, 65536 x 256 top 8: 20
-// us without and 23-26 us with a bias (71 MB: 14 us); bound by the vector ALU's issue,
-// busy 89% of the time (664 vector operations a wave of four tokens: about 260 for scores
-// and keys, 126 for the sorting network, 17 a choice).  A wave a token took 120 us,
-// looking for close choices once instead of after each choice 71 -> 47 us, the place in
-// the key 47 -> 41 us, a second round that takes a token at a time 41 -> 31 us.  With the loss 31 us + 9 us for its sums; 8192 x 64 top 6: 6.4 +
-// 5 us.  Backward, 65536 x 256: 30 us (140 MB: 27 us), bound by HBM; 8192 x 64: 5.7 us.
+// Measured on the GPU, fp32 logits, medians (copy rate 5.2 TB/s).  Choice, 65536 x 256 top
+// 8: 21 us without a bias, 25 us with one and sigmoid scores, 26-29 us with softmax scores
+// (71 MB: 14 us); bound by the vector ALU's issue, busy 87% of the time (661 vector
+// operations a wave of four tokens: about 260 for scores and keys, 126 for the sorting
+// network, 17 a choice).  A wave a token took 120 us, looking for close choices once
+// instead of after each choice 71 -> 47 us, the place in the key 47 -> 41 us, a second
+// round that takes a token at a time 41 -> 31 us.  With the loss 29 us (softmax) + 10 us
+// for its sums; 8192 x 64 top 6: 6.5 + 6 us.  Backward, 65536 x 256 (140 MB: 27 us): 28 us
+// softmax, bound by HBM, 32 us sigmoid (vector ALU 65% busy); 8192 x 64: 5.8 us.
+//
+// Where the second round takes every token the choice costs four times as much, and more:
+// constant logits 80 us (65536 x 256 top 8, no bias), a softmax row held by one expert under a bias
+// of zeros 108 us (the tolerance of close keys is absolute).
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "lane_groups.hpp"
@@ -1069,8 +1075,9 @@ static hipError_t gate_dispatch(int E, bool bf16, bool vec, bool sigmoid, F&& f)
     return vec ? scored(N{}, T{}) : scored(N{}, N{});
   };
   using std::integral_constant;
-  // The fewest lanes a token that hold its logits in at most 16 registers each: lane steps are shared by the
-  // wave's tokens (65536 x 256: a wave a token 120 us, 16 lanes 25 us).
+  // 16 lanes a token up to 256 experts, at most 16 logits a lane: lane steps are shared by the wave's tokens (65536 x 256:
+  // a wave a token 120 us, 16 lanes 25 us).  Four lanes where they hold the logits in four registers; more logits on four
+  // lanes, and 32 lanes for 257 to 512 experts, have not been measured.
   if (E <= 16) return types(integral_constant<int, 4>{}, integral_constant<int, 4>{});
   if (E <= 64) return types(integral_constant<int, 16>{}, integral_constant<int, 4>{});
   if (E <= 128) return types(integral_constant<int, 16>{}, integral_constant<int, 8>{});

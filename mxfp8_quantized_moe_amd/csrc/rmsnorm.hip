@@ -18,9 +18,9 @@
 // and s, h and the codes once.
 //
 // Bound by HBM: with a residual, h and codes 9 bytes an element.  Measured on the
-// GPU (a 1 GiB device copy moves 5.2 TB/s): 16384 x 5120 with MX codes 132-141 us =
-// 5.4-5.7 TB/s, 8192 x 4096 rowwise 50-52 us = 5.8-6.0 TB/s (part of its 302 MB stays in
-// the last-level cache between passes).  16 rows of 7168: 3.8 us, latency.
+// GPU, medians (a 1 GiB device copy moves 5.2 TB/s): 16384 x 5120 with MX codes 141 us =
+// 5.4 TB/s, 8192 x 4096 rowwise 52 us = 5.8 TB/s (part of its 302 MB stays in
+// the last-level cache between passes).  16 rows of 7168: 3.9 us, latency.
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "lane_groups.hpp"
@@ -312,10 +312,11 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
 // A workgroup walks rows with a stride of the grid and keeps its columns' share of
 // dgamma in registers (fp32); the shares go to the workspace, one row per
 // workgroup, and a second kernel adds them in a fixed order.  Bound by HBM: 8 bytes
-// an element with dsum.  512 workgroups: 16384 x 5120 takes 135 us (5.0 TB/s) + 5 us for
-// the shares; 1024 take 132 + 14, and where only 768 fit (8192 x 7168) 119 instead of
-// 97.  Loading dsum with the other rows instead of after the row's sum, and three
-// chunks a thread instead of four, brought both kernels together from 195 us to 141.
+// an element with dsum.  512 workgroups: 16384 x 5120 takes 137-143 us (medians of five
+// traces; 4.8 TB/s) + 5 us for the shares; 1024 take 132 + 14 where 512 took 135 + 5, and
+// where only 768 fit (8192 x 7168) 119 instead of 97.  Loading dsum with the other rows
+// instead of after the row's sum, and three chunks a thread instead of four, brought both
+// kernels together from 195 us to about 145.
 
 struct NormBwd {
   const uint16_t* dh;
