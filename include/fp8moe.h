@@ -80,6 +80,12 @@ extern "C" {
  * FP8-formátumának támogatása"; P4 "Тихая порча градиентов: проблема формата FNUZ".] */
 #define FP8MOE_E4M3FN 0
 #define FP8MOE_E4M3FNUZ 1
+/* Symmetric 8-bit integers: whole numbers in [-127, 127], two's complement, under the
+ * rowwise recipe with fmax 127 (q = the whole number nearest to clamp(fp32(x * s)), ties to
+ * even).  Taken by the rowwise quantizers of forward operands (quantize_rowwise,
+ * swiglu_quantize_rowwise, moe_permute_rowwise, moe_permute_quantized,
+ * rmsnorm_quantize_rowwise); their product is grouped_mm_scaled with FP8MOE_OPD_INT8. */
+#define FP8MOE_INT8 4
 
 /* MX shared-exponent rule X for a 1x32 block with |x| max `amax` (e8m0 code X+127):
  * FLOOR_OCP: X = floor(log2 amax) - 8 (OCP MX rule for e4m3; values above
@@ -110,6 +116,7 @@ extern "C" {
 #define FP8MOE_OPD_E4M3FN 0
 #define FP8MOE_OPD_E4M3FNUZ 1
 #define FP8MOE_OPD_BF16 2
+#define FP8MOE_OPD_INT8 4          /* signed 8-bit integers */
 
 /* scale kinds */
 #define FP8MOE_SCALE_F32 0         /* fp32 multipliers (divide in the epilogue) */
@@ -659,9 +666,13 @@ int64_t quantize_mx_rows_bound(int64_t rows, int32_t n_groups);
  *     SCALE_NONE with OPD_BF16 operands: a bf16 [M][N], b bf16 [M][K] (token-major).
  *   offs may be NULL only when n_groups == 1 (one group of all M rows).
  *   Formats: both operands FP8 (e4m3fn or e4m3fnuz, mixed allowed; e8m0 scales
- *   need e4m3fn) or both BF16 (GROUPED_K with SCALE_NONE only).
- *   Accumulation is fp32; out is bf16 (round to nearest even) or fp32.
- *   Requires: M, N, K >= 0; FP8 operands: K % 16 == 0 and K <= 2^23 (GROUPED_M) or
+ *   need e4m3fn), both BF16 (GROUPED_K with SCALE_NONE only) or both INT8
+ *   (GROUPED_M with SCALE_F32 only: a scale for each token and each weight
+ *   channel; K <= 131071, for which no sum of products leaves 32 bits, else
+ *   FP8MOE_ERR_UNSUPPORTED; any byte is a valid code).
+ *   Accumulation is fp32 (INT8: exact 32-bit integers, then one fp32 rounding
+ *   and the two scales' reciprocals); out is bf16 (round to nearest even) or fp32.
+ *   Requires: M, N, K >= 0; FP8 and INT8 operands: K % 16 == 0 and K <= 2^23 (GROUPED_M) or
  *   M % 16 == 0 and M <= 2^23 (GROUPED_K); BF16 operands: M, N, K % 8 == 0;
  *   all pointers 16-byte aligned.
  */

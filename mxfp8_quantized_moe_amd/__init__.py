@@ -13,15 +13,15 @@ import contextlib
 import torch
 
 from . import _lib
-from ._lib import (E4M3FN, E4M3FNUZ, MX_FLOOR_OCP, MX_CEIL, MX_LAYOUT_ROWS, MX_LAYOUT_K4, GROUPED_M, GROUPED_K,
-                   OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16, SCALE_F32, SCALE_E8M0, SCALE_NONE, SCALE_E8M0_K4,
+from ._lib import (E4M3FN, E4M3FNUZ, INT8, MX_FLOOR_OCP, MX_CEIL, MX_LAYOUT_ROWS, MX_LAYOUT_K4, GROUPED_M, GROUPED_K,
+                   OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16, OPD_INT8, SCALE_F32, SCALE_E8M0, SCALE_NONE, SCALE_E8M0_K4,
                    OUT_BF16, OUT_F32, GATE_SOFTMAX, GATE_SIGMOID,
                    Fp8MoeError)
 
 __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_rows_bound",
-           "grouped_mm_scaled", "encode_f32", "default_codec", "E4M3FN", "E4M3FNUZ", "MX_FLOOR_OCP",
+           "grouped_mm_scaled", "encode_f32", "default_codec", "E4M3FN", "E4M3FNUZ", "INT8", "MX_FLOOR_OCP",
            "MX_CEIL", "MX_LAYOUT_ROWS", "MX_LAYOUT_K4", "GROUPED_M", "GROUPED_K", "OPD_E4M3FN", "OPD_E4M3FNUZ",
-           "OPD_BF16", "SCALE_F32", "SCALE_E8M0", "SCALE_NONE", "SCALE_E8M0_K4", "OUT_BF16", "OUT_F32",
+           "OPD_BF16", "OPD_INT8", "SCALE_F32", "SCALE_E8M0", "SCALE_NONE", "SCALE_E8M0_K4", "OUT_BF16", "OUT_F32",
            "mx_k4_shape", "quantize_mx_dual", "swiglu_quantize_mx_dual", "swiglu_backward_quantize_mx_dual",
            "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise",
            "Fp8MoeError", "swiglu_quantize_rowwise",
@@ -52,14 +52,19 @@ def _bits(x: torch.Tensor) -> torch.Tensor:
     raise TypeError(f"expected bf16 (or its 16-bit pattern), got {x.dtype}")
 
 
+def _codes(codec):
+    """The dtype of a codec's codes."""
+    return torch.int8 if codec == INT8 else torch.uint8
+
+
 def quantize_rowwise(x, codec=E4M3FN, q=None, scale=None, stream=None):
-    """x [R, C] bf16 (row stride may exceed C) -> (q uint8 [R, C], scale f32 [R])."""
+    """x [R, C] bf16 (row stride may exceed C) -> (q uint8 [R, C], scale f32 [R]); codec=INT8 gives int8 codes."""
     x = _bits(x)
     R, C = x.shape
     if x.numel() and x.stride(1) != 1:
         raise ValueError("quantize_rowwise needs unit stride along the last dim")
     ld_x = x.stride(0) if x.numel() else C
-    q = torch.empty((R, C), dtype=torch.uint8, device=x.device) if q is None else q
+    q = torch.empty((R, C), dtype=_codes(codec), device=x.device) if q is None else q
     scale = torch.empty((R,), dtype=torch.float32, device=x.device) if scale is None else scale
     _lib.check("quantize_rowwise", _lib.lib().quantize_rowwise(
         _ptr(x), R, C, ld_x, codec, _ptr(q), _ptr(scale), _stream(stream)))
@@ -294,7 +299,7 @@ def swiglu_quantize_rowwise(h1, codec=E4M3FN, a2=None, q=None, scale=None, strea
     ld = h1.stride(0) if h1.numel() else F2
     a2 = torch.empty((R, F), dtype=torch.bfloat16, device=h1.device) if a2 is None else a2
     if codes:
-        q = torch.empty((R, F), dtype=torch.uint8, device=h1.device) if q is None else q
+        q = torch.empty((R, F), dtype=_codes(codec), device=h1.device) if q is None else q
         scale = torch.empty((R,), dtype=torch.float32, device=h1.device) if scale is None else scale
     else:
         q = scale = None
@@ -456,7 +461,7 @@ def moe_permute_quantized(q, scale, src, topk, codec=E4M3FN, qg=None, scale_g=No
     q = q.contiguous()
     T, C = q.shape
     R = src.numel()
-    qg = torch.empty((R, C), dtype=torch.uint8, device=q.device) if qg is None else qg
+    qg = torch.empty((R, C), dtype=_codes(codec), device=q.device) if qg is None else qg
     scale_g = torch.empty((R,), dtype=torch.float32, device=q.device) if scale_g is None else scale_g
     _lib.check("moe_permute_quantized", _lib.lib().moe_permute_quantized(
         _ptr(q), _ptr(scale), T, C, topk, _ptr(src), R, codec, _ptr(qg), _ptr(scale_g), _stream(stream)))
@@ -490,7 +495,7 @@ def moe_permute_rowwise(x, src, topk, codec=E4M3FN, xg=None, qg=None, scale_g=No
         xg = torch.empty((R, C), dtype=x.dtype, device=x.device) if xg is None else xg
     else:
         xg = None
-    qg = torch.empty((R, C), dtype=torch.uint8, device=x.device) if qg is None else qg
+    qg = torch.empty((R, C), dtype=_codes(codec), device=x.device) if qg is None else qg
     scale_g = torch.empty((R,), dtype=torch.float32, device=x.device) if scale_g is None else scale_g
     _lib.check("moe_permute_rowwise", _lib.lib().moe_permute_rowwise(
         _ptr(x), T, C, topk, _ptr(src), R, codec, _ptr(xg), _ptr(qg), _ptr(scale_g), _stream(stream)))
@@ -613,7 +618,7 @@ def rmsnorm_quantize_rowwise(x, gamma=None, eps=1e-6, residual=None, codec=E4M3F
                              sum_out=None, h=None, q=None, scale=None, rstd=None, stream=None):
     """x bf16 [R, C] (row stride may exceed C), gamma bf16 or f32 [C] or None, residual bf16 [R, C] or None ->
     (h bf16 [R, C] or None, q u8 [R, C] or None, scale f32 [R] or None, rstd f32 [R], sum bf16 [R, C]): the residual's
-    addition, the RMS norm and the rowwise FP8 quantization of the normed rows (from fp32) in one pass.  sum is
+    addition, the RMS norm and the rowwise FP8 quantization of the normed rows (from fp32; int8 codes with codec=INT8) in one pass.  sum is
     x + residual, the new residual stream (x itself without a residual); sum_out may be x or residual (contiguous).
     keep_bf16=False skips h, codes=False skips q and scale."""
     fn = "rmsnorm_quantize_rowwise"
@@ -622,7 +627,7 @@ def rmsnorm_quantize_rowwise(x, gamma=None, eps=1e-6, residual=None, codec=E4M3F
         dev = x.device
         s = _out(fn, "sum_out", sum_out, (R, C), torch.bfloat16, dev) if residual is not None else x
         h = _out(fn, "h", h, (R, C), torch.bfloat16, dev) if keep_bf16 else None
-        q = _out(fn, "q", q, (R, C), torch.uint8, dev) if codes else None
+        q = _out(fn, "q", q, (R, C), _codes(codec), dev) if codes else None
         scale = _out(fn, "scale", scale, (R,), torch.float32, dev) if codes else None
         rstd = _out(fn, "rstd", rstd, (R,), torch.float32, dev)
         _lib.check(fn, _lib.lib().rmsnorm_quantize_rowwise(

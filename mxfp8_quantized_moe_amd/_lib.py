@@ -12,11 +12,11 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8moe.s
 
 # status codes and enums (mirror include/fp8moe.h)
 OK, ERR_NULL, ERR_SHAPE, ERR_ENUM, ERR_ALIGN, ERR_UNSUPPORTED, ERR_LAUNCH, ERR_DEVICE, ERR_SCRATCH, ERR_VALUE = range(10)
-E4M3FN, E4M3FNUZ = 0, 1
+E4M3FN, E4M3FNUZ, INT8 = 0, 1, 4
 MX_FLOOR_OCP, MX_CEIL = 0, 1
 MX_LAYOUT_ROWS, MX_LAYOUT_K4 = 0, 1
 GROUPED_M, GROUPED_K = 0, 1
-OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16 = 0, 1, 2
+OPD_E4M3FN, OPD_E4M3FNUZ, OPD_BF16, OPD_INT8 = 0, 1, 2, 4
 SCALE_F32, SCALE_E8M0, SCALE_NONE, SCALE_E8M0_K4 = 0, 1, 2, 3
 OUT_BF16, OUT_F32 = 0, 1
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1

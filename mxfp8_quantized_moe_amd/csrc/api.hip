@@ -294,7 +294,8 @@ int rmsnorm_quantize_rowwise(const void* x_bf16, const void* residual_bf16, cons
   if (!st) st = check_rmsnorm_in_place(x_bf16, residual_bf16, rows, cols, ld_x, ld_residual, sum_bf16);
   if (st) return st;
   const NormArgs a{static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16), gamma,
-                   gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps, q ? codec : 4, 0,
+                   gamma_dtype == FP8MOE_OUT_BF16, rows, cols, ld_x, ld_residual, eps,
+                   !q ? 4 : codec == FP8MOE_INT8 ? 5 : codec, 0,
                    static_cast<uint16_t*>(sum_bf16), static_cast<uint16_t*>(h_bf16), static_cast<uint8_t*>(q), scale,
                    nullptr, rstd};
   return launch_status(launch_rmsnorm_quantize(a, as_stream(stream)));

@@ -11,8 +11,10 @@ namespace fp8moe {
 // ------------------------------------------------------------------ constants
 
 // Largest finite magnitudes: e4m3fnuz 240 (the pages' e4m3fnuz property table),
-// e4m3fn 448 (OCP 8-bit float).  [P1 Details; P4 "Тихая порча градиентов".]
-__host__ __device__ constexpr float fmax_of(int codec) { return codec == 0 ? 448.0f : 240.0f; }
+// e4m3fn 448 (OCP 8-bit float), and 127 for the symmetric 8-bit integers.  [P1
+// Details; P4 "Тихая порча градиентов".]
+constexpr int kInt8 = 4;   // FP8MOE_INT8
+__host__ __device__ constexpr float fmax_of(int codec) { return codec == 0 ? 448.0f : codec == kInt8 ? 127.0f : 240.0f; }
 
 // Floor under the absolute maximum before the division, so an all-zero or
 // empty reduction set still gets a finite scale (fmax / 1e-12).
@@ -171,13 +173,25 @@ __device__ __forceinline__ float scale_clamp(float x, float s) {
   return __builtin_amdgcn_fmed3f(__fmul_rn(x, s), -fm, fm);
 }
 
-// Four values -> four FP8 codes packed little-endian in a u32.
+// Four values already clamped to [-127, 127] -> four int8 codes packed little-endian in a u32, ties to even.
+// Adding 1.5 * 2^23 (unit in the last place 1) rounds to a whole number whose two's complement stands in the low
+// bits of the sum's pattern: one addition a value and three byte permutes for four of them.
+__device__ __forceinline__ uint32_t enc_int8x4(float a, float b, float c, float d) {
+  constexpr float kRound = 12582912.0f;
+  const uint32_t ab = __builtin_amdgcn_perm(__float_as_uint(b + kRound), __float_as_uint(a + kRound), 0x0C0C0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(__float_as_uint(d + kRound), __float_as_uint(c + kRound), 0x0C0C0400u);
+  return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+}
+
+// Four values -> four 8-bit codes packed little-endian in a u32.
 template <int CODEC>
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float s) {
   const float ya = scale_clamp<CODEC>(a, s), yb = scale_clamp<CODEC>(b, s);
   const float yc = scale_clamp<CODEC>(c, s), yd = scale_clamp<CODEC>(d, s);
   if constexpr (CODEC == 0) {
     return cvt_fn_pair<true>(yc, yd, cvt_fn_pair<false>(ya, yb, 0u));
+  } else if constexpr (CODEC == kInt8) {
+    return enc_int8x4(ya, yb, yc, yd);
   } else {
     return enc_fp8<1>(ya) | (enc_fp8<1>(yb) << 8) | (enc_fp8<1>(yc) << 16) | (enc_fp8<1>(yd) << 24);
   }

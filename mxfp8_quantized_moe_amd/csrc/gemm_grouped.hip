@@ -51,7 +51,9 @@
 namespace fp8moe {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v16i __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -537,9 +539,16 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
   return reinterpret_cast<T*>(uniform_i64(reinterpret_cast<int64_t>(p)));
 }
 
-template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT>
+// I8: the operands are signed 8-bit integers.  A 64-byte k step is then two
+// v_mfma_i32_32x32x32_i8 (each lane half takes the 16-byte half of its fragment
+// registers that the FP8 instruction takes too; both operands permute the
+// contraction alike), which together take the FP8 instruction's cycles; sums are
+// exact 32-bit integers, turned to fp32 in the epilogue.
+template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT, bool I8 = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_pipe(KParams p) {
+  static_assert(!I8 || SK == 0, "integer operands: fp32 scales");
+  using Acc = std::conditional_t<I8, v16i, v16f>;
   using R = PipeRing<BK>;
   constexpr int CH = R::CH, KS = BK / 64;
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
@@ -951,7 +960,7 @@ void gemm_fp8_pipe(KParams p) {
   constexpr bool HALF = LAY > 0;
   constexpr int TME = LAY == 2 ? TM / 2 : TM;                          // 32-row blocks per wave
   constexpr int TNE = HALF ? TN / 2 : TN, WNE = HALF ? WN / 2 : WN;   // column blocks and columns per wave
-  constexpr int NME = TME * TNE, NDE = 2 * (TME + TNE), ND0E = NDE + (E8 ? TME + TNE : 0);
+  constexpr int NME = TME * TNE * (I8 ? 2 : 1), NDE = 2 * (TME + TNE), ND0E = NDE + (E8 ? TME + TNE : 0);
   // Thread indices pass through an opaque copy each tile, so the compiler
   // derives per-lane addresses inside the tile instead of hoisting (and
   // spilling) all of them across the tile loop.
@@ -978,13 +987,13 @@ void gemm_fp8_pipe(KParams p) {
     raw_barrier();
   };
 
-  v16f acc[TME][TNE];
+  Acc acc[TME][TNE];
 #pragma unroll
   for (int i = 0; i < TME; ++i)
 #pragma unroll
     for (int j = 0; j < TNE; ++j)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
 
   const int g = lane >> 5, lrow = lane & 31;
   // Two register sets of MFMA fragments (one 64-byte k step each).
@@ -1064,7 +1073,14 @@ void gemm_fp8_pipe(KParams p) {
         if constexpr (E8)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[SET][j], fa[SET][i], acc[i][j], 0, 0, j,
                                                                       eb[SET], i, ea[SET]);
-        else
+        else if constexpr (I8) {
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              __builtin_shufflevector(fb[SET][j], fb[SET][j], 0, 1, 2, 3),
+              __builtin_shufflevector(fa[SET][i], fa[SET][i], 0, 1, 2, 3), acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              __builtin_shufflevector(fb[SET][j], fb[SET][j], 4, 5, 6, 7),
+              __builtin_shufflevector(fa[SET][i], fa[SET][i], 4, 5, 6, 7), acc[i][j], 0, 0, 0);
+        } else
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[SET][j], fa[SET][i], acc[i][j], 0, 0, 0, 0,
                                                                       0, 0);
       });
@@ -1305,7 +1321,7 @@ void gemm_fp8_pipe(KParams p) {
             // range leaves the zero accumulators untouched
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              v[e] = SK == 0 ? acc[i][JPP * jp + jj][4 * q + e] * inv_p[i] * inv_q[jj][q][e]
+              v[e] = SK == 0 ? (float)acc[i][JPP * jp + jj][4 * q + e] * inv_p[i] * inv_q[jj][q][e]
                              : acc[i][JPP * jp + jj][4 * q + e];
             const int u = 8 * jj + 2 * q + g;
             if constexpr (OUT == 0) {
@@ -1352,7 +1368,7 @@ void gemm_fp8_pipe(KParams p) {
     auto quad = [&](int i, int j, int q, float inv_p, const float* inv_q) {
       f32x4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * inv_p * inv_q[4 * q + e];
+      for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e] * inv_p * inv_q[4 * q + e];
       return v;
     };
 #pragma unroll
@@ -1463,7 +1479,7 @@ static int cu_count() {
   return cached[dev];
 }
 
-template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT>
+template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT, bool I8 = false>
 static hipError_t launch_pipe(const GemmArgs& g, hipStream_t st) {
   KParams p;
   fill_params(p, g, BM, BN);
@@ -1472,7 +1488,7 @@ static hipError_t launch_pipe(const GemmArgs& g, hipStream_t st) {
   if (!band_magic_exact(p)) return hipErrorInvalidValue;   // far beyond any expert layer
   // One workgroup fits per CU (LDS); a persistent grid of at most one per CU.
   const int64_t grid = std::min<int64_t>(total, cu_count());
-  hipLaunchKernelGGL((gemm_fp8_pipe<BM, BN, BK, SLOTS, MODE, SK, OUT>), dim3((unsigned)grid), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((gemm_fp8_pipe<BM, BN, BK, SLOTS, MODE, SK, OUT, I8>), dim3((unsigned)grid), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
@@ -1532,9 +1548,20 @@ static hipError_t dispatch_fp8(const GemmArgs& g, hipStream_t st) {
   return g.out_dtype == 0 ? pick_tile<MODE, 0, 0>(g, st) : pick_tile<MODE, 0, 1>(g, st);
 }
 
+// Integer operands (GROUPED_M): the FP8 tiles, chosen alike.
+template <int OUT>
+static hipError_t dispatch_i8(const GemmArgs& g, hipStream_t st) {
+  return g.n_groups > 1 && g.M / g.n_groups < 512 ? launch_pipe<128, 256, 128, 3, 0, 0, OUT, true>(g, st)
+                                                  : launch_pipe<256, 256, 128, 2, 0, 0, OUT, true>(g, st);
+}
+
 hipError_t launch_grouped_mm_bf16(const GemmArgs& g, hipStream_t st);
 
 hipError_t launch_grouped_mm(const GemmArgs& g, hipStream_t st) {
+  if (g.a_fmt == kInt8) {
+    if (g.M == 0) return hipSuccess;
+    return g.out_dtype == 0 ? dispatch_i8<0>(g, st) : dispatch_i8<1>(g, st);
+  }
   const bool fn = g.a_fmt == 0 && g.b_fmt == 0;
   if (g.a_fmt == 2 || !fn) return launch_grouped_mm_bf16(g, st);
   if (g.M == 0 && g.mode == 0) return hipSuccess;

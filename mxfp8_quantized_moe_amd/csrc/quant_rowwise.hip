@@ -160,6 +160,7 @@ hipError_t launch_quantize_rowwise(const uint16_t* x, int64_t rows, int64_t cols
                                    uint8_t* q, float* scale, hipStream_t st) {
   if (rows == 0) return hipSuccess;
   const RowGather none{nullptr, 1, 0, nullptr};
+  if (codec == kInt8) return dispatch_rw<kInt8, false>(x, rows, cols, ld_x, q, scale, none, st);
   return codec == 0 ? dispatch_rw<0, false>(x, rows, cols, ld_x, q, scale, none, st)
                     : dispatch_rw<1, false>(x, rows, cols, ld_x, q, scale, none, st);
 }
@@ -169,6 +170,7 @@ hipError_t launch_moe_permute_rowwise(const uint16_t* x, int64_t tokens, int64_t
                                       hipStream_t st) {
   if (rows_out == 0) return hipSuccess;
   const RowGather gt{src, topk, tokens * topk, xg};
+  if (codec == kInt8) return dispatch_rw<kInt8, true>(x, rows_out, cols, cols, qg, scale_g, gt, st);
   return codec == 0 ? dispatch_rw<0, true>(x, rows_out, cols, cols, qg, scale_g, gt, st)
                     : dispatch_rw<1, true>(x, rows_out, cols, cols, qg, scale_g, gt, st);
 }

@@ -95,11 +95,11 @@ __device__ __forceinline__ uint32_t quant4_fnuz(float a, float b, float c, float
   return mag | (w & (mag + 0x7F7F7F7Fu) & 0x80808080u);   // the sign where the magnitude is not 0
 }
 
-// FMT 0: rowwise e4m3fn, 1: rowwise e4m3fnuz, 2: MX floor rule, 3: MX ceil rule, 4: no codes.
+// FMT 0: rowwise e4m3fn, 1: rowwise e4m3fnuz, 2: MX floor rule, 3: MX ceil rule, 4: no codes, 5: rowwise int8.
 template <int TPR, int ITEMS, int FMT, int GT>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd p) {
   constexpr int NT = TPR > 256 ? TPR : 256, RPB = NT / TPR, WAVES = TPR / 64;
-  constexpr bool MX = FMT == 2 || FMT == 3, ROWWISE = FMT < 2;
+  constexpr bool MX = FMT == 2 || FMT == 3, ROWWISE = FMT < 2 || FMT == 5;
   __shared__ float red_s[TPR > 64 ? WAVES : 1];
   __shared__ uint32_t red_m[TPR > 64 ? WAVES : 1];
   const int lt = threadIdx.x % TPR;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
   }
   const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ss * p.inv_c + p.eps));
   float scale = 0.0f;
-  if constexpr (ROWWISE) scale = scale_from_amax(__uint_as_float(mb) * rstd, FMT);
+  if constexpr (ROWWISE) scale = scale_from_amax(__uint_as_float(mb) * rstd, FMT == 5 ? kInt8 : FMT);
   if (valid && lt == 0) {
     if (p.rstd != nullptr) p.rstd[row] = rstd;
     if constexpr (ROWWISE) p.scale[row] = scale;
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rmsnorm_kernel(NormFwd 
     if (in && p.h != nullptr) reinterpret_cast<u32x4*>(p.h + r * cols)[c] = pack8(a);
     if constexpr (ROWWISE) {
       auto four = [&](int k) {
-        if constexpr (FMT == 0) return quant4<0>(a[k], a[k + 1], a[k + 2], a[k + 3], scale);
+        if constexpr (FMT != 1) return quant4<FMT == 5 ? kInt8 : 0>(a[k], a[k + 1], a[k + 2], a[k + 3], scale);
         else return quant4_fnuz(a[k], a[k + 1], a[k + 2], a[k + 3], scale);
       };
       if (in) reinterpret_cast<u32x2*>(p.q + r * cols)[c] = u32x2{four(0), four(4)};
@@ -298,6 +298,7 @@ hipError_t launch_rmsnorm_quantize(const NormArgs& a, hipStream_t st) {
       case 1: e = launch_fwd<1>(p, gt, st); break;
       case 2: e = launch_fwd<2>(p, gt, st); break;
       case 3: e = launch_fwd<3>(p, gt, st); break;
+      case 5: e = launch_fwd<5>(p, gt, st); break;
       default: e = launch_fwd<4>(p, gt, st); break;
     }
     if (e != hipSuccess) return e;

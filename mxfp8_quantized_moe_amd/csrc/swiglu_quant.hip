@@ -225,6 +225,7 @@ static hipError_t sw_bwd(const uint16_t* da2, const uint16_t* h1, int64_t rows, 
 hipError_t launch_swiglu_quantize_rowwise(const uint16_t* h1, int64_t rows, int64_t F, int64_t ld_h1, int codec,
                                           uint16_t* a2, uint8_t* q, float* scale, hipStream_t st) {
   if (rows == 0 || F == 0) return hipSuccess;
+  if (codec == kInt8) return sw_fwd<kInt8>(h1, rows, F, ld_h1, a2, q, scale, st);
   return codec == 0 ? sw_fwd<0>(h1, rows, F, ld_h1, a2, q, scale, st)
                     : sw_fwd<1>(h1, rows, F, ld_h1, a2, q, scale, st);
 }

@@ -11,6 +11,7 @@ namespace fp8moe {
 namespace {
 
 constexpr int64_t kI32Max = 2147483647;
+constexpr int64_t kInt8MaxK = 131071;   // 131071 * 128 * 128 < 2^31
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool need(const void* p, int64_t elems) { return elems == 0 || p != nullptr; }
@@ -22,6 +23,9 @@ int64_t mul(int64_t a, int64_t b) {
   return a * b;
 }
 
+// Codecs of the rowwise forward operands (the integers' product has no other scaling).
+bool rowwise_codec(int codec) { return codec == FP8MOE_E4M3FN || codec == FP8MOE_E4M3FNUZ || codec == FP8MOE_INT8; }
+
 }  // namespace
 
 int64_t mx_rows_bound(int64_t rows, int32_t n_groups) {
@@ -31,7 +35,7 @@ int64_t mx_rows_bound(int64_t rows, int32_t n_groups) {
 
 int check_quantize_rowwise(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int codec, const void* q,
                            const void* scale) {
-  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (!rowwise_codec(codec)) return FP8MOE_ERR_ENUM;
   if (rows < 0 || cols < 0 || ld_x < cols || rows > kI32Max * 256LL || cols > kI32Max) return FP8MOE_ERR_SHAPE;
   const int64_t n = mul(rows, cols);
   if (n < 0 || mul(rows, ld_x) < 0) return FP8MOE_ERR_SHAPE;
@@ -171,7 +175,8 @@ int check_grouped_mm(int mode, const void* a, int a_fmt, const void* sa, const v
                      const void* sb, int scale_kind, const int32_t* offs, int32_t n_groups, int64_t M,
                      int64_t N, int64_t K, const void* out, int out_dtype) {
   if (mode != FP8MOE_GROUPED_M && mode != FP8MOE_GROUPED_K) return FP8MOE_ERR_ENUM;
-  if (a_fmt < 0 || a_fmt > 2 || b_fmt < 0 || b_fmt > 2) return FP8MOE_ERR_ENUM;
+  const bool a_i8 = a_fmt == FP8MOE_OPD_INT8, b_i8 = b_fmt == FP8MOE_OPD_INT8;
+  if (a_fmt < 0 || (a_fmt > 2 && !a_i8) || b_fmt < 0 || (b_fmt > 2 && !b_i8)) return FP8MOE_ERR_ENUM;
   if (scale_kind < 0 || scale_kind > 3) return FP8MOE_ERR_ENUM;
   if (out_dtype != FP8MOE_OUT_BF16 && out_dtype != FP8MOE_OUT_F32) return FP8MOE_ERR_ENUM;
   if (M < 0 || N < 0 || K < 0 || n_groups < 1 || n_groups > (1 << 20)) return FP8MOE_ERR_SHAPE;
@@ -181,6 +186,8 @@ int check_grouped_mm(int mode, const void* a, int a_fmt, const void* sa, const v
   if (a_bf16 != b_bf16) return FP8MOE_ERR_UNSUPPORTED;
   if (a_bf16 && (scale_kind != FP8MOE_SCALE_NONE || mode != FP8MOE_GROUPED_K)) return FP8MOE_ERR_UNSUPPORTED;
   if (!a_bf16 && scale_kind == FP8MOE_SCALE_NONE) return FP8MOE_ERR_UNSUPPORTED;
+  if (a_i8 != b_i8 || (a_i8 && (mode != FP8MOE_GROUPED_M || scale_kind != FP8MOE_SCALE_F32))) return FP8MOE_ERR_UNSUPPORTED;
+  if (a_i8 && K > kInt8MaxK) return FP8MOE_ERR_UNSUPPORTED;   // the largest sum that stays in 32 bits
   const bool e8 = scale_kind == FP8MOE_SCALE_E8M0, k4 = scale_kind == FP8MOE_SCALE_E8M0_K4;
   if ((e8 || k4) && (a_fmt != FP8MOE_OPD_E4M3FN || b_fmt != FP8MOE_OPD_E4M3FN)) return FP8MOE_ERR_UNSUPPORTED;
   const int64_t E = n_groups;
@@ -216,7 +223,7 @@ int check_grouped_mm(int mode, const void* a, int a_fmt, const void* sa, const v
 
 int check_swiglu(const void* h1, int64_t rows, int64_t F, int64_t ld_h1, int codec, const void* out_bf16,
                  const void* q, const void* scale, const void* da2, bool backward) {
-  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (!rowwise_codec(codec) || (backward && codec == FP8MOE_INT8)) return FP8MOE_ERR_ENUM;
   if (rows < 0 || F < 0 || rows > kI32Max * 256LL || F > kI32Max / 2 || ld_h1 < 2 * F) return FP8MOE_ERR_SHAPE;
   const int64_t n = mul(rows, 2 * F);
   if (n < 0 || mul(rows, ld_h1) < 0) return FP8MOE_ERR_SHAPE;
@@ -361,7 +368,7 @@ int check_moe_permute(const void* x, int64_t tokens, int64_t cols, int32_t topk,
 int check_moe_permute_quantized(const void* q, const float* scale, int64_t tokens, int64_t cols, int32_t topk,
                                 const int32_t* src, int64_t rows_out, int codec, const void* qg,
                                 const float* scale_g) {
-  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (!rowwise_codec(codec)) return FP8MOE_ERR_ENUM;
   if (tokens < 0 || cols < 0 || topk < 1 || rows_out < 0 || rows_out > kI32Max) return FP8MOE_ERR_SHAPE;
   const int64_t S = mul(tokens, topk), nq = mul(tokens, cols), ng = mul(rows_out, cols);
   if (S < 0 || S > kI32Max || nq < 0 || ng < 0) return FP8MOE_ERR_SHAPE;
@@ -387,7 +394,7 @@ int check_moe_combine(const void* yg, int64_t rows_in, const int32_t* dest, cons
 
 int check_moe_permute_rowwise(const void* x, int64_t tokens, int64_t cols, int32_t topk, const int32_t* src,
                               int64_t rows_out, int codec, const void* xg, const void* qg, const float* scale_g) {
-  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (!rowwise_codec(codec)) return FP8MOE_ERR_ENUM;
   if (tokens < 0 || cols < 0 || topk < 1 || rows_out < 0 || rows_out > kI32Max * 256LL || cols > kI32Max)
     return FP8MOE_ERR_SHAPE;
   const int64_t S = mul(tokens, topk), nx = mul(tokens, cols), ng = mul(rows_out, cols);
@@ -442,7 +449,7 @@ int check_rmsnorm_in_place(const void* x, const void* res, int64_t rows, int64_t
 
 int check_rmsnorm_rowwise(int codec, const void* q, const void* scale) {
   (void)q;
-  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (!rowwise_codec(codec)) return FP8MOE_ERR_ENUM;
   return aligned(scale, 4) ? FP8MOE_OK : FP8MOE_ERR_ALIGN;
 }
 
