@@ -846,6 +846,48 @@ int moe_gate_backward(const void *logits, int logit_dtype, int64_t tokens, int32
                       const float *dprob, const float *dloss, void *dlogits, void *stream);
 
 /*
+ * moe_few_tokens -- the whole expert block (gather, W1, SwiGLU, W2, weighted sum) for
+ * a few tokens, as a decoding step meets it: every used expert's 8-bit weights are
+ * read once, and the activations stay in bf16.
+ *   [P4 "MoE" (routed experts between two products, their outputs summed per token
+ *   with the router's weights); P1 Details, MoE paragraph (the experts' quantized
+ *   weights); the form for single tokens is this library's.]
+ *   For each token t and each expert e that ids[t] names, with w = the sum of its
+ *   weights of those slots: [g | u] = x[t] W1[e]^T, a = bf16(silu(g) * u),
+ *   y[t] = bf16(sum over e of w * (a W2[e]^T)); sums in fp32 in a fixed order.
+ *   x         bf16 [tokens][ld_x]   (the first K of each row are read)
+ *   ids       int32 [tokens][topk]  an id outside [0, n_experts) adds nothing (as
+ *             moe_gate's -1); an expert may be named twice
+ *   weights   f32 [tokens][topk]
+ *   w1        [n_experts][2F][K]    gate rows [0, F), up rows [F, 2F) of each expert
+ *   w2        [n_experts][K][F]
+ *   w_fmt, scale_kind  OPD_E4M3FN with SCALE_F32, SCALE_E8M0 or SCALE_E8M0_K4, or
+ *             OPD_INT8 with SCALE_F32; others: FP8MOE_ERR_UNSUPPORTED
+ *   w1_scale, w2_scale  SCALE_F32: f32 [n_experts][2F] and [n_experts][K] (what
+ *             quantize_rowwise gives for the rows); SCALE_E8M0(_K4): e8m0 of the
+ *             n_experts*2F and n_experts*K rows, as quantize_mx with axis 1 lays them out
+ *             (a scaled weight below 2^-126 counts as 0 or to bf16's spacing there)
+ *   y         bf16 [tokens][K]      zeros for a token without an expert (written).  It
+ *             may be x itself where ld_x is K
+ *   workspace device memory of moe_few_tokens_workspace_bytes(tokens, topk, F) bytes,
+ *             16-byte aligned, owned by the caller; contents on entry do not matter.
+ *             Calls that may overlap (other streams, graphs replayed side by side) need
+ *             one each
+ *   Requires: tokens <= 64, tokens*topk <= 1024, n_experts <= 1024 (else
+ *   FP8MOE_ERR_UNSUPPORTED: more tokens take moe_route and the grouped GEMMs);
+ *   K % 16 == 0 and F % 16 == 0 (e8m0 scales: 32); ld_x >= K, ld_x % 8 == 0; x, w1, w2,
+ *   y 16-byte aligned, the int32 and f32 arrays 4-byte aligned.  Two kernels, no
+ *   allocation.
+ */
+int moe_few_tokens(const void *x_bf16, int64_t tokens, int64_t K, int64_t ld_x, const int32_t *ids,
+                   const float *weights, int32_t topk, const void *w1, const void *w1_scale, const void *w2,
+                   const void *w2_scale, int w_fmt, int scale_kind, int32_t n_experts, int64_t F, void *y_bf16,
+                   void *workspace, void *stream);
+
+/* Workspace bytes moe_few_tokens needs (-1: invalid sizes). */
+int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t F);
+
+/*
  * fp8moe_encode_f32 -- the device FP8 encoder alone: q[i] = enc(y[i]) for
  * values already inside [-fmax, fmax] (round to nearest, ties to the even
  * code; e4m3fn keeps the sign of zero, e4m3fnuz has one unsigned zero).  The

@@ -31,7 +31,7 @@ __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "quantize_blockwise_tokens", "grouped_mm_blockwise_k",
            "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
            "GATE_SOFTMAX", "GATE_SIGMOID", "moe_gate", "moe_gate_balance", "moe_gate_backward", "moe_balance_loss",
-           "moe_balance_loss_backward", "moe_balance_workspace_bytes"]
+           "moe_balance_loss_backward", "moe_balance_workspace_bytes", "moe_few_tokens", "moe_few_tokens_workspace_bytes"]
 
 
 def _ptr(t):
@@ -835,6 +835,54 @@ def _gate_backward(fn, logits, T, E, ld, dt, topk, ids, dweights, score, token_m
             _ptr(logits), dt, T, E, ld, topk, score, _ptr(token_mask), bool(renormalize), route_scale, _ptr(ids),
             _ptr(dweights), _ptr(seq_offs), S, _ptr(dprob), _ptr(dloss), _ptr(dlogits), _current(logits)))
     return dlogits
+
+
+def moe_few_tokens_workspace_bytes(tokens: int, topk: int, ffn: int) -> int:
+    return int(_lib.lib().moe_few_tokens_workspace_bytes(tokens, topk, ffn))
+
+
+def _few_weights(fn, name, w, scale, E, rows, cols, w_fmt, scale_kind):
+    """Quantized weights [E, rows, cols] of the given format and their scales, checked."""
+    dtypes = (torch.int8, torch.uint8) if w_fmt == OPD_INT8 else (torch.uint8, torch.float8_e4m3fn)
+    if tuple(w.shape) != (E, rows, cols) or w.dtype not in dtypes or not w.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape "
+                         f"{(E, rows, cols)}, got {w.dtype} {tuple(w.shape)}")
+    n = E * rows
+    if scale_kind == SCALE_F32:
+        dtype, need = torch.float32, n
+    else:
+        nb = cols // 32
+        dtype, need = torch.uint8, 4 * n * -(-nb // 4) if scale_kind == SCALE_E8M0_K4 else n * nb
+    if scale.dtype != dtype or scale.numel() != need or not scale.is_contiguous():
+        raise ValueError(f"{fn}: {name}_scale must be a contiguous {dtype} tensor of {need} elements, got {scale.dtype} "
+                         f"{tuple(scale.shape)}")
+
+
+def moe_few_tokens(x, ids, weights, w1, w1_scale, w2, w2_scale, w_fmt=OPD_E4M3FN, scale_kind=SCALE_F32, y=None,
+                   workspace=None, stream=None):
+    """The whole expert block for at most 64 tokens: x bf16 [T, K] (row stride may exceed K), ids int32 and weights f32
+    [T, topk] (as moe_gate gives them), w1 [E, 2F, K] (gate | up rows) and w2 [E, K, F] in 8 bits with their scales ->
+    y bf16 [T, K] = the weighted sum of the experts' SwiGLU blocks.  Formats: e4m3fn codes (uint8 or float8_e4m3fn) with
+    f32 row scales or e8m0 scales (SCALE_E8M0, SCALE_E8M0_K4), or OPD_INT8 codes with f32 row scales, as quantize_rowwise
+    and quantize_mx give them.  y may be x (contiguous)."""
+    fn = "moe_few_tokens"
+    T, K, ld = _rows2d(fn, "x", x, _BF16)
+    topk = _gate_slots(fn, "ids", ids, T, _I32)
+    if topk < 1 or _gate_slots(fn, "weights", weights, T, _F32) != topk:
+        raise ValueError(f"{fn}: ids and weights must have one shape [T, topk], got {tuple(ids.shape)}, {tuple(weights.shape)}")
+    if w1.dim() != 3 or w1.shape[1] % 2:
+        raise ValueError(f"{fn}: w1 must have the shape [E, 2F, K], got {tuple(w1.shape)}")
+    E, F = w1.shape[0], w1.shape[1] // 2
+    _few_weights(fn, "w1", w1, w1_scale, E, 2 * F, K, w_fmt, scale_kind)
+    _few_weights(fn, "w2", w2, w2_scale, E, K, F, w_fmt, scale_kind)
+    with _on(fn, stream, x, ids, weights, w1, w1_scale, w2, w2_scale, workspace):
+        dev = x.device
+        y = _out(fn, "y", y, (T, K), torch.bfloat16, dev)
+        workspace = _workspace(fn, workspace, max(moe_few_tokens_workspace_bytes(T, topk, F), 16), dev)
+        _lib.check(fn, _lib.lib().moe_few_tokens(
+            _ptr(x), T, K, ld, _ptr(ids), _ptr(weights), topk, _ptr(w1), _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), w_fmt,
+            scale_kind, E, F, _ptr(y), _ptr(workspace), _current(x)))
+    return y
 
 
 def encode_f32(y, codec=E4M3FN, q=None, stream=None):

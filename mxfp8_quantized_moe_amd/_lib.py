@@ -31,7 +31,8 @@ EXPORTS = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "moe_permute_rowwise", "moe_combine_backward", "quantize_mx_dual", "swiglu_quantize_mx_dual",
            "swiglu_backward_quantize_mx_dual", "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise",
            "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
-           "moe_gate", "moe_balance_loss", "moe_balance_workspace_bytes", "moe_gate_balance", "moe_gate_backward"]
+           "moe_gate", "moe_balance_loss", "moe_balance_workspace_bytes", "moe_gate_balance", "moe_gate_backward",
+           "moe_few_tokens", "moe_few_tokens_workspace_bytes"]
 
 _lib = None
 
@@ -92,6 +93,9 @@ _SIGS = {
                                 _f32, _vp, _vp, _vp, _vp, _vp]),
     "moe_gate_backward": (_int, [_vp, _int, _i64, _i32, _i64, _i32, _int, _vp, _int, _f32, _vp, _vp, _vp, _i32, _vp,
                                  _vp, _vp, _vp]),
+    "moe_few_tokens": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _int, _int, _i32, _i64, _vp,
+                              _vp, _vp]),
+    "moe_few_tokens_workspace_bytes": (_i64, [_i64, _i32, _i64]),
 }
 
 

@@ -161,4 +161,24 @@ struct GateBwdArgs {
 };
 hipError_t launch_moe_gate_backward(const GateBwdArgs& a, hipStream_t st);
 
+// The expert block for a few tokens.  fmt 0: e4m3fn with fp32 row scales, 1: int8 with fp32 row scales, 2, 3: MXFP8
+// with row-major, K4 scales.
+struct FewArgs {
+  const uint16_t* x;
+  int64_t ld_x;
+  const int32_t* ids;
+  const float* weights;
+  int64_t tokens;
+  int topk, n_experts;
+  int64_t K, F;
+  const uint8_t* w1;
+  const uint8_t* w2;
+  const void* s1;
+  const void* s2;
+  int fmt;
+  uint16_t* a2;
+  uint16_t* y;
+};
+hipError_t launch_moe_few_tokens(const FewArgs& a, hipStream_t st);
+
 }  // namespace fp8moe

@@ -569,4 +569,36 @@ int check_encode_f32(const void* y, int64_t n, int codec, const void* q) {
   return FP8MOE_OK;
 }
 
+int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t F) {
+  if (tokens < 0 || topk < 1 || F < 0 || tokens > kFewMaxTokens || tokens * topk > kFewMaxSlots || F > kI32Max / 4) return -1;
+  return tokens * topk * F * 2;
+}
+
+int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x, const void* ids, const void* weights,
+                         int32_t topk, const void* w1, const void* s1, const void* w2, const void* s2, int w_fmt,
+                         int scale_kind, int32_t E, int64_t F, const void* y, const void* workspace) {
+  const bool fp8 = w_fmt == FP8MOE_OPD_E4M3FN, i8 = w_fmt == FP8MOE_OPD_INT8;
+  if (!fp8 && !i8 && w_fmt != FP8MOE_OPD_E4M3FNUZ && w_fmt != FP8MOE_OPD_BF16) return FP8MOE_ERR_ENUM;
+  if (scale_kind < 0 || scale_kind > 3) return FP8MOE_ERR_ENUM;
+  const bool mx = scale_kind == FP8MOE_SCALE_E8M0, k4 = scale_kind == FP8MOE_SCALE_E8M0_K4;
+  if (tokens < 0 || K < 0 || F < 0 || topk < 1 || E < 1 || ld_x < K || K > kI32Max / 4 || F > kI32Max / 4) return FP8MOE_ERR_SHAPE;
+  if (!(fp8 || (i8 && !mx && !k4)) || scale_kind == FP8MOE_SCALE_NONE) return FP8MOE_ERR_UNSUPPORTED;
+  if (tokens > kFewMaxTokens || topk > kFewMaxSlots || tokens * topk > kFewMaxSlots || E > kFewMaxExperts)
+    return FP8MOE_ERR_UNSUPPORTED;
+  const int64_t rows1 = mul(E, 2 * F), rows2 = mul(E, K), n = mul(rows2, F);
+  const int64_t ns1 = mx ? mul(rows1, K / 32) : k4 ? mx_k4_bytes(rows1, K / 32) : rows1;
+  const int64_t ns2 = mx ? mul(rows2, F / 32) : k4 ? mx_k4_bytes(rows2, F / 32) : rows2;
+  if (rows1 < 0 || rows2 < 0 || n < 0 || mul(n, 2) < 0 || ns1 < 0 || ns2 < 0 || mul(tokens, ld_x) < 0) return FP8MOE_ERR_SHAPE;
+  const int64_t nx = mul(tokens, K);
+  const bool work = nx > 0 && F > 0;
+  if (!need(x, nx) || !need(ids, nx ? tokens : 0) || !need(weights, nx ? tokens : 0) || !need(y, nx)) return FP8MOE_ERR_NULL;
+  if (work && (!w1 || !w2 || !s1 || !s2 || !workspace)) return FP8MOE_ERR_NULL;
+  const int64_t step = mx || k4 ? 32 : 16;
+  if (K % step || F % step || ld_x % 8) return FP8MOE_ERR_ALIGN;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) ||
+      !aligned(workspace, 16) || (!mx && (!aligned(s1, 4) || !aligned(s2, 4))))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
 }  // namespace fp8moe

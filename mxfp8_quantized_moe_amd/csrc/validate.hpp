@@ -134,4 +134,13 @@ int check_moe_gate_backward(int64_t tokens, int32_t topk, float route_scale, con
                             const void* seq_offs, int32_t n_seqs, const void* dprob, const void* dloss,
                             const void* dlogits, int dtype);
 
+// The expert block for a few tokens: a token for each lane of a wave, the choices in LDS.
+constexpr int kFewMaxTokens = 64;
+constexpr int kFewMaxSlots = 1024;
+constexpr int kFewMaxExperts = 1024;
+int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t F);
+int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x, const void* ids, const void* weights,
+                         int32_t topk, const void* w1, const void* s1, const void* w2, const void* s2, int w_fmt,
+                         int scale_kind, int32_t E, int64_t F, const void* y, const void* workspace);
+
 }  // namespace fp8moe
