@@ -888,6 +888,65 @@ int moe_few_tokens(const void *x_bf16, int64_t tokens, int64_t K, int64_t ld_x, 
 int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t F);
 
 /*
+ * swiglu_quantize_rowwise_save -- SwiGLU with the rowwise quantization of its output, its
+ * input kept for the backward pass in 8 bits in the same pass: 2.06 F bytes a row instead
+ * of the 4 F of h1 and the 2 F of a2.
+ *   [as swiglu_quantize_rowwise; the kept form is quantize_mx's.]
+ *   h1      bf16 [rows][ld_h1]  gate in columns [0, F), up in [F, 2F)
+ *   q       u8   [rows][F], scale f32 [rows]: the rowwise recipe over the fp32 values
+ *           a = silu(gate) * up (not over their bf16 copy a2, which swiglu_quantize_rowwise
+ *           quantizes: one rounding instead of two) (written)
+ *   a2      bf16 [rows][F]      bf16(a) (written), or NULL
+ *   hq      u8   [rows][2F], hs_e8m0 u8 [rows][2F / 32]: quantize_mx(h1) with axis 1,
+ *           `rule` and row-major scales (written)
+ *   Requires: rows, F >= 0; F % 32 == 0; ld_h1 >= 2F, ld_h1 % 8 == 0; h1, a2, q, hq 16-byte
+ *   aligned, scale 4-byte aligned; codec E4M3FN or E4M3FNUZ.  One kernel, no allocation.
+ */
+int swiglu_quantize_rowwise_save(const void *h1_bf16, int64_t rows, int64_t F, int64_t ld_h1, int codec, int rule,
+                                 void *a2_bf16, void *q, float *scale, void *hq, void *hs_e8m0, void *stream);
+
+/*
+ * swiglu_backward_quantize_rowwise_saved -- SwiGLU's backward from the kept 8-bit input,
+ * with the rowwise quantization of the gradient for the W1 dgrad GEMM, and the
+ * activation formed again for the W2 weight gradient.
+ *   [as swiglu_backward_quantize_rowwise]
+ *   da2     bf16 [rows][F]   gradient of the activation
+ *   hq, hs_e8m0              as swiglu_quantize_rowwise_save (or quantize_mx) wrote them: g and
+ *           u are the values dec(hq) * 2^(hs - 127).  No gradient passes through the rounding
+ *   dh1     bf16 [rows][2F]  bf16 of [da2 u s (1 + g (1 - s)) | da2 g s], s = sigmoid(g) (written),
+ *           or NULL
+ *   q, scale  u8 [rows][2F], f32 [rows]: the rowwise recipe over those fp32 values (written), or
+ *           NULL together
+ *   a2      bf16 [rows][F]   bf16(g s u) (written), or NULL
+ *   At least one result is asked for.  Requires: rows, F >= 0; F % 32 == 0; bf16 and code
+ *   pointers 16-byte aligned, scale 4-byte aligned; codec E4M3FN or E4M3FNUZ.  One kernel, no
+ *   allocation.
+ */
+int swiglu_backward_quantize_rowwise_saved(const void *da2_bf16, const void *hq, const void *hs_e8m0, int64_t rows,
+                                           int64_t F, int codec, void *dh1_bf16, void *q, float *scale, void *a2_bf16,
+                                           void *stream);
+
+/*
+ * swiglu_quantize_mx_dual_saved, swiglu_backward_quantize_mx_dual_saved --
+ * swiglu_quantize_mx_dual and swiglu_backward_quantize_mx_dual from the kept 8-bit input (the
+ * MXFP8 recipe's backward: the first forms the W2 weight gradient's operand again).
+ *   hq, hs_e8m0  u8 [rows][2F] and [rows][2F / 32], quantize_mx(h1) with axis 1 and
+ *                row-major scales under either rule
+ *   Every result is that of the call without _saved on the bf16 tensor of the values
+ *   dec(hq) * 2^(hs - 127) (exact in bf16 for scales from 2^-117 on; below, a value under 2^-126
+ *   counts as 0 or to bf16's spacing there), and every other argument and requirement as there
+ *   (offs required, non-NULL; hq 16-byte aligned).
+ */
+int swiglu_quantize_mx_dual_saved(const void *hq, const void *hs_e8m0, int64_t rows, int64_t F, const int32_t *offs,
+                                  int32_t n_groups, int rule, int scale_layout, void *a2_bf16, void *q,
+                                  void *scale_e8m0, void *q_t, void *scale_t_e8m0, int64_t rows_pad,
+                                  int32_t *offs_pad_out, void *stream);
+int swiglu_backward_quantize_mx_dual_saved(const void *da2_bf16, const void *hq, const void *hs_e8m0, int64_t rows,
+                                           int64_t F, const int32_t *offs, int32_t n_groups, int rule, int scale_layout,
+                                           void *dh1_bf16, void *q, void *scale_e8m0, void *q_t, void *scale_t_e8m0,
+                                           int64_t rows_pad, int32_t *offs_pad_out, void *stream);
+
+/*
  * fp8moe_encode_f32 -- the device FP8 encoder alone: q[i] = enc(y[i]) for
  * values already inside [-fmax, fmax] (round to nearest, ties to the even
  * code; e4m3fn keeps the sign of zero, e4m3fnuz has one unsigned zero).  The

@@ -31,7 +31,9 @@ __all__ = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "quantize_blockwise_tokens", "grouped_mm_blockwise_k",
            "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
            "GATE_SOFTMAX", "GATE_SIGMOID", "moe_gate", "moe_gate_balance", "moe_gate_backward", "moe_balance_loss",
-           "moe_balance_loss_backward", "moe_balance_workspace_bytes", "moe_few_tokens", "moe_few_tokens_workspace_bytes"]
+           "moe_balance_loss_backward", "moe_balance_workspace_bytes", "moe_few_tokens", "moe_few_tokens_workspace_bytes",
+           "swiglu_quantize_rowwise_save", "swiglu_backward_quantize_rowwise_saved", "swiglu_quantize_mx_dual_saved",
+           "swiglu_backward_quantize_mx_dual_saved"]
 
 
 def _ptr(t):
@@ -835,6 +837,108 @@ def _gate_backward(fn, logits, T, E, ld, dt, topk, ids, dweights, score, token_m
             _ptr(logits), dt, T, E, ld, topk, score, _ptr(token_mask), bool(renormalize), route_scale, _ptr(ids),
             _ptr(dweights), _ptr(seq_offs), S, _ptr(dprob), _ptr(dloss), _ptr(dlogits), _current(logits)))
     return dlogits
+
+
+_F8_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _saved_input(fn, hq, hs):
+    """(rows, F) of a SwiGLU input kept in MXFP8 [R, 2F] with row-major scales [R, 2F / 32]."""
+    R, F2, ld = _rows2d(fn, "hq", hq, _F8_CODES)
+    if F2 % 64 or (ld != F2 and R > 1):
+        raise ValueError(f"{fn}: hq must be contiguous [R, 2F] with F a multiple of 32, got {tuple(hq.shape)}, strides {hq.stride()}")
+    if hs.dtype not in (torch.uint8, torch.float8_e8m0fnu) or tuple(hs.shape) != (R, F2 // 32) or not hs.is_contiguous():
+        raise ValueError(f"{fn}: hs must be a contiguous e8m0 (uint8) tensor of shape {(R, F2 // 32)}, got {hs.dtype} "
+                         f"{tuple(hs.shape)}")
+    return R, F2 // 2
+
+
+def _saved_gradient(fn, da2, R, F):
+    if tuple(da2.shape) != (R, F) or da2.dtype != torch.bfloat16 or not da2.is_contiguous():
+        raise ValueError(f"{fn}: da2 must be a contiguous torch.bfloat16 tensor of shape {(R, F)}, got {da2.dtype} "
+                         f"{tuple(da2.shape)}")
+
+
+def swiglu_quantize_rowwise_save(h1, codec=E4M3FN, rule=MX_FLOOR_OCP, keep_bf16=False, a2=None, q=None, scale=None,
+                                 hq=None, hs=None, stream=None):
+    """h1 bf16 [R, 2F] (gate | up; row stride may exceed 2F) -> (a2 bf16 [R, F] or None, q u8 [R, F], scale f32 [R], hq u8
+    [R, 2F], hs u8 [R, 2F / 32]): the rowwise codes of silu(gate) * up (from fp32) for the W2 product, and h1 in MXFP8, all
+    that the backward needs of it.  keep_bf16=True also writes bf16(silu(gate) * up)."""
+    fn = "swiglu_quantize_rowwise_save"
+    R, F2, ld = _rows2d(fn, "h1", h1, _BF16)
+    if F2 % 64:
+        raise ValueError(f"{fn}: h1 needs 2F columns with F a multiple of 32, got {F2}")
+    F = F2 // 2
+    with _on(fn, stream, h1):
+        dev = h1.device
+        a2 = _out(fn, "a2", a2, (R, F), torch.bfloat16, dev) if keep_bf16 else None
+        q = _out(fn, "q", q, (R, F), torch.uint8, dev)
+        scale = _out(fn, "scale", scale, (R,), torch.float32, dev)
+        hq = _out(fn, "hq", hq, (R, F2), torch.uint8, dev)
+        hs = _out(fn, "hs", hs, (R, F2 // 32), torch.uint8, dev)
+        _lib.check(fn, _lib.lib().swiglu_quantize_rowwise_save(
+            _ptr(h1), R, F, ld, codec, rule, _ptr(a2), _ptr(q), _ptr(scale), _ptr(hq), _ptr(hs), _current(h1)))
+    return a2, q, scale, hq, hs
+
+
+def swiglu_backward_quantize_rowwise_saved(da2, hq, hs, codec=E4M3FN, keep_bf16=True, codes=True, want_a2=False, dh1=None,
+                                           q=None, scale=None, a2=None, stream=None):
+    """da2 bf16 [R, F] and the input kept in MXFP8, hq [R, 2F] and hs [R, 2F / 32] -> (dh1 bf16 [R, 2F] or None, q u8 [R, 2F]
+    or None, scale f32 [R] or None, a2 bf16 [R, F] or None): SwiGLU's input gradient and its rowwise codes (from fp32), and
+    with want_a2 the activation again.  keep_bf16=False skips dh1, codes=False skips q and scale."""
+    fn = "swiglu_backward_quantize_rowwise_saved"
+    R, F = _saved_input(fn, hq, hs)
+    _saved_gradient(fn, da2, R, F)
+    if not (keep_bf16 or codes or want_a2):
+        raise ValueError(f"{fn}: no result asked for")
+    with _on(fn, stream, da2, hq, hs):
+        dev = da2.device
+        dh1 = _out(fn, "dh1", dh1, (R, 2 * F), torch.bfloat16, dev) if keep_bf16 else None
+        q = _out(fn, "q", q, (R, 2 * F), torch.uint8, dev) if codes else None
+        scale = _out(fn, "scale", scale, (R,), torch.float32, dev) if codes else None
+        a2 = _out(fn, "a2", a2, (R, F), torch.bfloat16, dev) if want_a2 else None
+        _lib.check(fn, _lib.lib().swiglu_backward_quantize_rowwise_saved(
+            _ptr(da2), _ptr(hq), _ptr(hs), R, F, codec, _ptr(dh1), _ptr(q), _ptr(scale), _ptr(a2), _current(da2)))
+    return dh1, q, scale, a2
+
+
+def _saved_groups(fn, offs):
+    if offs.numel() < 1:
+        raise ValueError(f"{fn}: offs needs at least one group")
+    _vec(fn, "offs", offs, offs.numel(), _I32)
+
+
+def swiglu_quantize_mx_dual_saved(hq, hs, offs, rule=MX_FLOOR_OCP, rows_pad=None, a2=None, q=None, scale=None, q_t=None,
+                                  scale_t=None, offs_pad=None, layout=MX_LAYOUT_K4, stream=None):
+    """swiglu_quantize_mx_dual from the input kept in MXFP8, hq [R, 2F] and hs [R, 2F / 32]: the same results from the kept
+    values (the W2 weight gradient's operand, formed again in the backward)."""
+    fn = "swiglu_quantize_mx_dual_saved"
+    R, F = _saved_input(fn, hq, hs)
+    _saved_groups(fn, offs)
+    with _on(fn, stream, hq, hs, offs):
+        rp, q, scale, q_t, scale_t, offs_pad = _mx_dual_outputs(R, F, offs, rows_pad, q, scale, q_t, scale_t, offs_pad,
+                                                                layout, hq.device)
+        _lib.check(fn, _lib.lib().swiglu_quantize_mx_dual_saved(
+            _ptr(hq), _ptr(hs), R, F, _ptr(offs), offs.numel(), rule, layout, _ptr(a2), _ptr(q), _ptr(scale), _ptr(q_t),
+            _ptr(scale_t), rp, _ptr(offs_pad), _current(hq)))
+    return a2, q, scale, q_t, scale_t, offs_pad
+
+
+def swiglu_backward_quantize_mx_dual_saved(da2, hq, hs, offs, rule=MX_FLOOR_OCP, rows_pad=None, dh1=None, q=None,
+                                           scale=None, q_t=None, scale_t=None, offs_pad=None, layout=MX_LAYOUT_K4,
+                                           stream=None):
+    """swiglu_backward_quantize_mx_dual from the input kept in MXFP8, hq [R, 2F] and hs [R, 2F / 32] (F a multiple of 128)."""
+    fn = "swiglu_backward_quantize_mx_dual_saved"
+    R, F = _saved_input(fn, hq, hs)
+    _saved_gradient(fn, da2, R, F)
+    _saved_groups(fn, offs)
+    with _on(fn, stream, da2, hq, hs, offs):
+        rp, q, scale, q_t, scale_t, offs_pad = _mx_dual_outputs(R, 2 * F, offs, rows_pad, q, scale, q_t, scale_t, offs_pad,
+                                                                layout, hq.device)
+        _lib.check(fn, _lib.lib().swiglu_backward_quantize_mx_dual_saved(
+            _ptr(da2), _ptr(hq), _ptr(hs), R, F, _ptr(offs), offs.numel(), rule, layout, _ptr(dh1), _ptr(q), _ptr(scale),
+            _ptr(q_t), _ptr(scale_t), rp, _ptr(offs_pad), _current(da2)))
+    return dh1, q, scale, q_t, scale_t, offs_pad
 
 
 def moe_few_tokens_workspace_bytes(tokens: int, topk: int, ffn: int) -> int:

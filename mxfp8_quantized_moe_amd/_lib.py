@@ -32,7 +32,9 @@ EXPORTS = ["quantize_rowwise", "quantize_colwise", "quantize_mx", "quantize_mx_r
            "swiglu_backward_quantize_mx_dual", "moe_permute_quantize_mx_dual", "moe_permute_quantize_colwise",
            "rmsnorm_quantize_rowwise", "rmsnorm_quantize_mx", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
            "moe_gate", "moe_balance_loss", "moe_balance_workspace_bytes", "moe_gate_balance", "moe_gate_backward",
-           "moe_few_tokens", "moe_few_tokens_workspace_bytes"]
+           "moe_few_tokens", "moe_few_tokens_workspace_bytes", "swiglu_quantize_rowwise_save",
+           "swiglu_backward_quantize_rowwise_saved", "swiglu_quantize_mx_dual_saved",
+           "swiglu_backward_quantize_mx_dual_saved"]
 
 _lib = None
 
@@ -96,6 +98,12 @@ _SIGS = {
     "moe_few_tokens": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _int, _int, _i32, _i64, _vp,
                               _vp, _vp]),
     "moe_few_tokens_workspace_bytes": (_i64, [_i64, _i32, _i64]),
+    "swiglu_quantize_rowwise_save": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "swiglu_backward_quantize_rowwise_saved": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
+    "swiglu_quantize_mx_dual_saved": (_int, [_vp, _vp, _i64, _i64, _vp, _i32, _int, _int, _vp, _vp, _vp, _vp, _vp, _i64,
+                                             _vp, _vp]),
+    "swiglu_backward_quantize_mx_dual_saved": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _i32, _int, _int, _vp, _vp, _vp,
+                                                      _vp, _vp, _i64, _vp, _vp]),
 }
 
 

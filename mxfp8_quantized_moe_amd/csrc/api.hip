@@ -431,6 +431,52 @@ int moe_few_tokens(const void* x_bf16, int64_t tokens, int64_t K, int64_t ld_x, 
   return launch_status(launch_moe_few_tokens(a, as_stream(stream)));
 }
 
+int swiglu_quantize_rowwise_save(const void* h1_bf16, int64_t rows, int64_t F, int64_t ld_h1, int codec, int rule,
+                                 void* a2_bf16, void* q, float* scale, void* hq, void* hs_e8m0, void* stream) {
+  const int st = check_swiglu_save(h1_bf16, rows, F, ld_h1, codec, rule, a2_bf16, q, scale, hq, hs_e8m0);
+  if (st) return st;
+  return launch_status(launch_swiglu_save(static_cast<const uint16_t*>(h1_bf16), rows, F, ld_h1, codec, rule,
+                                          static_cast<uint16_t*>(a2_bf16), static_cast<uint8_t*>(q), scale,
+                                          static_cast<uint8_t*>(hq), static_cast<uint8_t*>(hs_e8m0), as_stream(stream)));
+}
+
+int swiglu_backward_quantize_rowwise_saved(const void* da2_bf16, const void* hq, const void* hs_e8m0, int64_t rows,
+                                           int64_t F, int codec, void* dh1_bf16, void* q, float* scale, void* a2_bf16,
+                                           void* stream) {
+  const int st = check_swiglu_saved_backward(da2_bf16, hq, hs_e8m0, rows, F, codec, dh1_bf16, q, scale, a2_bf16);
+  if (st) return st;
+  return launch_status(launch_swiglu_saved_backward(
+      static_cast<const uint16_t*>(da2_bf16), static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), rows, F,
+      codec, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q), scale, static_cast<uint16_t*>(a2_bf16),
+      as_stream(stream)));
+}
+
+int swiglu_quantize_mx_dual_saved(const void* hq, const void* hs_e8m0, int64_t rows, int64_t F, const int32_t* offs,
+                                  int32_t n_groups, int rule, int scale_layout, void* a2_bf16, void* q, void* scale_e8m0,
+                                  void* q_t, void* scale_t_e8m0, int64_t rows_pad, int32_t* offs_pad_out, void* stream) {
+  const int st = check_swiglu_mx_dual_saved(hq, hs_e8m0, nullptr, false, rows, F, offs, n_groups, rule, scale_layout,
+                                            a2_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
+  if (st) return st;
+  return launch_status(launch_swiglu_mx_dual_saved(
+      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), nullptr, rows, F, offs, n_groups, rule,
+      scale_layout, static_cast<uint16_t*>(a2_bf16), static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale_e8m0),
+      static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad, offs_pad_out, as_stream(stream)));
+}
+
+int swiglu_backward_quantize_mx_dual_saved(const void* da2_bf16, const void* hq, const void* hs_e8m0, int64_t rows,
+                                           int64_t F, const int32_t* offs, int32_t n_groups, int rule, int scale_layout,
+                                           void* dh1_bf16, void* q, void* scale_e8m0, void* q_t, void* scale_t_e8m0,
+                                           int64_t rows_pad, int32_t* offs_pad_out, void* stream) {
+  const int st = check_swiglu_mx_dual_saved(hq, hs_e8m0, da2_bf16, true, rows, F, offs, n_groups, rule, scale_layout,
+                                            dh1_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
+  if (st) return st;
+  return launch_status(launch_swiglu_mx_dual_saved(
+      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), static_cast<const uint16_t*>(da2_bf16), rows, F,
+      offs, n_groups, rule, scale_layout, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q),
+      static_cast<uint8_t*>(scale_e8m0), static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad,
+      offs_pad_out, as_stream(stream)));
+}
+
 int fp8moe_encode_f32(const float* y, int64_t n, int codec, void* q, void* stream) {
   const int st = check_encode_f32(y, n, codec, q);
   if (st) return st;

@@ -380,7 +380,8 @@ constexpr int kDualRows = 128, kDualCols = 128;
 // Where the dual kernel's tensor comes from.  PROD 0: read as is.  PROD 1: the
 // SwiGLU output bf16(silu(gate) * up) computed from W1's output h1 (gate in
 // columns [0, F), up in [F, 2F)).  PROD 2: SwiGLU's input gradient [d gate |
-// d up] (2F columns) computed from dA2 and h1.  The tensor then never exists
+// d up] (2F columns) computed from dA2 and h1.  PROD 4, 5: as 1 and 2 from h1's
+// row-major MX form, the bf16 values of its codes.  The tensor then never exists
 // in memory unless `out` asks for a bf16 copy.  Columns of a 16-column slice
 // never straddle F (F % 16 == 0).
 struct DualSrc {
@@ -394,8 +395,22 @@ struct DualSrc {
   const float* gw;        // PROD 3: [slots] router weights, or null
   int topk;               // PROD 3: slots per token
   int64_t slots;          // PROD 3: tokens * topk
+  const uint8_t* hq;      // PROD 4, 5: [rows][2F] e4m3fn codes of h1
+  const uint8_t* hs;      // PROD 4, 5: [rows][2F / 32] their e8m0 scales
 };
 
+
+// The 16 columns [col, col + 16) of row `row` of h1 as two bf16 chunks, from its MX form (exact from scales
+// of 2^-117 on).
+__device__ __forceinline__ void saved_load(const DualSrc& sr, int64_t row, int col, u32x4& v0, u32x4& v1) {
+  const u32x4 c = *reinterpret_cast<const u32x4*>(sr.hq + row * 2 * sr.F + col);
+  const float so = mx_scale_operand(sr.hs[row * (2 * sr.F / 32) + (col >> 5)]);
+  auto two = [&](uint32_t w, auto hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, so, decltype(hi)::value));
+  };
+  v0 = u32x4{two(c.x, std::false_type{}), two(c.x, std::true_type{}), two(c.y, std::false_type{}), two(c.y, std::true_type{})};
+  v1 = u32x4{two(c.z, std::false_type{}), two(c.z, std::true_type{}), two(c.w, std::false_type{}), two(c.w, std::true_type{})};
+}
 
 // The 16 columns [col, col + 16) of tensor row `row` (cols columns) as two 8-column chunks.
 template <int PROD>
@@ -424,6 +439,12 @@ __device__ __forceinline__ void dual_load(const DualSrc& sr, int64_t row, int co
     const uint16_t* g = sr.h1 + row * sr.ld_h1 + col;
     const u32x4 g0 = *reinterpret_cast<const u32x4*>(g), g1 = *reinterpret_cast<const u32x4*>(g + 8);
     const u32x4 u0 = *reinterpret_cast<const u32x4*>(g + sr.F), u1 = *reinterpret_cast<const u32x4*>(g + sr.F + 8);
+    v0 = sw_fwd_chunk(g0, u0);
+    v1 = sw_fwd_chunk(g1, u1);
+  } else if constexpr (PROD == 4) {
+    u32x4 g0, g1, u0, u1;
+    saved_load(sr, row, col, g0, g1);
+    saved_load(sr, row, col + sr.F, u0, u1);
     v0 = sw_fwd_chunk(g0, u0);
     v1 = sw_fwd_chunk(g1, u1);
   } else {
@@ -517,25 +538,34 @@ __global__ __launch_bounds__(256) void mx_dual_kernel(DualSrc sr, int64_t batch,
   // Items stride over the columns of the tensor, except for SwiGLU's backward, whose items stride
   // over F and emit both the d gate tile (columns c0 ..) and the d up tile (F + c0 ..) of dH1 from one
   // evaluation of the product rule (F % 128 == 0, so those tiles are whole).
-  const int cols_i = PROD == 2 ? sr.F : cols;
+  constexpr bool BWD = PROD == 2 || PROD == 5;
+  const int cols_i = BWD ? sr.F : cols;
   const int c0 = strip * kDualCols;
   const int col = c0 + cc * 16;
   const bool col_ok = col < cols_i;                // cols % 32 == 0: a slice is wholly in or out
   const bool full = c0 + kDualCols <= cols_i && A + kDualRows <= r_end && lo + (A + kDualRows - plo) <= hi;
-  u32x4 v[4][2], vu[PROD == 2 ? 4 : 1][2];
+  u32x4 v[4][2], vu[BWD ? 4 : 1][2];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int r = A + 4 * rs + k, in = lo + (r - plo);
     v[k][0] = v[k][1] = u32x4{0, 0, 0, 0};
-    if constexpr (PROD == 2) vu[k][0] = vu[k][1] = u32x4{0, 0, 0, 0};
+    if constexpr (BWD) vu[k][0] = vu[k][1] = u32x4{0, 0, 0, 0};
     if (full || (col_ok && r < r_end && in < hi)) {
-      if constexpr (PROD == 2) {
+      if constexpr (BWD) {
         const int64_t row = lrow0 + in;
         const uint16_t* d = sr.da2 + row * sr.F + col;
-        const uint16_t* g = sr.h1 + row * sr.ld_h1 + col;
         const u32x4 d0 = *reinterpret_cast<const u32x4*>(d), d1 = *reinterpret_cast<const u32x4*>(d + 8);
-        const u32x4 g0 = *reinterpret_cast<const u32x4*>(g), g1 = *reinterpret_cast<const u32x4*>(g + 8);
-        const u32x4 u0 = *reinterpret_cast<const u32x4*>(g + sr.F), u1 = *reinterpret_cast<const u32x4*>(g + sr.F + 8);
+        u32x4 g0, g1, u0, u1;
+        if constexpr (PROD == 5) {
+          saved_load(sr, row, col, g0, g1);
+          saved_load(sr, row, col + sr.F, u0, u1);
+        } else {
+          const uint16_t* g = sr.h1 + row * sr.ld_h1 + col;
+          g0 = *reinterpret_cast<const u32x4*>(g);
+          g1 = *reinterpret_cast<const u32x4*>(g + 8);
+          u0 = *reinterpret_cast<const u32x4*>(g + sr.F);
+          u1 = *reinterpret_cast<const u32x4*>(g + sr.F + 8);
+        }
         sw_bwd_chunk(d0, g0, u0, v[k][0], vu[k][0]);
         sw_bwd_chunk(d1, g1, u1, v[k][1], vu[k][1]);
         if (sr.out != nullptr) {
@@ -671,7 +701,7 @@ __global__ __launch_bounds__(256) void mx_dual_kernel(DualSrc sr, int64_t batch,
   };
 
   emit(v, c0);
-  if constexpr (PROD == 2) {
+  if constexpr (BWD) {
     __syncthreads();   // the codes tile and the block exponents are reused
     emit(vu, sr.F + c0);
   }
@@ -742,6 +772,30 @@ hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, int64_
                                        offs_pad_out, grid, n_strips, st)
                    : launch_dual<1, 1>(sr, 1, rows, cols, offs, n_groups, k4, q, sc, q_t, sc_t, rows_pad,
                                        offs_pad_out, grid, n_strips, st);
+}
+
+hipError_t launch_swiglu_mx_dual_saved(const uint8_t* hq, const uint8_t* hs, const uint16_t* da2, int64_t rows, int64_t F,
+                                       const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
+                                       uint8_t* q, uint8_t* sc, uint8_t* q_t, uint8_t* sc_t, int64_t rows_pad,
+                                       int32_t* offs_pad_out, hipStream_t st) {
+  const bool k4 = scale_layout == 1, bwd = da2 != nullptr;
+  const int64_t cols = bwd ? 2 * F : F;
+  if (cols == 0 && offs_pad_out == nullptr) return hipSuccess;
+  const int n_strips = (int)std::max<int64_t>((F + kDualCols - 1) / kDualCols, 1);   // the backward's items stride over F
+  const int64_t blocks = mx_dual_grid_bound(1, rows, F, true, n_groups, rows_pad);
+  if (blocks == 0) return hipSuccess;
+  DualSrc sr{nullptr, nullptr, da2, 0, (int)F, out};
+  sr.hq = hq;
+  sr.hs = hs;
+  auto pick = [&](auto rule_tag) {
+    constexpr int RULE = decltype(rule_tag)::value;
+    return bwd ? (k4 ? mx_dual_kernel<RULE, true, true, 5> : mx_dual_kernel<RULE, true, false, 5>)
+               : (k4 ? mx_dual_kernel<RULE, true, true, 4> : mx_dual_kernel<RULE, true, false, 4>);
+  };
+  auto kern = rule == 0 ? pick(std::integral_constant<int, 0>{}) : pick(std::integral_constant<int, 1>{});
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), 0, st, sr, (int64_t)1, (int)rows, (int)cols, offs, n_groups, q,
+                     sc, rows, q_t, sc_t, rows_pad, offs_pad_out, n_strips);
+  return hipGetLastError();
 }
 
 hipError_t launch_moe_permute_mx_dual(const uint16_t* x, int64_t tokens, int64_t cols, int topk, const int32_t* src,

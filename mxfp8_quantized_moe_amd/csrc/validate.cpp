@@ -601,4 +601,43 @@ int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x,
   return FP8MOE_OK;
 }
 
+int check_swiglu_save(const void* h1, int64_t rows, int64_t F, int64_t ld_h1, int codec, int rule, const void* a2,
+                      const void* q, const void* scale, const void* hq, const void* hs) {
+  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (rule != FP8MOE_MX_FLOOR_OCP && rule != FP8MOE_MX_CEIL) return FP8MOE_ERR_ENUM;
+  if (rows < 0 || F < 0 || rows > kI32Max || F > kI32Max / 4 || ld_h1 < 2 * F) return FP8MOE_ERR_SHAPE;
+  const int64_t n = mul(rows, 2 * F);
+  if (n < 0 || mul(rows, ld_h1) < 0) return FP8MOE_ERR_SHAPE;
+  if (!need(h1, n) || !need(q, n) || !need(scale, n) || !need(hq, n) || !need(hs, n)) return FP8MOE_ERR_NULL;
+  if (F % 32 || ld_h1 % 8 || !aligned(h1, 16) || !aligned(a2, 16) || !aligned(q, 16) || !aligned(hq, 16) || !aligned(scale, 4))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+int check_swiglu_saved_backward(const void* da2, const void* hq, const void* hs, int64_t rows, int64_t F, int codec,
+                                const void* dh1, const void* q, const void* scale, const void* a2) {
+  if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
+  if (rows < 0 || F < 0 || rows > kI32Max || F > kI32Max / 4 || mul(rows, 2 * F) < 0) return FP8MOE_ERR_SHAPE;
+  const int64_t n = mul(rows, 2 * F);
+  if (n && (q == nullptr) != (scale == nullptr)) return FP8MOE_ERR_NULL;   // codes and scales come together
+  if (!need(da2, n) || !need(hq, n) || !need(hs, n) || (n && !dh1 && !q && !a2)) return FP8MOE_ERR_NULL;
+  if (F % 32 || !aligned(da2, 16) || !aligned(hq, 16) || !aligned(dh1, 16) || !aligned(q, 16) || !aligned(a2, 16) ||
+      !aligned(scale, 4))
+    return FP8MOE_ERR_ALIGN;
+  return FP8MOE_OK;
+}
+
+int check_swiglu_mx_dual_saved(const void* hq, const void* hs, const void* da2, bool backward, int64_t rows, int64_t F,
+                               const int32_t* offs, int32_t n_groups, int rule, int scale_layout, const void* out,
+                               const void* q, const void* sc, const void* q_t, const void* sc_t, int64_t rows_pad,
+                               const int32_t* offs_pad_out) {
+  if (offs == nullptr) return FP8MOE_ERR_NULL;   // the grouped layout of moe_route
+  if (F > kI32Max / 4) return FP8MOE_ERR_SHAPE;
+  // the kept form is contiguous: its codes stand in for the bf16 tensor
+  const int st = check_swiglu_mx_dual(hq, da2, backward, rows, F, 2 * F, offs, n_groups, rule, scale_layout, out, q, sc,
+                                      q_t, sc_t, rows_pad, offs_pad_out);
+  if (st) return st;
+  return need(hs, mul(rows, F)) ? FP8MOE_OK : FP8MOE_ERR_NULL;
+}
+
 }  // namespace fp8moe

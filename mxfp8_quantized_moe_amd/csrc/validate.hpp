@@ -143,4 +143,13 @@ int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x,
                          int32_t topk, const void* w1, const void* s1, const void* w2, const void* s2, int w_fmt,
                          int scale_kind, int32_t E, int64_t F, const void* y, const void* workspace);
 
+int check_swiglu_save(const void* h1, int64_t rows, int64_t F, int64_t ld_h1, int codec, int rule, const void* a2,
+                      const void* q, const void* scale, const void* hq, const void* hs);
+int check_swiglu_saved_backward(const void* da2, const void* hq, const void* hs, int64_t rows, int64_t F, int codec,
+                                const void* dh1, const void* q, const void* scale, const void* a2);
+int check_swiglu_mx_dual_saved(const void* hq, const void* hs, const void* da2, bool backward, int64_t rows, int64_t F,
+                               const int32_t* offs, int32_t n_groups, int rule, int scale_layout, const void* out,
+                               const void* q, const void* sc, const void* q_t, const void* sc_t, int64_t rows_pad,
+                               const int32_t* offs_pad_out);
+
 }  // namespace fp8moe
