@@ -81,8 +81,8 @@ extern "C" {
 #define FP8MOE_E4M3FN 0
 #define FP8MOE_E4M3FNUZ 1
 /* Symmetric 8-bit integers: whole numbers in [-127, 127], two's complement, under the
- * rowwise recipe with fmax 127 (q = the whole number nearest to clamp(fp32(x * s)), ties to
- * even).  Taken by the rowwise quantizers of forward operands (quantize_rowwise,
+ * rowwise recipe with s = fp32(127 * fp32(1 / max(amax, 1e-12f))) (the two roundings that torch
+ * makes of `127 / amax`) and q = the whole number nearest to clamp(fp32(x * s)), ties to even.  Taken by the rowwise quantizers of forward operands (quantize_rowwise,
  * swiglu_quantize_rowwise, moe_permute_rowwise, moe_permute_quantized,
  * rmsnorm_quantize_rowwise); their product is grouped_mm_scaled with FP8MOE_OPD_INT8. */
 #define FP8MOE_INT8 4

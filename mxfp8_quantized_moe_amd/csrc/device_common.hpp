@@ -129,8 +129,11 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 
 // ------------------------------------------------------------------ scale
 
-// s = fmax / max(amax, 1e-12f) with an IEEE round-to-nearest-even division.
+// s = fmax / max(amax, 1e-12f) with an IEEE round-to-nearest-even division; for the integers 127 times the
+// reciprocal, two roundings, which is what torch evaluates for `127 / amax`: whole-number codes then agree with those
+// of weights that a line of torch quantized, also where a value lies on the border between two.
 __device__ __forceinline__ float scale_from_amax(float amax, int codec) {
+  if (codec == kInt8) return __fmul_rn(127.0f, __fdiv_rn(1.0f, fmaxf(amax, kAmaxFloor)));
   return __fdiv_rn(fmax_of(codec), fmaxf(amax, kAmaxFloor));
 }
 

@@ -2,7 +2,7 @@
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 
-The rowwise recipe with fmax 127: s = fp32(127 / max(amax, 1e-12)), y =
+The rowwise recipe with fmax 127: s = fp32(127 * fp32(1 / max(amax, 1e-12))), y =
 clamp(fp32(x * s), -127, 127), q = the whole number nearest to y, ties to even.
 The product of two such operands sums whole numbers: exact in fp64 below 2^53.
 """
@@ -20,7 +20,7 @@ def quantize_rows_f32(f: np.ndarray):
     """fp32 rows -> (codes int8 [R, C], scale f32 [R])."""
     f = np.asarray(f, np.float32)
     amax = np.abs(f).max(axis=1) if f.shape[1] else np.zeros(f.shape[0], np.float32)
-    scale = FMAX / np.maximum(amax, EPS)
+    scale = FMAX * (np.float32(1) / np.maximum(amax, EPS))
     y = np.clip(f * scale[:, None], -FMAX, FMAX)
     return np.rint(y).astype(np.int8), scale
 

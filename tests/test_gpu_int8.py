@@ -14,7 +14,7 @@ from gpu_helpers import DEV, note, bf16_dev, i32_dev, host, bf16_bits_to_f64, as
 pytestmark = pytest.mark.gpu
 
 INT8 = fm.INT8
-PAD_SCALE = np.float32(127) / np.float32(1e-12)
+PAD_SCALE = np.float32(127) * (np.float32(1) / np.float32(1e-12))
 
 
 def rows(rng, R, C):

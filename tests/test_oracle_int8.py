@@ -22,12 +22,19 @@ def test_codes_by_fractions():
     for r in range(len(x)):
         amax = max(abs(float(v)) for v in f[r])
         exact = Fraction(127) / Fraction(max(amax, float(np.float32(1e-12))))
-        assert abs(Fraction(float(s[r])) - exact) <= exact / 2 ** 24
+        assert abs(Fraction(float(s[r])) - exact) <= 2 * exact / 2 ** 24 + exact / 2 ** 47   # two roundings
         for c in range(24):
             y = np.float32(f[r, c] * s[r])                     # one rounded product
             assert q[r, c] == nearest_even(Fraction(float(np.clip(y, -127, 127))))
-    assert not q[6].any() and s[6] == np.float32(127) / np.float32(1e-12)
+    assert not q[6].any() and s[6] == np.float32(127) * (np.float32(1) / np.float32(1e-12))
     assert (np.abs(q[:6].astype(int)).max(axis=1) == 127).all()   # the row's largest value is the largest code
+
+
+def test_scale_is_torchs():
+    torch = pytest.importorskip("torch")
+    x = round_bf16(np.random.default_rng(3).standard_normal((2000, 8)))
+    t = torch.from_numpy(oi.bf16_to_f32(x))
+    assert (oi.quantize_rowwise(x)[1] == (127.0 / t.abs().amax(1)).numpy()).all()
 
 
 def test_ties_go_to_even():
