@@ -869,12 +869,13 @@ int moe_gate_backward(const void *logits, int logit_dtype, int64_t tokens, int32
  *             (a scaled weight below 2^-126 counts as 0 or to bf16's spacing there)
  *   y         bf16 [tokens][K]      zeros for a token without an expert (written).  It
  *             may be x itself where ld_x is K
- *   workspace device memory of moe_few_tokens_workspace_bytes(tokens, topk, F) bytes,
+ *   workspace device memory of moe_few_tokens_workspace_bytes(tokens, topk, K, F) bytes,
  *             16-byte aligned, owned by the caller; contents on entry do not matter.
  *             Calls that may overlap (other streams, graphs replayed side by side) need
  *             one each
  *   Requires: tokens <= 64, tokens*topk <= 1024, n_experts <= 1024 (else
  *   FP8MOE_ERR_UNSUPPORTED: more tokens take moe_route and the grouped GEMMs);
+ *   K, F <= 2^20, ld_x <= 2^24;
  *   K % 16 == 0 and F % 16 == 0 (e8m0 scales: 32); ld_x >= K, ld_x % 8 == 0; x, w1, w2,
  *   y 16-byte aligned, the int32 and f32 arrays 4-byte aligned.  Two kernels, no
  *   allocation.
@@ -885,7 +886,7 @@ int moe_few_tokens(const void *x_bf16, int64_t tokens, int64_t K, int64_t ld_x, 
                    void *workspace, void *stream);
 
 /* Workspace bytes moe_few_tokens needs (-1: invalid sizes). */
-int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t F);
+int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, int64_t F);
 
 /*
  * swiglu_quantize_rowwise_save -- SwiGLU with the rowwise quantization of its output, its

@@ -941,8 +941,8 @@ def swiglu_backward_quantize_mx_dual_saved(da2, hq, hs, offs, rule=MX_FLOOR_OCP,
     return dh1, q, scale, q_t, scale_t, offs_pad
 
 
-def moe_few_tokens_workspace_bytes(tokens: int, topk: int, ffn: int) -> int:
-    return int(_lib.lib().moe_few_tokens_workspace_bytes(tokens, topk, ffn))
+def moe_few_tokens_workspace_bytes(tokens: int, topk: int, cols: int, ffn: int) -> int:
+    return int(_lib.lib().moe_few_tokens_workspace_bytes(tokens, topk, cols, ffn))
 
 
 def _few_weights(fn, name, w, scale, E, rows, cols, w_fmt, scale_kind):
@@ -982,7 +982,7 @@ def moe_few_tokens(x, ids, weights, w1, w1_scale, w2, w2_scale, w_fmt=OPD_E4M3FN
     with _on(fn, stream, x, ids, weights, w1, w1_scale, w2, w2_scale, workspace):
         dev = x.device
         y = _out(fn, "y", y, (T, K), torch.bfloat16, dev)
-        workspace = _workspace(fn, workspace, max(moe_few_tokens_workspace_bytes(T, topk, F), 16), dev)
+        workspace = _workspace(fn, workspace, max(moe_few_tokens_workspace_bytes(T, topk, K, F), 16), dev)
         _lib.check(fn, _lib.lib().moe_few_tokens(
             _ptr(x), T, K, ld, _ptr(ids), _ptr(weights), topk, _ptr(w1), _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), w_fmt,
             scale_kind, E, F, _ptr(y), _ptr(workspace), _current(x)))

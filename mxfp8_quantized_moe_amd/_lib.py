@@ -97,7 +97,7 @@ _SIGS = {
                                  _vp, _vp, _vp]),
     "moe_few_tokens": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _int, _int, _i32, _i64, _vp,
                               _vp, _vp]),
-    "moe_few_tokens_workspace_bytes": (_i64, [_i64, _i32, _i64]),
+    "moe_few_tokens_workspace_bytes": (_i64, [_i64, _i32, _i64, _i64]),
     "swiglu_quantize_rowwise_save": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "swiglu_backward_quantize_rowwise_saved": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
     "swiglu_quantize_mx_dual_saved": (_int, [_vp, _vp, _i64, _i64, _vp, _i32, _int, _int, _vp, _vp, _vp, _vp, _vp, _i64,

@@ -414,8 +414,8 @@ int grouped_mm_scaled(int mode, const void* a, int a_fmt, const void* a_scale, c
   return launch_status(launch_grouped_mm(g, as_stream(stream)));
 }
 
-int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t F) {
-  return few_workspace_bytes(tokens, topk, F);
+int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, int64_t F) {
+  return few_workspace_bytes(tokens, topk, K, F);
 }
 
 int moe_few_tokens(const void* x_bf16, int64_t tokens, int64_t K, int64_t ld_x, const int32_t* ids, const float* weights,
@@ -427,7 +427,7 @@ int moe_few_tokens(const void* x_bf16, int64_t tokens, int64_t K, int64_t ld_x, 
   const int fmt = w_fmt == FP8MOE_OPD_INT8 ? 1 : scale_kind == FP8MOE_SCALE_F32 ? 0 : scale_kind == FP8MOE_SCALE_E8M0 ? 2 : 3;
   const FewArgs a{static_cast<const uint16_t*>(x_bf16), ld_x, ids, weights, tokens, topk, n_experts, K, F,
                   static_cast<const uint8_t*>(w1), static_cast<const uint8_t*>(w2), w1_scale, w2_scale, fmt,
-                  static_cast<uint16_t*>(workspace), static_cast<uint16_t*>(y_bf16)};
+                  workspace, static_cast<uint16_t*>(y_bf16)};
   return launch_status(launch_moe_few_tokens(a, as_stream(stream)));
 }
 

@@ -176,7 +176,7 @@ struct FewArgs {
   const void* s1;
   const void* s2;
   int fmt;
-  uint16_t* a2;
+  void* workspace;
   uint16_t* y;
 };
 hipError_t launch_moe_few_tokens(const FewArgs& a, hipStream_t st);

@@ -17,10 +17,11 @@
 // bf16 exactly (e4m3 and whole numbers up to 128 have at most eight significant bits); an e8m0 scale goes into
 // that conversion, an fp32 scale divides the sum.  Activations come from L2 straight into registers.
 //
-// Tokens that choose one expert are found from the ids by every workgroup for itself: a bitmap of the
-// experts in use, and for an expert a ballot over the tokens (at most 64, one a lane).  A
-// token that names an expert twice is one column with the sum of its weights.
-#include "device_common.hpp"
+// Tokens that choose one expert are found from the ids by every workgroup of the first kernel for itself (a
+// token that names an expert twice is one column with the sum of its weights); the workgroup of an expert's first tile
+// leaves the list for the second kernel, whose waves go through all experts: finding it there again cost 2 us a wave
+// and expert, a fifth of the time at 64 tokens of 32 experts.
+#include "gemm_common.hpp"
 #include "kernels.hpp"
 #include "swiglu_common.hpp"
 #include "validate.hpp"
@@ -42,53 +43,19 @@ struct FewParams {
   const uint8_t* w2;      // [E][K][F]
   const void* s1;
   const void* s2;
-  uint16_t* a2;           // [T * topk][F]: the row of a token's first slot of an expert
   uint16_t* y;            // [T][K]
   int T, topk, E, K, F;
+  int ranks;              // experts that can be in use: min(E, T * topk)
+  // workspace
+  uint16_t* a2;           // [T * topk][F]: the row of a token's first slot of an expert
+  float* part;            // [T * topk][K]: that slot's weighted product with W2
+  int2* lists;            // [ranks][T]: an expert's tokens: token << 16 | slot, and the weight's bits
+  int32_t* heads;         // [ranks]: id | tokens << 16
+  int32_t* firsts;        // [T * topk]: 1 for a token's first slot of an expert, else 0
+  int32_t* arrived;       // [ceil(K / 32)][32]: workgroups of the second kernel that are through with these columns
 };
 
 // ---------------------------------------------------------------- who chose whom
-
-struct FewIds {
-  int n_act;                       // experts in use
-  int ids[kFewMaxSlots];
-  float w[kFewMaxSlots];
-  uint32_t bits[32];               // experts in use, one bit each (E <= 1024)
-  int act[kFewMaxSlots];           // the experts in use, in increasing order
-};
-
-// Fills `s` (every thread of the workgroup; ends with a barrier).
-__device__ __forceinline__ void few_experts(const FewParams& p, FewIds& s) {
-  const int t = threadIdx.x, S = p.T * p.topk;
-  if (t < 32) s.bits[t] = 0;
-  for (int i = t; i < S; i += blockDim.x) {
-    s.ids[i] = p.ids[i];
-    s.w[i] = p.weights[i];
-  }
-  __syncthreads();
-  for (int i = t; i < S; i += blockDim.x) {
-    const int e = s.ids[i];
-    if (e >= 0 && e < p.E) atomicOr(&s.bits[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  if (t < 64) {
-    uint32_t b = t < 32 ? s.bits[t] : 0u;
-    int at = __popc(b);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up(at, d, 64);
-      if (t >= d) at += o;
-    }
-    if (t == 31) s.n_act = at;
-    for (at -= __popc(b); b != 0u; b &= b - 1u) s.act[at++] = 32 * t + __ffs(b) - 1;
-  }
-  __syncthreads();
-}
-
-struct FewList {
-  int tok[64], slot[64];
-  float w[64];
-};
 
 // LDS written by the wave's lanes so far is seen by its other lanes.
 __device__ __forceinline__ void few_wave_sync() {
@@ -96,37 +63,121 @@ __device__ __forceinline__ void few_wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The tokens of expert e, in order, by one wave; their count.
-__device__ __forceinline__ int few_members(const FewParams& p, const FewIds& s, int e, FewList& l) {
-  const int lane = threadIdx.x & 63;
-  int first = -1;
+// Every slot's expert (0xFFFF: none), a bitmap of the experts in use and their list.
+struct FewIds {
+  uint32_t bits[32];
+  int n_act;
+  uint16_t ids[kFewMaxSlots];
+  uint16_t act[kFewMaxSlots];
+};
+
+// An expert's tokens in increasing order: token << 16 | the token's first slot of the expert, and its weight.
+struct FewList {
+  int ts[64];
+  float w[64];
+};
+
+// The tokens of the expert of rank `rank`, by every wave for itself into its own list; their count (0: no expert of that
+// rank).  How ranks are given out:
+//  * up to 64 slots: in the order of the experts' first slots, a slot a lane, by ballots;
+//  * no more experts than slots: rank and expert are the same, a token a lane;
+//  * else through LDS, experts in increasing order (every thread of the workgroup calls it).
+// The first two take no LDS and no barrier: a single token's 528 workgroups spent 3 of 16 us on those.
+__device__ __forceinline__ int few_members(const FewParams& p, int rank, bool want_w, FewIds& s, FewList& l, int& e) {
+  const int lane = threadIdx.x & 63, S = p.T * p.topk;
+  bool first = false;
+  int tok = lane, slot = 0;
   float w = 0.0f;
-  if (lane < p.T) {
-    for (int j = 0; j < p.topk; ++j) {
-      const int i = lane * p.topk + j;
-      if (s.ids[i] == e) {
-        if (first < 0) first = i;
-        w += s.w[i];
+  if (S <= 64) {
+    int id = lane < S ? p.ids[lane] : -1;
+    if (id >= p.E) id = -1;
+    unsigned long long rest = __ballot(id >= 0), m = 0;
+    e = -1;
+    for (int r = 0; rest != 0ull; ++r) {
+      e = __builtin_amdgcn_readlane(id, __ffsll(rest) - 1);
+      m = __ballot(id == e);
+      if (r == rank) break;
+      rest &= ~m;
+    }
+    if (rest == 0ull) return 0;
+    if (id == e) {
+      tok = lane / p.topk;
+      slot = lane;
+      unsigned long long own = m >> (tok * p.topk);           // the token's slots of this expert
+      if (p.topk < 64) own &= (1ull << p.topk) - 1ull;
+      first = (own & ((1ull << (lane - tok * p.topk)) - 1ull)) == 0ull;
+      if (first && want_w)
+        for (; own != 0ull; own &= own - 1ull) w += p.weights[tok * p.topk + __ffsll(own) - 1];
+    }
+  } else {
+    if (p.E <= S) {
+      e = rank;
+      if (lane < p.T) {
+        int at = -1;
+#pragma unroll 8
+        for (int j = p.topk - 1; j >= 0; --j) at = p.ids[lane * p.topk + j] == e ? j : at;
+        first = at >= 0;
+        slot = lane * p.topk + at;
+      }
+    } else {
+      const int t = threadIdx.x;
+      if (t < 32) s.bits[t] = 0;
+      __syncthreads();
+      for (int i = t; i < S; i += blockDim.x) {
+        const int id = p.ids[i];
+        const bool in = id >= 0 && id < p.E;
+        s.ids[i] = in ? (uint16_t)id : (uint16_t)0xFFFF;
+        if (in) atomicOr(&s.bits[id >> 5], 1u << (id & 31));
+      }
+      __syncthreads();
+      if (t < 64) {
+        uint32_t b = t < 32 ? s.bits[t] : 0u;
+        int at = __popc(b);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up(at, d, 64);
+          if (t >= d) at += o;
+        }
+        if (t == 31) s.n_act = at;
+        for (at -= __popc(b); b != 0u; b &= b - 1u) s.act[at++] = (uint16_t)(32 * t + __ffs(b) - 1);
+      }
+      __syncthreads();
+      if (rank >= s.n_act) return 0;
+      e = s.act[rank];
+      if (lane < p.T) {
+        int at = -1;
+        for (int j = p.topk - 1; j >= 0; --j) at = (int)s.ids[lane * p.topk + j] == e ? j : at;
+        first = at >= 0;
+        slot = lane * p.topk + at;
       }
     }
+    if (first && want_w)
+      for (int j = slot; j < (lane + 1) * p.topk; ++j)
+        if (p.ids[j] == e) w += p.weights[j];
   }
-  const unsigned long long m = __ballot(first >= 0);
-  if (first >= 0) {
+  e = __builtin_amdgcn_readfirstlane(e);
+  const unsigned long long m = __ballot(first);
+  if (first) {
     const int at = __popcll(m & ((1ull << lane) - 1ull));
-    l.tok[at] = lane;
-    l.slot[at] = first;
+    l.ts[at] = (tok << 16) | slot;
     l.w[at] = w;
   }
+  few_wave_sync();
   return __popcll(m);
 }
 
 // ---------------------------------------------------------------- products
 
-// Sixteen bytes of a weight row and, for MX, the scale of their block.
-__device__ __forceinline__ u32x4 few_load16(const uint8_t* q) {
+// Sixteen bytes, streamed (non-temporal) or not.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 few_load16(const uint8_t* base, uint32_t off) {
   typedef unsigned int v4u __attribute__((ext_vector_type(4)));
-  const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(q));
-  return u32x4{v.x, v.y, v.z, v.w};
+  if constexpr (STREAM) {
+    const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(base + off));
+    return u32x4{v.x, v.y, v.z, v.w};
+  } else {
+    return *reinterpret_cast<const u32x4*>(base + off);
+  }
 }
 
 template <int FMT>
@@ -151,245 +202,338 @@ __device__ __forceinline__ few_v8bf few_bf16(uint32_t a, uint32_t b, float sc) {
   return __builtin_bit_cast(few_v8bf, u32x4{o[0], o[1], o[2], o[3]});
 }
 
-// A lane's row of an operand with MX scales: byte of block b at base + (b >> 2) * group + (b & 3) (K4), or base + b.
-struct FewScale {
-  const uint8_t* base;
+// A tile of weight rows and their e8m0 scales: first row, and the scale of its block b at
+// (b >> 2) * group + (b & 3) (K4) or b.
+struct FewTile {
+  const uint8_t* w;
+  const uint8_t* s;
   int64_t group;
 };
 template <int FMT>
-__device__ __forceinline__ FewScale few_scale_row(const void* s, int64_t row, int64_t rows, int L) {
+__device__ __forceinline__ FewTile few_tile(const uint8_t* w, const void* s, int64_t row, int64_t rows, int L) {
   const uint8_t* b = static_cast<const uint8_t*>(s);
-  if constexpr (FMT == kFewMx) return FewScale{b + row * (L / 32), 0};
-  else if constexpr (FMT == kFewMxK4) return FewScale{b + 4 * row, 4 * rows};
-  else return FewScale{nullptr, 0};
+  if constexpr (FMT == kFewMx) return FewTile{w + row * L, b + row * (L / 32), 0};
+  else if constexpr (FMT == kFewMxK4) return FewTile{w + row * L, b + 4 * row, 4 * rows};
+  else return FewTile{w + row * L, nullptr, 0};
 }
 
-// acc[r][b] += (tile r of 16 weight rows) x (16 tokens of block b) over the steps [s0, s1) of 64 contraction
-// values; w and x are the lane's own rows.  Steps that pass L (a multiple of 16) load a valid chunk again and
-// multiply it by zero.
-template <int FMT, int R, int NB, int U>
-__device__ __forceinline__ void few_dot(const uint8_t* const (&w)[R], const FewScale (&sc)[R],
-                                        const uint16_t* const (&x)[NB], int L, int s0, int s1,
-                                        few_v4f (&acc)[R][NB]) {
-  const int kl = 16 * ((threadIdx.x & 63) >> 4);
-  auto steps = [&](int s, auto whole_tag) {
-    constexpr bool WHOLE = decltype(whole_tag)::value;
-    u32x4 wv[U][R], xv[U][NB][2];
-    float f[U][R];
+// Products of NT tiles of 16 weight rows with the tokens of an expert, over the steps [s0, s1) of 64 Q
+// contraction values of rows of length L (a multiple of 16; a step that passes it loads a valid chunk again and
+// multiplies it by zero).
+//
+// Q = 1: a tile is the instruction's 16 rows, NB blocks of 16 tokens its columns; a load takes 64 bytes of each
+// row.  Q = 2, 4 (up to 16 / Q tokens): a tile is Q parts of 16 / Q rows, and an instruction takes a part's rows Q times,
+// each time with another of Q neighbouring chunks of 64 bytes, and the tokens with those chunks in its
+// columns.  Of the result the Q blocks on the diagonal are products of one chunk; their sum is the answer, the rest
+// is not used.  A load then takes 64 Q bytes of a row together, whole cache lines, and the activations' loads are shared by
+// the parts: a Q-th of them.
+//
+// STREAM: loads of whole cache lines are non-temporal, which leaves the activations in L2 (half lines that are streamed
+// would be fetched twice).
+template <int FMT, int NT, int NB, int Q, bool STREAM>
+struct FewDot {
+  static constexpr int ROWS = 16 / Q, PARTS = Q, R = NT * PARTS, STEP = 64 * Q;
+  static constexpr int U = R * NB >= 8 ? 1 : R * NB >= 4 ? 2 : 4;   // steps whose loads are in flight together
+  few_v4f acc[R][NB];
+
+  // x: byte offset of the lane's row of activations from `xb`
+  __device__ __forceinline__ void run(const FewTile (&tile)[NT], const uint16_t* xb, const uint32_t (&x)[NB], int L, int s0,
+                                      int s1) {
+    const int lane = threadIdx.x & 63;
+    const int kl = 16 * (lane >> 4) + 64 * ((lane & 15) / ROWS);
+    const uint32_t row = (lane & 15) % ROWS;
+    const uint32_t row_w = row * L, row_s = FMT == kFewMxK4 ? 4 * row : row * (L / 32);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kk = 64 * (s + u) + kl;
-      const int k = WHOLE ? kk : min(kk, L - 16);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        wv[u][r] = few_load16(w[r] + k);
-        f[u][r] = 1.0f;
-        if constexpr (FMT == kFewMx) f[u][r] = __uint_as_float((uint32_t)sc[r].base[k >> 5] << 23);
-        if constexpr (FMT == kFewMxK4)
-          f[u][r] = __uint_as_float((uint32_t)sc[r].base[(int64_t)(k >> 7) * sc[r].group + ((k >> 5) & 3)] << 23);
-      }
+      for (int b = 0; b < NB; ++b) acc[r][b] = few_v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto steps = [&](int s, auto whole_tag) {
+      constexpr bool WHOLE = decltype(whole_tag)::value;
+      u32x4 wv[U][R], xv[U][NB][2];
+      uint32_t e[U][R];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        xv[u][b][0] = *reinterpret_cast<const u32x4*>(x[b] + k);
-        xv[u][b][1] = *reinterpret_cast<const u32x4*>(x[b] + k + 8);
-      }
-    }
+      for (int u = 0; u < U; ++u) {
+        const int kk = STEP * (s + u) + kl;
+        const uint32_t k = WHOLE ? kk : min(kk, L - 16);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if constexpr (!WHOLE) {
-        const bool in = s + u < s1 && 64 * (s + u) + kl < L;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          if (!in) xv[u][b][0] = xv[u][b][1] = u32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const few_v8bf lo = few_bf16<FMT>(wv[u][r].x, wv[u][r].y, f[u][r]);
-        const few_v8bf hi = few_bf16<FMT>(wv[u][r].z, wv[u][r].w, f[u][r]);
+        for (int r = 0; r < R; ++r) {
+          const FewTile& t = tile[r / PARTS];
+          wv[u][r] = few_load16<(STREAM && Q > 1)>(t.w + (int64_t)(r % PARTS) * ROWS * L, row_w + k);
+          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * ROWS * (L / 32))[row_s + (k >> 5)];
+          if constexpr (FMT == kFewMxK4)
+            e[u][r] = t.s[(int64_t)(k >> 7) * t.group + (row_s + (r % PARTS) * ROWS * 4 + ((k >> 5) & 3))];
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(few_v8bf, xv[u][b][0]), acc[r][b], 0, 0, 0);
-          acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(few_v8bf, xv[u][b][1]), acc[r][b], 0, 0, 0);
+          const uint8_t* xr = reinterpret_cast<const uint8_t*>(xb);
+          xv[u][b][0] = few_load16<false>(xr, x[b] + 2 * k);
+          xv[u][b][1] = few_load16<false>(xr, x[b] + 2 * k + 16);
         }
       }
-    }
-  };
-  int s = s0;
-  for (; s + U <= s1 && 64 * (s + U) <= L; s += U) steps(s, std::true_type{});
-  for (; s < s1; s += U) steps(s, std::false_type{});
-}
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if constexpr (!WHOLE) {
+          const bool in = s + u < s1 && STEP * (s + u) + kl < L;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (!in) xv[u][b][0] = xv[u][b][1] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float sc = 1.0f;
+          if constexpr (FMT == kFewMx || FMT == kFewMxK4) sc = __uint_as_float(e[u][r] << 23);
+          const few_v8bf lo = few_bf16<FMT>(wv[u][r].x, wv[u][r].y, sc);
+          const few_v8bf hi = few_bf16<FMT>(wv[u][r].z, wv[u][r].w, sc);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(few_v8bf, xv[u][b][0]), acc[r][b], 0, 0, 0);
+            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(few_v8bf, xv[u][b][1]), acc[r][b], 0, 0, 0);
+          }
+        }
+      }
+    };
+    int s = s0;
+    for (; s + U <= s1 && STEP * (s + U) <= L; s += U) steps(s, std::true_type{});
+    for (; s < s1; s += U) steps(s, std::false_type{});
+  }
 
-// Calls f(NB) with the blocks of 16 that n tokens (1 .. 64) fill: 1, 2 or 4.
+  // The lane that holds rows 4 c .. 4 c + 3 of a tile (c = 0 .. 3) for token m of its block, of chunk q; the register
+  // is acc[tile * Q + c / (4 / Q)].
+  static __device__ __forceinline__ int lane_of(int c, int m, int q) { return 16 * (q * (4 / Q) + c % (4 / Q)) + q * ROWS + m; }
+};
+
+// Calls f(NB, Q) for n tokens (1 .. 64): up to 16 tokens in blocks of 16 / Q with Q chunks, more in blocks of 16.
 template <typename Fn>
 __device__ __forceinline__ void few_blocks(int n, Fn&& f) {
-  if (n <= 16) f(std::integral_constant<int, 1>{});
-  else if (n <= 32) f(std::integral_constant<int, 2>{});
-  else f(std::integral_constant<int, 4>{});
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  if (n <= 4) f(I1{}, I4{});
+  else if (n <= 8) f(I1{}, I2{});
+  else if (n <= 16) f(I2{}, I2{});
+  else if (n <= 32) f(I2{}, I1{});
+  else f(I4{}, I1{});
 }
 
-// ---------------------------------------------------------------- first kernel: a = silu(x Wg^T) * (x Wu^T)
+// ---------------------------------------------------------------- the two kernels
 
-// A workgroup takes 16 columns of F of one expert: 16 gate and 16 up rows of W1; its waves split K and
-// add up through LDS.
-template <int FMT, int W>
-__global__ __launch_bounds__(64 * W) void few_up_kernel(FewParams p) {
-  __shared__ FewIds ids;
-  __shared__ FewList list;
-  __shared__ int s_n;
-  __shared__ few_v4f red[W][4][2][64];
-  few_experts(p, ids);
-  const int tiles = p.F / 16;
-  const int rank = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  if (rank >= ids.n_act) return;
-  const int e = ids.act[rank];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (wave == 0) {
-    const int n = few_members(p, ids, e, list);
-    if (lane == 0) s_n = n;
-  }
-  __syncthreads();
-  const int n = s_n;
-  const int64_t row = (int64_t)e * 2 * p.F + tile * 16 + (lane & 15);   // gate row; the up row lies F further
-  const uint8_t* const w[2] = {p.w1 + row * p.K, p.w1 + (row + p.F) * p.K};
-  const int64_t rows = (int64_t)p.E * 2 * p.F;
-  const FewScale sc[2] = {few_scale_row<FMT>(p.s1, row, rows, p.K), few_scale_row<FMT>(p.s1, row + p.F, rows, p.K)};
-  const int steps = (p.K + 63) / 64;
-  const int s0 = steps * wave / W, s1 = steps * (wave + 1) / W;
-  few_blocks(n, [&](auto nb_tag) {
-    constexpr int NB = decltype(nb_tag)::value;
-    const uint16_t* x[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) x[b] = p.x + (int64_t)list.tok[min(16 * b + (lane & 15), n - 1)] * p.ld_x;
-    few_v4f acc[2][NB] = {};
-    few_dot<FMT, 2, NB, NB == 4 ? 2 : 4>(w, sc, x, p.K, s0, s1, acc);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      red[wave][b][0][lane] = acc[0][b];
-      red[wave][b][1][lane] = acc[1][b];
-    }
-  });
-  __syncthreads();
-  // lane l of a block: token l & 15, columns 4 (l >> 4) .. + 3 of the tile
-  for (int i = threadIdx.x; i < ((n + 15) / 16) * 64; i += 64 * W) {
-    const int b = i >> 6, l = i & 63, m = 16 * b + (l & 15);
-    if (m >= n) continue;
-    few_v4f g = red[0][b][0][l], u = red[0][b][1][l];
-#pragma unroll
-    for (int v = 1; v < W; ++v) {
-      g += red[v][b][0][l];
-      u += red[v][b][1][l];
-    }
-    const int c = tile * 16 + 4 * (l >> 4);
-    float a[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float gj = g[j], uj = u[j];
-      if constexpr (FMT == kFewFp8 || FMT == kFewInt8) {
-        const float* s = static_cast<const float*>(p.s1) + (int64_t)e * 2 * p.F + c + j;
-        gj = __fdiv_rn(gj, s[0]);
-        uj = __fdiv_rn(uj, s[p.F]);
-      }
-      a[j] = gj * sw_sigmoid(gj) * uj;
-    }
-    *reinterpret_cast<u32x2*>(p.a2 + (int64_t)list.slot[m] * p.F + c) = u32x2{sw_pack(a[0], a[1]), sw_pack(a[2], a[3])};
-  }
+typedef float few_f4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// Sixteen bytes to memory past the XCD's caches, as a relaxed atomic store at agent scope would go, in one piece.
+__device__ __forceinline__ void few_store_agent16(float* to, few_v4f v) {
+  asm volatile("global_store_dwordx4 %0, %1, off sc1" ::"v"(to), "v"(v) : "memory");
 }
 
-// ---------------------------------------------------------------- second kernel: y = sum of w * (a W2^T)
-
-// A workgroup takes 16 columns of y: 16 rows of every used expert's W2.  The (expert, step) pairs of all experts in
-// use form one sequence that its waves split evenly, each adding its products, times the router's weights, to its
-// own sums in LDS; the waves' sums are added in order at the end, so no result depends on arrival.
-template <int FMT, int W>
-__global__ __launch_bounds__(64 * W) void few_down_kernel(FewParams p) {
-  extern __shared__ __attribute__((aligned(16))) float few_y[];   // [W][T][16]
+// A workgroup takes two tiles of 16 weight rows of one expert for all its tokens; its W waves split the
+// contraction and add up through LDS.
+//
+// UP: 16 gate rows and the matching up rows of W1; writes 16 columns of a = silu(g) * u.  Behind the
+// tiles' workgroups one for each rank writes the expert's list for the second kernel, and one more the counters
+// and the slots' marks.
+//
+// Else 32 rows of W2: 32 columns of each token's product, times its weight, go to the slot's row of `part`; the
+// last workgroup that is through with these columns adds up each token's slots in order and writes y.  Rows of part
+// are written and read past the caches of an XCD (agent scope), and a workgroup's stores have reached memory before
+// it counts itself, each column range on a cache line of its own; which one is last changes nothing.
+template <int FMT, bool UP, int W, bool STREAM>
+__global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
+  __shared__ few_v4f red[W][8][64];
   __shared__ FewIds ids;
   __shared__ FewList lists[W];
-  few_experts(p, ids);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = UP ? p.F / 16 : (p.K + 31) / 32;
+  const int rank = blockIdx.x / tiles, tile = blockIdx.x - rank * tiles;
+  const int L = UP ? p.K : p.F;
   FewList& list = lists[wave];
-  float* const mine = few_y + wave * p.T * 16;
-  for (int i = lane; i < p.T * 16; i += 64) mine[i] = 0.0f;
-  few_wave_sync();
-  const int c0 = blockIdx.x * 16;
-  const int per = (p.F + 63) / 64;   // steps of an expert
-  const int total = ids.n_act * per;
-  int at = (int)((int64_t)total * wave / W);
-  const int end = (int)((int64_t)total * (wave + 1) / W);
-  while (at < end) {
-    const int rank = at / per, s0 = at - rank * per, s1 = min(per, s0 + end - at);
-    const int e = __builtin_amdgcn_readfirstlane(ids.act[rank]);
-    const int n = few_members(p, ids, e, list);
-    few_wave_sync();
-    const int64_t row = (int64_t)e * p.K + c0 + (lane & 15);
-    const uint8_t* const w[1] = {p.w2 + row * p.F};
-    const FewScale sc[1] = {few_scale_row<FMT>(p.s2, row, (int64_t)p.E * p.K, p.F)};
-    few_v4f inv = {1.0f, 1.0f, 1.0f, 1.0f};
-    if constexpr (FMT == kFewFp8 || FMT == kFewInt8) {
-      const float* s = static_cast<const float*>(p.s2) + (int64_t)e * p.K + c0 + 4 * (lane >> 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) inv[j] = s[j];
+  int e, n;
+  if constexpr (UP) {
+    if (rank >= p.ranks) {
+      const int r = blockIdx.x - p.ranks * tiles;
+      if (r < p.ranks) {
+        n = few_members(p, r, true, ids, list, e);
+        if (wave == 0) {
+          if (lane == 0) p.heads[r] = n > 0 ? e | (n << 16) : 0;
+          if (lane < n) p.lists[r * p.T + lane] = int2{list.ts[lane], __float_as_int(list.w[lane])};
+        }
+        return;
+      }
+      for (int i = threadIdx.x; i < (p.K + 31) / 32; i += 64 * W) p.arrived[32 * i] = 0;
+      const int S = p.T * p.topk;
+      for (int i = threadIdx.x; i < S; i += 64 * W) {
+        const int id = p.ids[i];
+        ids.ids[i] = id >= 0 && id < p.E ? (uint16_t)id : (uint16_t)0xFFFF;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < S; i += 64 * W) {
+        bool f = ids.ids[i] != 0xFFFF;
+        for (int j = i - i % p.topk; j < i; ++j) f &= ids.ids[j] != ids.ids[i];
+        p.firsts[i] = f;
+      }
+      return;
     }
-    few_blocks(n, [&](auto nb_tag) {
-      constexpr int NB = decltype(nb_tag)::value;
-      const uint16_t* x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[b] = p.a2 + (int64_t)list.slot[min(16 * b + (lane & 15), n - 1)] * p.F;
-      few_v4f acc[1][NB] = {};
-      few_dot<FMT, 1, NB, NB == 4 ? 2 : 4>(w, sc, x, p.F, s0, s1, acc);
+    n = few_members(p, rank, false, ids, list, e);
+    if (n == 0) return;
+  } else {
+    const int head = __builtin_amdgcn_readfirstlane(p.heads[rank]);
+    e = head & 0xFFFF;
+    n = head >> 16;
+    const int2 v = p.lists[rank * p.T + min(lane, p.T - 1)];
+    list.ts[lane] = v.x;
+    list.w[lane] = __int_as_float(v.y);
+    few_wave_sync();
+  }
+  if (UP || n > 0) {
+    const int64_t row = UP ? (int64_t)e * 2 * p.F + tile * 16 : (int64_t)e * p.K + tile * 32;   // first weight row
+    const bool two = UP || tile * 32 + 16 < p.K;                                                // K may end behind one tile
+    const int64_t row2 = UP ? row + p.F : two ? row + 16 : row;
+    const int64_t rows = (int64_t)p.E * (UP ? 2 * p.F : p.K);
+    const uint8_t* const wp = UP ? p.w1 : p.w2;
+    const void* const sp = UP ? p.s1 : p.s2;
+    const FewTile w[2] = {few_tile<FMT>(wp, sp, row, rows, L), few_tile<FMT>(wp, sp, row2, rows, L)};
+    // a lane will write four columns of each tile: c .. c + 3
+    const int c = 4 * (lane >> 4);
+    few_v4f div[2] = {{1.0f, 1.0f, 1.0f, 1.0f}, {1.0f, 1.0f, 1.0f, 1.0f}};
+    if constexpr (FMT == kFewFp8 || FMT == kFewInt8) {
+      div[0] = *reinterpret_cast<const few_f4u*>(static_cast<const float*>(sp) + row + c);
+      div[1] = *reinterpret_cast<const few_f4u*>(static_cast<const float*>(sp) + row2 + c);
+    }
+    few_blocks(n, [&](auto nb_tag, auto q_tag) {
+      constexpr int NB = decltype(nb_tag)::value, Q = decltype(q_tag)::value;
+      using Dot = FewDot<FMT, 2, NB, Q, STREAM>;
+      uint32_t x[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int m = 16 * b + (lane & 15);
-        if (m >= n) continue;
-        few_v4f* d = reinterpret_cast<few_v4f*>(mine + list.tok[m] * 16 + 4 * (lane >> 4));
-        const float wt = list.w[m];
-        few_v4f v = *d;
+        const int ts = list.ts[min(Dot::ROWS * b + (lane & 15) % Dot::ROWS, n - 1)];
+        x[b] = UP ? (uint32_t)(2 * (ts >> 16) * p.ld_x) : (uint32_t)(2 * (ts & 0xFFFF) * p.F);
+      }
+      const int steps = (L + Dot::STEP - 1) / Dot::STEP;
+      Dot d;
+      d.run(w, UP ? p.x : p.a2, x, L, steps * wave / W, steps * (wave + 1) / W);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float o = acc[0][b][j];
-          if constexpr (FMT == kFewFp8 || FMT == kFewInt8) o = __fdiv_rn(o, inv[j]);
-          v[j] += wt * o;
+      for (int r = 0; r < Dot::R; ++r)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) red[wave][r * NB + b][lane] = d.acc[r][b];
+      __syncthreads();
+      // a lane takes token 16 i + (l & 15), columns 4 (l >> 4) .. + 3 of the tiles
+      for (int i = wave; i < (NB * Dot::ROWS + 15) / 16; i += W) {
+        const int m = 16 * i + (lane & 15), cq = lane >> 4, b = m / Dot::ROWS;
+        if (m >= n) continue;
+        few_v4f g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+#pragma unroll
+        for (int v = 0; v < W; ++v)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const int from = Dot::lane_of(cq, m % Dot::ROWS, q), r = cq / (4 / Q);
+            g += red[v][r * NB + b][from];
+            u += red[v][(Q + r) * NB + b][from];
+          }
+        const int slot = list.ts[m] & 0xFFFF;
+        if constexpr (UP) {
+          float a[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float gj = __fdiv_rn(g[j], div[0][j]), uj = __fdiv_rn(u[j], div[1][j]);
+            a[j] = gj * sw_sigmoid(gj) * uj;
+          }
+          *reinterpret_cast<u32x2*>(p.a2 + (int64_t)slot * p.F + tile * 16 + c) = u32x2{sw_pack(a[0], a[1]), sw_pack(a[2], a[3])};
+        } else {
+          float* o = p.part + (int64_t)slot * p.K + tile * 32 + c;
+          const float wt = list.w[m];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            g[j] = wt * __fdiv_rn(g[j], div[0][j]);
+            u[j] = wt * __fdiv_rn(u[j], div[1][j]);
+          }
+          few_store_agent16(o, g);
+          if (two) few_store_agent16(o + 16, u);
         }
-        *d = v;
       }
     });
-    few_wave_sync();   // the list is rewritten for the next expert
-    at += s1 - s0;
   }
-  __syncthreads();
-  // two columns a thread: four bytes of y
-  for (int i = threadIdx.x; i < p.T * 8; i += 64 * W) {
-    float a = 0.0f, b = 0.0f;
-    for (int v = 0; v < W; ++v) {
-      a += few_y[v * p.T * 16 + 2 * i];
-      b += few_y[v * p.T * 16 + 2 * i + 1];
+  if constexpr (!UP) {
+    __shared__ int s_last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores have reached memory
+    __syncthreads();
+    if (threadIdx.x == 0)
+      s_last = __hip_atomic_fetch_add(p.arrived + 32 * tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.ranks - 1;
+    __syncthreads();
+    if (!s_last) return;
+    // two columns a thread: four bytes of y
+    for (int i = threadIdx.x; i < p.T * 16; i += 64 * W) {
+      const int t = i >> 4, col = tile * 32 + 2 * (i & 15);
+      if (col >= p.K) continue;
+      float a = 0.0f, b = 0.0f;
+#pragma unroll 8
+      for (int j = 0; j < p.topk; ++j) {
+        const int slot = t * p.topk + j;
+        const unsigned long long v = __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p.part + (int64_t)slot * p.K + col),
+                                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const bool f = p.firsts[slot] != 0;   // other slots' rows hold nothing
+        a += f ? __uint_as_float((uint32_t)v) : 0.0f;
+        b += f ? __uint_as_float((uint32_t)(v >> 32)) : 0.0f;
+      }
+      *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.K + col) = sw_pack(a, b);
     }
-    *reinterpret_cast<uint32_t*>(p.y + (int64_t)(i >> 3) * p.K + c0 + 2 * (i & 7)) = sw_pack(a, b);
   }
+}
+
+// Without F there is no product: y is zero.
+__global__ __launch_bounds__(256) void few_zero_kernel(uint32_t* y, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) y[i] = 0;
+}
+
+template <int FMT, bool UP>
+static hipError_t few_launch(const FewParams& p, hipStream_t st) {
+  const int64_t blocks = (int64_t)p.ranks * (UP ? p.F / 16 : (p.K + 31) / 32);
+  const dim3 grid((unsigned)(blocks + (UP ? p.ranks + 1 : 0)));
+  // Short rows leave four waves a step or two each: two waves where the workgroups fill the GPU by themselves
+  // (64 tokens of 64 experts 2048 x 1408: first kernel 75 -> 68 us; rows of 7168: 149 -> 154 us).
+  const bool two = (UP ? p.K : p.F) <= 2048 && blocks >= 512;
+  // Streamed loads where the experts' weights are beyond the last-level cache (64 tokens of 32 experts 7168 x 2048, 1.4 GB:
+  // first kernel 153 -> 144 us); weights that stay there from one call to the next are not (4 tokens of 7 experts
+  // 1040 x 336, 7 MB: 11.9 us streamed, 5.8 not).
+  const bool stream = (int64_t)p.E * 3 * p.K * p.F > (256ll << 20);
+  auto kern = stream ? (two ? few_kernel<FMT, UP, 2, true> : few_kernel<FMT, UP, 4, true>)
+                     : (two ? few_kernel<FMT, UP, 2, false> : few_kernel<FMT, UP, 4, false>);
+  hipLaunchKernelGGL(kern, grid, dim3(two ? 128 : 256), 0, st, p);
+  return hipGetLastError();
 }
 
 template <int FMT>
-static hipError_t few_launch(const FewParams& p, hipStream_t st) {
-  constexpr int W1 = 4, W2 = 8;
-  const int64_t most = std::min<int64_t>(p.E, (int64_t)p.T * p.topk);
-  if (p.F > 0) {
-    hipLaunchKernelGGL((few_up_kernel<FMT, W1>), dim3((unsigned)(most * (p.F / 16))), dim3(64 * W1), 0, st, p);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  hipLaunchKernelGGL((few_down_kernel<FMT, W2>), dim3((unsigned)(p.K / 16)), dim3(64 * W2), W2 * p.T * 64, st, p);
-  return hipGetLastError();
+static hipError_t few_both(const FewParams& p, hipStream_t st) {
+  const hipError_t err = few_launch<FMT, true>(p, st);
+  return err != hipSuccess ? err : few_launch<FMT, false>(p, st);
 }
 
 hipError_t launch_moe_few_tokens(const FewArgs& a, hipStream_t st) {
   if (a.tokens == 0 || a.K == 0) return hipSuccess;
-  const FewParams p{a.x, a.ld_x, a.ids, a.weights, a.w1, a.w2, a.s1, a.s2, a.a2, a.y,
-                    (int)a.tokens, a.topk, a.n_experts, (int)a.K, (int)a.F};
+  if (a.F == 0) {
+    const int64_t n = a.tokens * a.K / 2;
+    hipLaunchKernelGGL(few_zero_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, reinterpret_cast<uint32_t*>(a.y), n);
+    return hipGetLastError();
+  }
+  FewParams p{a.x, a.ld_x, a.ids, a.weights, a.w1, a.w2, a.s1, a.s2, a.y,
+              (int)a.tokens, a.topk, a.n_experts, (int)a.K, (int)a.F};
+  const int64_t slots = a.tokens * a.topk;
+  p.ranks = (int)std::min<int64_t>(slots, a.n_experts);
+  char* ws = static_cast<char*>(a.workspace);   // few_workspace_bytes, in this order (each part's size keeps the next aligned)
+  auto take = [&](int64_t bytes) {
+    char* at = ws;
+    ws += bytes;
+    return at;
+  };
+  p.a2 = reinterpret_cast<uint16_t*>(take(slots * a.F * 2));
+  p.part = reinterpret_cast<float*>(take(slots * a.K * 4));
+  p.lists = reinterpret_cast<int2*>(take(slots * a.tokens * 8));
+  p.heads = reinterpret_cast<int32_t*>(take(slots * 4));
+  p.firsts = reinterpret_cast<int32_t*>(take(slots * 4));
+  p.arrived = reinterpret_cast<int32_t*>(take((a.K + 31) / 32 * 128));
   switch (a.fmt) {
-    case kFewFp8: return few_launch<kFewFp8>(p, st);
-    case kFewInt8: return few_launch<kFewInt8>(p, st);
-    case kFewMx: return few_launch<kFewMx>(p, st);
-    default: return few_launch<kFewMxK4>(p, st);
+    case kFewFp8: return few_both<kFewFp8>(p, st);
+    case kFewInt8: return few_both<kFewInt8>(p, st);
+    case kFewMx: return few_both<kFewMx>(p, st);
+    default: return few_both<kFewMxK4>(p, st);
   }
 }
 

@@ -569,9 +569,13 @@ int check_encode_f32(const void* y, int64_t n, int codec, const void* q) {
   return FP8MOE_OK;
 }
 
-int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t F) {
-  if (tokens < 0 || topk < 1 || F < 0 || tokens > kFewMaxTokens || tokens * topk > kFewMaxSlots || F > kI32Max / 4) return -1;
-  return tokens * topk * F * 2;
+int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, int64_t F) {
+  if (tokens < 0 || topk < 1 || K < 0 || F < 0 || tokens > kFewMaxTokens || tokens * topk > kFewMaxSlots ||
+      K > kFewMaxWidth || F > kFewMaxWidth)
+    return -1;
+  // rows of the activation and of the products, the experts' lists of tokens and their heads, marks, counters
+  const int64_t slots = tokens * topk;
+  return slots * (F * 2 + K * 4 + tokens * 8 + 8) + (K + 31) / 32 * 128;
 }
 
 int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x, const void* ids, const void* weights,
@@ -581,7 +585,8 @@ int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x,
   if (!fp8 && !i8 && w_fmt != FP8MOE_OPD_E4M3FNUZ && w_fmt != FP8MOE_OPD_BF16) return FP8MOE_ERR_ENUM;
   if (scale_kind < 0 || scale_kind > 3) return FP8MOE_ERR_ENUM;
   const bool mx = scale_kind == FP8MOE_SCALE_E8M0, k4 = scale_kind == FP8MOE_SCALE_E8M0_K4;
-  if (tokens < 0 || K < 0 || F < 0 || topk < 1 || E < 1 || ld_x < K || K > kI32Max / 4 || F > kI32Max / 4) return FP8MOE_ERR_SHAPE;
+  if (tokens < 0 || K < 0 || F < 0 || topk < 1 || E < 1 || ld_x < K || K > kFewMaxWidth || F > kFewMaxWidth || ld_x > 16 * kFewMaxWidth)
+    return FP8MOE_ERR_SHAPE;
   if (!(fp8 || (i8 && !mx && !k4)) || scale_kind == FP8MOE_SCALE_NONE) return FP8MOE_ERR_UNSUPPORTED;
   if (tokens > kFewMaxTokens || topk > kFewMaxSlots || tokens * topk > kFewMaxSlots || E > kFewMaxExperts)
     return FP8MOE_ERR_UNSUPPORTED;

@@ -138,7 +138,8 @@ int check_moe_gate_backward(int64_t tokens, int32_t topk, float route_scale, con
 constexpr int kFewMaxTokens = 64;
 constexpr int kFewMaxSlots = 1024;
 constexpr int kFewMaxExperts = 1024;
-int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t F);
+constexpr int64_t kFewMaxWidth = 1 << 20;   // offsets within a tile and the activations are 32-bit
+int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, int64_t F);
 int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x, const void* ids, const void* weights,
                          int32_t topk, const void* w1, const void* s1, const void* w2, const void* s2, int w_fmt,
                          int scale_kind, int32_t E, int64_t F, const void* y, const void* workspace);

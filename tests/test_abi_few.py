@@ -44,8 +44,8 @@ def test_nothing_to_do(lib):
 
 
 def test_workspace_bytes():
-    assert fm.moe_few_tokens_workspace_bytes(64, 16, 4096) >= 64 * 16 * 4096 * 2
-    for bad in ((-1, 1, 16), (65, 1, 16), (64, 17, 16), (4, 0, 16), (4, 1, -16)):
+    assert fm.moe_few_tokens_workspace_bytes(64, 16, 2048, 4096) >= 64 * 16 * (4096 * 2 + 2048 * 4)
+    for bad in ((-1, 1, 16, 16), (65, 1, 16, 16), (64, 17, 16, 16), (4, 0, 16, 16), (4, 1, 16, -16), (4, 1, -16, 16), (4, 1, 1 << 21, 16)):
         assert fm.moe_few_tokens_workspace_bytes(*bad) == -1
 
 

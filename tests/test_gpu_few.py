@@ -192,7 +192,7 @@ def test_captured_and_side_by_side():
     torch.cuda.synchronize()
     for s in streams:
         held = [t.clone() for t in inputs[0]]
-        ws = torch.empty(fm.moe_few_tokens_workspace_bytes(T, k, F), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(fm.moe_few_tokens_workspace_bytes(T, k, K, F), dtype=torch.uint8, device=DEV)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
