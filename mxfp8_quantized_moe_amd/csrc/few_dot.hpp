@@ -1,0 +1,193 @@
+// Products of 8-bit weight rows with the activations of a few tokens (at most 64), bound by the read of the weights.
+//
+// A weight is the matrix instruction's row operand (16 rows a tile), a token a column, so one read of a tile serves all
+// tokens.  A lane loads 16 bytes of a row, and both operands permute the contraction alike, so no byte moves between
+// lanes.  With bf16 activations the codes become bf16 on the way (exactly: e4m3 and whole numbers up to 128 have at most
+// eight significant bits) and two v_mfma_f32_16x16x32_bf16 take a lane's bytes; with whole-number activations
+// one v_mfma_i32_16x16x64_i8 does.  Activations come from L2 straight into registers.
+#pragma once
+
+#include <type_traits>
+
+#include "device_common.hpp"
+
+namespace fp8moe {
+
+typedef __bf16 few_v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 few_v2bf __attribute__((ext_vector_type(2)));
+typedef float few_v4f __attribute__((ext_vector_type(4)));
+
+typedef int few_v4i __attribute__((ext_vector_type(4)));
+
+// Weights: e4m3fn, whole numbers, e4m3fn with e8m0 scales (row-major, K4), all with bf16 activations; whole numbers
+// with whole-number activations.
+enum { kFewFp8 = 0, kFewInt8 = 1, kFewMx = 2, kFewMxK4 = 3, kFewInt8Both = 4 };
+
+typedef float few_f4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float few_v2f __attribute__((ext_vector_type(2)));
+
+// Two fp32 values -> one word of two bf16 (round to nearest even).
+__device__ __forceinline__ uint32_t few_pack(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(few_v2f{a, b}, few_v2bf));
+}
+
+// Sixteen bytes, streamed (non-temporal) or not.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 few_load16(const uint8_t* base, uint32_t off) {
+  typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+  if constexpr (STREAM) {
+    const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(base + off));
+    return u32x4{v.x, v.y, v.z, v.w};
+  } else {
+    return *reinterpret_cast<const u32x4*>(base + off);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ few_v8bf few_bf16(uint32_t a, uint32_t b, float sc) {
+  uint32_t o[4];
+  if constexpr (FMT == kFewInt8) {
+    const uint32_t w[2] = {a, b};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // exact in bf16, so the upper halves of the fp32 patterns are the values
+      const float f0 = (float)(signed char)(w[i] & 0xFFu), f1 = (float)(signed char)((w[i] >> 8) & 0xFFu);
+      const float f2 = (float)(signed char)((w[i] >> 16) & 0xFFu), f3 = (float)(signed char)(w[i] >> 24);
+      o[2 * i] = __builtin_amdgcn_perm(__float_as_uint(f1), __float_as_uint(f0), 0x07060302u);
+      o[2 * i + 1] = __builtin_amdgcn_perm(__float_as_uint(f3), __float_as_uint(f2), 0x07060302u);
+    }
+  } else {
+    o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sc, false));
+    o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, sc, true));
+    o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sc, false));
+    o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, sc, true));
+  }
+  return __builtin_bit_cast(few_v8bf, u32x4{o[0], o[1], o[2], o[3]});
+}
+
+// A tile of weight rows and their e8m0 scales: first row, and the scale of its block b at
+// (b >> 2) * group + (b & 3) (K4) or b.
+struct FewTile {
+  const uint8_t* w;
+  const uint8_t* s;
+  int64_t group;
+};
+template <int FMT>
+__device__ __forceinline__ FewTile few_tile(const uint8_t* w, const void* s, int64_t row, int64_t rows, int L) {
+  const uint8_t* b = static_cast<const uint8_t*>(s);
+  if constexpr (FMT == kFewMx) return FewTile{w + row * L, b + row * (L / 32), 0};
+  else if constexpr (FMT == kFewMxK4) return FewTile{w + row * L, b + 4 * row, 4 * rows};
+  else return FewTile{w + row * L, nullptr, 0};
+}
+
+// Products of NT tiles of 16 weight rows with the tokens of an expert, over the steps [s0, s1) of 64 Q
+// contraction values of rows of length L (a multiple of 16; a step that passes it loads a valid chunk again and
+// multiplies it by zero).
+//
+// Q = 1: a tile is the instruction's 16 rows, NB blocks of 16 tokens its columns; a load takes 64 bytes of each
+// row.  Q = 2, 4 (up to 16 / Q tokens): a tile is Q parts of 16 / Q rows, and an instruction takes a part's rows Q times,
+// each time with another of Q neighbouring chunks of 64 bytes, and the tokens with those chunks in its
+// columns.  Of the result the Q blocks on the diagonal are products of one chunk; their sum is the answer, the rest
+// is not used.  A load then takes 64 Q bytes of a row together, whole cache lines, and the activations' loads are shared by
+// the parts: a Q-th of them.
+//
+// STREAM: loads of whole cache lines are non-temporal, which leaves the activations in L2 (half lines that are streamed
+// would be fetched twice).
+template <int FMT, int NT, int NB, int Q, bool STREAM>
+struct FewDot {
+  static constexpr int ROWS = 16 / Q, PARTS = Q, R = NT * PARTS, STEP = 64 * Q;
+  static constexpr int U = R * NB >= 8 ? 1 : R * NB >= 4 ? 2 : 4;   // steps whose loads are in flight together
+  using Acc = std::conditional_t<FMT == kFewInt8Both, few_v4i, few_v4f>;
+  static constexpr int XB = FMT == kFewInt8Both ? 1 : 2;   // bytes of an activation
+  Acc acc[R][NB];
+
+  // x: byte offset of the lane's row of activations from `xb`
+  __device__ __forceinline__ void run(const FewTile (&tile)[NT], const void* xb, const uint32_t (&x)[NB], int L, int s0,
+                                      int s1) {
+    const int lane = threadIdx.x & 63;
+    const int kl = 16 * (lane >> 4) + 64 * ((lane & 15) / ROWS);
+    const uint32_t row = (lane & 15) % ROWS;
+    const uint32_t row_w = row * L, row_s = FMT == kFewMxK4 ? 4 * row : row * (L / 32);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[r][b] = Acc{0, 0, 0, 0};
+    auto steps = [&](int s, auto whole_tag) {
+      constexpr bool WHOLE = decltype(whole_tag)::value;
+      u32x4 wv[U][R], xv[U][NB][XB];
+      uint32_t e[U][R];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = STEP * (s + u) + kl;
+        const uint32_t k = WHOLE ? kk : min(kk, L - 16);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const FewTile& t = tile[r / PARTS];
+          wv[u][r] = few_load16<(STREAM && Q > 1)>(t.w + (int64_t)(r % PARTS) * ROWS * L, row_w + k);
+          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * ROWS * (L / 32))[row_s + (k >> 5)];
+          if constexpr (FMT == kFewMxK4)
+            e[u][r] = t.s[(int64_t)(k >> 7) * t.group + (row_s + (r % PARTS) * ROWS * 4 + ((k >> 5) & 3))];
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+          for (int h = 0; h < XB; ++h)
+            xv[u][b][h] = few_load16<false>(static_cast<const uint8_t*>(xb), x[b] + XB * k + 16 * h);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if constexpr (!WHOLE) {
+          const bool in = s + u < s1 && STEP * (s + u) + kl < L;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < XB; ++h)
+              if (!in) xv[u][b][h] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if constexpr (FMT == kFewInt8Both) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              acc[r][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(few_v4i, wv[u][r]),
+                                                                __builtin_bit_cast(few_v4i, xv[u][b][0]), acc[r][b], 0, 0, 0);
+            continue;
+          } else {
+          float sc = 1.0f;
+          if constexpr (FMT == kFewMx || FMT == kFewMxK4) sc = __uint_as_float(e[u][r] << 23);
+          const few_v8bf lo = few_bf16<FMT>(wv[u][r].x, wv[u][r].y, sc);
+          const few_v8bf hi = few_bf16<FMT>(wv[u][r].z, wv[u][r].w, sc);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(few_v8bf, xv[u][b][0]), acc[r][b], 0, 0, 0);
+            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(few_v8bf, xv[u][b][1]), acc[r][b], 0, 0, 0);
+          }
+          }
+        }
+      }
+    };
+    int s = s0;
+    for (; s + U <= s1 && STEP * (s + U) <= L; s += U) steps(s, std::true_type{});
+    for (; s < s1; s += U) steps(s, std::false_type{});
+  }
+
+  // The lane that holds rows 4 c .. 4 c + 3 of a tile (c = 0 .. 3) for token m of its block, of chunk q; the register
+  // is acc[tile * Q + c / (4 / Q)].
+  static __device__ __forceinline__ int lane_of(int c, int m, int q) { return 16 * (q * (4 / Q) + c % (4 / Q)) + q * ROWS + m; }
+};
+
+// Calls f(NB, Q) for n tokens (1 .. 64): up to 16 tokens in blocks of 16 / Q with Q chunks, more in blocks of 16.
+template <typename Fn>
+__device__ __forceinline__ void few_blocks(int n, Fn&& f) {
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  if (n <= 4) f(I1{}, I4{});
+  else if (n <= 8) f(I1{}, I2{});
+  else if (n <= 16) f(I2{}, I2{});
+  else if (n <= 32) f(I2{}, I1{});
+  else f(I4{}, I1{});
+}
+
+}  // namespace fp8moe

@@ -1559,7 +1559,8 @@ hipError_t launch_grouped_mm_bf16(const GemmArgs& g, hipStream_t st);
 
 hipError_t launch_grouped_mm(const GemmArgs& g, hipStream_t st) {
   if (g.a_fmt == kInt8) {
-    if (g.M == 0) return hipSuccess;
+    if (g.M == 0 || g.N == 0) return hipSuccess;
+    if (i8_rows_wanted(g)) return launch_i8_rows(g, st);
     return g.out_dtype == 0 ? dispatch_i8<0>(g, st) : dispatch_i8<1>(g, st);
   }
   const bool fn = g.a_fmt == 0 && g.b_fmt == 0;

@@ -55,6 +55,9 @@ struct GemmArgs {
 };
 
 hipError_t launch_grouped_mm(const GemmArgs& g, hipStream_t st);
+// Integer operands with few rows a group.
+bool i8_rows_wanted(const GemmArgs& g);
+hipError_t launch_i8_rows(const GemmArgs& g, hipStream_t st);
 
 // Poll budget of the single-pass colwise exchange (negative: the default); returns the previous one.
 int set_colwise_poll_budget(int polls);

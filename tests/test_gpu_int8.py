@@ -124,6 +124,8 @@ def check_product(M, N, K, offs, f32, seed=0, a=None, b=None):
     (65, 129, 144, [65]), (300, 513, 272, [300]), (700, 264, 400, [700]),
     (77, 96, 192, [10, 10, 9, 60, 60]), (500, 270, 176, [-3, 130, 131, 600, 480]), (40, 64, 64, [0, 0]),
     (1200, 130, 320, [600, 1150]), (2, 24, 32, [1, 2]), (5000, 48, 64, [20, 5000]),
+    (150, 67, 208, [0, 1, 140, 150]), (90, 100, 4112, [70, 90]), (3, 33, 1008, [3]), (260, 72, 96, [3, 5, 260]), (24, 31, 64, [24]),
+    (7, 14336, 64, [7]), (200, 14336, 64, [200]),
 ])
 def test_product(M, N, K, offs, f32):
     note(f"grouped_mm_scaled INT8 {M}x{N}x{K} offs {offs} f32 {f32}")
