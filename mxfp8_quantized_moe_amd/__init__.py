@@ -41,8 +41,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:   # the raw handle: torch.cuda.current_stream builds a Stream object first (2.7 us instead of 0.3)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _bits(x: torch.Tensor) -> torch.Tensor:

@@ -200,6 +200,25 @@ __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, f
   }
 }
 
+// Four e4m3fnuz codes of f * s.  A code's value is half the e4m3fn value of the same code, so enc_fnuz(y) =
+// enc_fn(2y) up to 224 (doubling is exact); 2y above the tie 464 is 240 (0x7F: the low bit on top of the clamped
+// 448's 0x7E), and a zero result drops its sign.  On whole words: 24 operations for four codes, where four single
+// codes take over 40.
+__device__ __forceinline__ uint32_t quant4_fnuz(float a, float b, float c, float d, float s) {
+  const float s2 = 2.0f * s;
+  const float y[4] = {a * s2, b * s2, c * s2, d * s2};
+  float k[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k[i] = __builtin_amdgcn_fmed3f(y[i], -448.0f, 448.0f);
+    top |= fabsf(y[i]) > 464.0f ? 1u << (8 * i) : 0u;
+  }
+  const uint32_t w = cvt_fn_pair<true>(k[2], k[3], cvt_fn_pair<false>(k[0], k[1], 0u)) | top;
+  const uint32_t mag = w & 0x7F7F7F7Fu;
+  return mag | (w & (mag + 0x7F7F7F7Fu) & 0x80808080u);   // the sign where the magnitude is not 0
+}
+
 // Two packed bf16 pairs (4 values) -> four codes.
 template <int CODEC>
 __device__ __forceinline__ uint32_t quant_bf16x4(uint32_t p0, uint32_t p1, float s) {

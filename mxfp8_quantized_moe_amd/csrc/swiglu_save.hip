@@ -51,7 +51,11 @@ __device__ __forceinline__ u32x4 sv_pack(const float (&f)[8]) {
 }
 template <int CODEC>
 __device__ __forceinline__ u32x2 sv_codes(const float (&f)[8], float s) {
-  return u32x2{quant4<CODEC>(f[0], f[1], f[2], f[3], s), quant4<CODEC>(f[4], f[5], f[6], f[7], s)};
+  auto four = [&](int k) {
+    if constexpr (CODEC == 0) return quant4<0>(f[k], f[k + 1], f[k + 2], f[k + 3], s);
+    else return quant4_fnuz(f[k], f[k + 1], f[k + 2], f[k + 3], s);
+  };
+  return u32x2{four(0), four(4)};
 }
 __device__ __forceinline__ float sv_most(float m, const float (&f)[8]) {
 #pragma unroll
@@ -274,11 +278,15 @@ static hipError_t sv_launch(const SaveArgs& p, hipStream_t st) {
 template <bool BWD, int CODEC>
 static hipError_t sv_pick(const SaveArgs& p, hipStream_t st) {
   const int64_t nc = p.F >> 3;
+  // A whole workgroup a row of up to 256 chunks, one chunk a thread, where a wave's three or four chunks one after the other
+  // take longer than idle threads cost: long rows (16384 x 2048: forward 53 -> 48 us, backward 76 -> 71), the backward
+  // (49152 x 1408: 150 -> 143 us; 49152 x 800 88 -> 93 and not taken), few rows (509 x 1056: 5.0 -> 3.6 us). The forward
+  // of 49152 x 1408 takes 93 us by waves, 109 by workgroups.
+  if (nc <= 256 && (nc > 192 || (BWD && nc > 128) || (nc > 64 && p.rows < 2048))) return sv_launch<BWD, CODEC, 256, 1>(p, st);
   if (nc <= 16) return sv_launch<BWD, CODEC, 16, 1>(p, st);
   if (nc <= 64) return sv_launch<BWD, CODEC, 64, 1>(p, st);
   if (nc <= 128) return sv_launch<BWD, CODEC, 64, 2>(p, st);
-  if (nc <= 192) return sv_launch<BWD, CODEC, 64, 3>(p, st);
-  if (nc <= 256) return sv_launch<BWD, CODEC, 64, 4>(p, st);
+  if (!BWD && nc <= 192) return sv_launch<BWD, CODEC, 64, 3>(p, st);
   if (nc <= 512) return sv_launch<BWD, CODEC, 256, 2>(p, st);
   if (nc <= 1024) return sv_launch<BWD, CODEC, 256, 4>(p, st);
   if (nc <= 2048 && !BWD) return sv_launch<BWD, CODEC, 256, 8>(p, st);
