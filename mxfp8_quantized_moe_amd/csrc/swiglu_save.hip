@@ -289,7 +289,7 @@ static hipError_t sv_pick(const SaveArgs& p, hipStream_t st) {
   if (!BWD && nc <= 192) return sv_launch<BWD, CODEC, 64, 3>(p, st);
   if (nc <= 512) return sv_launch<BWD, CODEC, 256, 2>(p, st);
   if (nc <= 1024) return sv_launch<BWD, CODEC, 256, 4>(p, st);
-  if (nc <= 2048 && !BWD) return sv_launch<BWD, CODEC, 256, 8>(p, st);
+  if (nc <= 2048) return sv_launch<BWD, CODEC, 256, 8>(p, st);
   return sv_launch<BWD, CODEC, 256, 0>(p, st);
 }
 
