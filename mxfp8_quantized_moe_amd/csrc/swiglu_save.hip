@@ -63,6 +63,22 @@ __device__ __forceinline__ float sv_most(float m, const float (&f)[8]) {
   return m;
 }
 
+// e^-|g| and from it sigmoid(g) and its complement sigmoid(-g), both with their own digits (1 - s keeps none where s nears
+// 1). -|g| log2(e) is taken as a rounded product t and the rest of it, which the product rule of the exponential puts
+// back: within 2 ulp, in half the instructions of expf, whose checks for overflow cannot act here (the kernels are bound
+// by their arithmetic: 46 instructions a value before).
+__device__ __forceinline__ void sv_sigmoid(float g, float& s, float& n) {
+  const float x = fmaxf(-fabsf(g), -104.0f);                  // below, e^x is 0 in fp32
+  const float t = x * 1.44269504f;
+  const float rest = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e * rest, 0.693147182f, e);
+  const float rc = __builtin_amdgcn_rcpf(1.0f + e), er = e * rc;   // the denominator lies in [1, 2]
+  const bool pos = g >= 0.0f;
+  s = pos ? rc : er;
+  n = pos ? er : rc;
+}
+
 // Keeps chunk c of a row's MX form; the four lanes of a block call it together.
 __device__ __forceinline__ void sv_keep(const u32x4& v, int rule, uint8_t* q, uint8_t* s, int64_t c) {
   uint32_t m = pk_absmax_bf16(pk_absmax_bf16(0u, v.x), v.y);
@@ -115,7 +131,11 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(SaveArgs p) {
     sv_unpack(g, gf);
     sv_unpack(u, uf);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) a[k] = gf[k] * sw_sigmoid(gf[k]) * uf[k];
+    for (int k = 0; k < 8; ++k) {
+      float s, n;
+      sv_sigmoid(gf[k], s, n);
+      a[k] = gf[k] * s * uf[k];
+    }
   };
   auto first = [&](const u32x4& g, const u32x4& u, int c, float (&a)[8]) {
     sv_keep(g, p.rule, hq, hs, c);
@@ -130,7 +150,6 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(SaveArgs p) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = i * TPR + lt;
-      gv[i] = uv[i] = u32x4{0, 0, 0, 0};
       if (valid && c < nc) {
         gv[i] = gr[c];
         uv[i] = ur[c];
@@ -194,9 +213,9 @@ __global__ __launch_bounds__(256) void swiglu_saved_bwd_kernel(SaveArgs p) {
     sv_values(u, (uint8_t)eu, uf);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // the sigmoid and its complement both from the exponential: 1 - s would keep no digit where s nears 1
-      const float e = expf(-fabsf(gf[k])), rc = __builtin_amdgcn_rcpf(1.0f + e);
-      const float s = (gf[k] >= 0.0f ? 1.0f : e) * rc, n = (gf[k] >= 0.0f ? e : 1.0f) * rc, gs_ = gf[k] * s;
+      float s, n;
+      sv_sigmoid(gf[k], s, n);
+      const float gs_ = gf[k] * s;
       dg[k] = df[k] * uf[k] * s * (1.0f + gf[k] * n);
       du[k] = df[k] * gs_;
       a[k] = gs_ * uf[k];
