@@ -177,14 +177,17 @@ struct FewDot {
   static __device__ __forceinline__ int lane_of(int c, int m, int q) { return 16 * (q * (4 / Q) + c % (4 / Q)) + q * ROWS + m; }
 };
 
-// Calls f(NB, Q) for n tokens (1 .. 64): up to 16 tokens in blocks of 16 / Q with Q chunks, more in blocks of 16.
-template <typename Fn>
+// Calls f(NB, Q) for n tokens (1 .. 64) and NT tiles: up to 16 tokens in blocks of 16 / Q with Q chunks, more in blocks
+// of 16 (four tiles: parts of four rows would be 16 accumulators of their own).
+template <int NT, typename Fn>
 __device__ __forceinline__ void few_blocks(int n, Fn&& f) {
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
-  if (n <= 4) f(I1{}, I4{});
-  else if (n <= 8) f(I1{}, I2{});
+  if constexpr (NT == 2) {
+    if (n <= 4) return f(I1{}, I4{});
+  }
+  if (n <= 8) f(I1{}, I2{});
   else if (n <= 16) f(I2{}, I2{});
   else if (n <= 32) f(I2{}, I1{});
   else f(I4{}, I1{});

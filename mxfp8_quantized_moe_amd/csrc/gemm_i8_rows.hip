@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
     w[h] = few_tile<kFewInt8Both>(p.b, nullptr, row + 16 * h, rows, p.K);
     sq[h] = *reinterpret_cast<const few_f4u*>(p.sb + row + 16 * h + 4 * (lane >> 4));
   }
-  few_blocks(n, [&](auto nb_tag, auto q_tag) {
+  few_blocks<NT>(n, [&](auto nb_tag, auto q_tag) {
     constexpr int NB = decltype(nb_tag)::value, Q = decltype(q_tag)::value;
     using Dot = FewDot<kFewInt8Both, NT, NB, Q, STREAM>;
     uint32_t x[NB];

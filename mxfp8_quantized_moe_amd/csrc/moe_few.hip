@@ -167,24 +167,25 @@ __device__ __forceinline__ void few_store_agent16(float* to, few_v4f v) {
   asm volatile("global_store_dwordx4 %0, %1, off sc1" ::"v"(to), "v"(v) : "memory");
 }
 
-// A workgroup takes two tiles of 16 weight rows of one expert for all its tokens; its W waves split the
+// A workgroup takes NT (2 or 4) tiles of 16 weight rows of one expert for all its tokens; its W waves split the
 // contraction and add up through LDS.
 //
-// UP: 16 gate rows and the matching up rows of W1; writes 16 columns of a = silu(g) * u.  Behind the
+// UP: gate rows and the matching up rows of W1; writes 8 NT columns of a = silu(g) * u.  Behind the
 // tiles' workgroups one for each rank writes the expert's list for the second kernel, and one more the counters
 // and the slots' marks.
 //
-// Else 32 rows of W2: 32 columns of each token's product, times its weight, go to the slot's row of `part`; the
+// Else 16 NT rows of W2: as many columns of each token's product, times its weight, go to the slot's row of `part`; the
 // last workgroup that is through with these columns adds up each token's slots in order and writes y.  Rows of part
 // are written and read past the caches of an XCD (agent scope), and a workgroup's stores have reached memory before
 // it counts itself, each column range on a cache line of its own; which one is last changes nothing.
-template <int FMT, bool UP, int W, bool STREAM>
+template <int FMT, bool UP, int W, int NT, bool STREAM>
 __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
-  __shared__ few_v4f red[W][8][64];
+  constexpr int PAIRS = NT / 2, COLS = UP ? 16 * PAIRS : 16 * NT;   // columns of the result
+  __shared__ few_v4f red[W][4 * NT][64];
   __shared__ FewIds ids;
   __shared__ FewList lists[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles = UP ? p.F / 16 : (p.K + 31) / 32;
+  const int N = UP ? p.F : p.K, tiles = (N + COLS - 1) / COLS;
   const int rank = blockIdx.x / tiles, tile = blockIdx.x - rank * tiles;
   const int L = UP ? p.K : p.F;
   FewList& list = lists[wave];
@@ -226,23 +227,27 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
     few_wave_sync();
   }
   if (UP || n > 0) {
-    const int64_t row = UP ? (int64_t)e * 2 * p.F + tile * 16 : (int64_t)e * p.K + tile * 32;   // first weight row
-    const bool two = UP || tile * 32 + 16 < p.K;                                                // K may end behind one tile
-    const int64_t row2 = UP ? row + p.F : two ? row + 16 : row;
+    const int64_t row0 = (int64_t)e * (UP ? 2 * p.F : p.K);   // the expert's first weight row
     const int64_t rows = (int64_t)p.E * (UP ? 2 * p.F : p.K);
     const uint8_t* const wp = UP ? p.w1 : p.w2;
     const void* const sp = UP ? p.s1 : p.s2;
-    const FewTile w[2] = {few_tile<FMT>(wp, sp, row, rows, L), few_tile<FMT>(wp, sp, row2, rows, L)};
     // a lane will write four columns of each tile: c .. c + 3
     const int c = 4 * (lane >> 4);
-    few_v4f div[2] = {{1.0f, 1.0f, 1.0f, 1.0f}, {1.0f, 1.0f, 1.0f, 1.0f}};
-    if constexpr (FMT == kFewFp8 || FMT == kFewInt8) {
-      div[0] = *reinterpret_cast<const few_f4u*>(static_cast<const float*>(sp) + row + c);
-      div[1] = *reinterpret_cast<const few_f4u*>(static_cast<const float*>(sp) + row2 + c);
+    FewTile w[NT];
+    few_v4f div[NT];
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      // tile h's first row in the expert; a tile behind the last one is the first again, and not written
+      const int col = UP ? 16 * (tile * PAIRS + h / 2) : 16 * (tile * NT + h);
+      const int64_t row = row0 + (col < N ? col : 0) + (UP && (h & 1) ? p.F : 0);
+      w[h] = few_tile<FMT>(wp, sp, row, rows, L);
+      div[h] = few_v4f{1.0f, 1.0f, 1.0f, 1.0f};
+      if constexpr (FMT == kFewFp8 || FMT == kFewInt8)
+        div[h] = *reinterpret_cast<const few_f4u*>(static_cast<const float*>(sp) + row + c);
     }
-    few_blocks(n, [&](auto nb_tag, auto q_tag) {
+    few_blocks<NT>(n, [&](auto nb_tag, auto q_tag) {
       constexpr int NB = decltype(nb_tag)::value, Q = decltype(q_tag)::value;
-      using Dot = FewDot<FMT, 2, NB, Q, STREAM>;
+      using Dot = FewDot<FMT, NT, NB, Q, STREAM>;
       uint32_t x[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -257,16 +262,20 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) red[wave][r * NB + b][lane] = d.acc[r][b];
       __syncthreads();
-      // a lane takes token 16 i + (l & 15), columns 4 (l >> 4) .. + 3 of the tiles
-      for (int i = wave; i < (NB * Dot::ROWS + 15) / 16; i += W) {
-        const int m = 16 * i + (lane & 15), cq = lane >> 4, b = m / Dot::ROWS;
-        if (m >= n) continue;
-        few_v4f g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+      // a lane takes token 16 i + (l & 15), columns 4 (l >> 4) .. + 3 of the tiles, two tiles at a time
+      for (int i = wave; i < (NB * Dot::ROWS + 15) / 16 * PAIRS; i += W) {
+        const int m = 16 * (i / PAIRS) + (lane & 15), cq = lane >> 4, b = m / Dot::ROWS;
+        const int col = 16 * (UP ? 1 : 2) * (tile * PAIRS + i % PAIRS);   // first column of the pair
+        if (m >= n || col >= N) continue;
+        few_v4f g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g, dg = div[0], du = div[1];
+        if constexpr (PAIRS > 1) {
+          if (i % PAIRS) dg = div[2], du = div[3];
+        }
 #pragma unroll
         for (int v = 0; v < W; ++v)
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            const int from = Dot::lane_of(cq, m % Dot::ROWS, q), r = cq / (4 / Q);
+            const int from = Dot::lane_of(cq, m % Dot::ROWS, q), r = 2 * Q * (i % PAIRS) + cq / (4 / Q);
             g += red[v][r * NB + b][from];
             u += red[v][(Q + r) * NB + b][from];
           }
@@ -275,20 +284,20 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
           float a[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float gj = __fdiv_rn(g[j], div[0][j]), uj = __fdiv_rn(u[j], div[1][j]);
+            const float gj = __fdiv_rn(g[j], dg[j]), uj = __fdiv_rn(u[j], du[j]);
             a[j] = gj * sw_sigmoid(gj) * uj;
           }
-          *reinterpret_cast<u32x2*>(p.a2 + (int64_t)slot * p.F + tile * 16 + c) = u32x2{sw_pack(a[0], a[1]), sw_pack(a[2], a[3])};
+          *reinterpret_cast<u32x2*>(p.a2 + (int64_t)slot * p.F + col + c) = u32x2{sw_pack(a[0], a[1]), sw_pack(a[2], a[3])};
         } else {
-          float* o = p.part + (int64_t)slot * p.K + tile * 32 + c;
+          float* o = p.part + (int64_t)slot * p.K + col + c;
           const float wt = list.w[m];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            g[j] = wt * __fdiv_rn(g[j], div[0][j]);
-            u[j] = wt * __fdiv_rn(u[j], div[1][j]);
+            g[j] = wt * __fdiv_rn(g[j], dg[j]);
+            u[j] = wt * __fdiv_rn(u[j], du[j]);
           }
           few_store_agent16(o, g);
-          if (two) few_store_agent16(o + 16, u);
+          if (col + 16 < N) few_store_agent16(o + 16, u);
         }
       }
     });
@@ -302,8 +311,8 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
     __syncthreads();
     if (!s_last) return;
     // two columns a thread: four bytes of y
-    for (int i = threadIdx.x; i < p.T * 16; i += 64 * W) {
-      const int t = i >> 4, col = tile * 32 + 2 * (i & 15);
+    for (int i = threadIdx.x; i < p.T * (COLS / 2); i += 64 * W) {
+      const int t = i / (COLS / 2), col = tile * COLS + 2 * (i % (COLS / 2));
       if (col >= p.K) continue;
       float a = 0.0f, b = 0.0f;
 #pragma unroll 8
@@ -328,17 +337,25 @@ __global__ __launch_bounds__(256) void few_zero_kernel(uint32_t* y, int64_t n) {
 
 template <int FMT, bool UP>
 static hipError_t few_launch(const FewParams& p, hipStream_t st) {
-  const int64_t blocks = (int64_t)p.ranks * (UP ? p.F / 16 : (p.K + 31) / 32);
+  // Four tiles a workgroup share the activations' loads, which outgrow the weights' from some 16 tokens an expert on, where
+  // the workgroups still fill the GPU (64 tokens, eight of 16 experts 5120 x 8192: first kernel 593 -> 448 us, second 303 ->
+  // 238; 64 tokens of one expert 4096 x 8192: first, 256 workgroups, 43 -> 35 us, second, 64 workgroups, 41 -> 63;
+  // eight tokens an expert: none to 6% slower).
+  auto count = [&](int cols) { return (int64_t)p.ranks * (((UP ? p.F : p.K) + cols - 1) / cols); };
+  constexpr int COLS = UP ? 16 : 32;
+  const bool wide = (int64_t)p.T * p.topk >= 16 * (int64_t)p.E && count(2 * COLS) >= 224;
+  const int64_t blocks = count(wide ? 2 * COLS : COLS);
   const dim3 grid((unsigned)(blocks + (UP ? p.ranks + 1 : 0)));
   // Short rows leave four waves a step or two each: two waves where the workgroups fill the GPU by themselves
   // (64 tokens of 64 experts 2048 x 1408: first kernel 75 -> 68 us; rows of 7168: 149 -> 154 us).
-  const bool two = (UP ? p.K : p.F) <= 2048 && blocks >= 512;
+  const bool two = !wide && (UP ? p.K : p.F) <= 2048 && blocks >= 512;
   // Streamed loads where the experts' weights are beyond the last-level cache (64 tokens of 32 experts 7168 x 2048, 1.4 GB:
   // first kernel 153 -> 144 us); weights that stay there from one call to the next are not (4 tokens of 7 experts
   // 1040 x 336, 7 MB: 11.9 us streamed, 5.8 not).
   const bool stream = (int64_t)p.E * 3 * p.K * p.F > (256ll << 20);
-  auto kern = stream ? (two ? few_kernel<FMT, UP, 2, true> : few_kernel<FMT, UP, 4, true>)
-                     : (two ? few_kernel<FMT, UP, 2, false> : few_kernel<FMT, UP, 4, false>);
+  auto kern = wide ? few_kernel<FMT, UP, 4, 4, false>
+              : stream ? (two ? few_kernel<FMT, UP, 2, 2, true> : few_kernel<FMT, UP, 4, 2, true>)
+                       : (two ? few_kernel<FMT, UP, 2, 2, false> : few_kernel<FMT, UP, 4, 2, false>);
   hipLaunchKernelGGL(kern, grid, dim3(two ? 128 : 256), 0, st, p);
   return hipGetLastError();
 }

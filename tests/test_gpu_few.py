@@ -75,6 +75,7 @@ def choices(rng, T, k, E, kind):
     (1, 1, 1, 32, 32, "distinct"), (1, 6, 64, 256, 96, "distinct"), (2, 2, 3, 96, 160, "wild"), (5, 3, 7, 1056, 352, "wild"),
     (16, 2, 4, 128, 64, "one"), (17, 1, 5, 192, 128, "one"), (33, 4, 6, 320, 224, "wild"), (64, 8, 40, 512, 256, "distinct"),
     (64, 2, 3, 64, 2080, "one"), (48, 1, 2, 2080, 64, "distinct"), (64, 16, 1024, 64, 32, "wild"), (3, 300, 200, 64, 64, "wild"),
+    (20, 2, 2, 7200, 96, "one"), (64, 3, 8, 1824, 928, "wild"), (40, 1, 2, 96, 3616, "distinct"), (64, 1, 1, 7168, 32, "one"),
 ])
 def test_against_fp64(T, k, E, K, F, kind, fmt):
     note(f"moe_few_tokens {fmt} T {T} topk {k} E {E} K {K} F {F} {kind}")
