@@ -337,13 +337,13 @@ __global__ __launch_bounds__(256) void few_zero_kernel(uint32_t* y, int64_t n) {
 
 template <int FMT, bool UP>
 static hipError_t few_launch(const FewParams& p, hipStream_t st) {
-  // Four tiles a workgroup share the activations' loads, which outgrow the weights' from some 16 tokens an expert on, where
+  // Four tiles a workgroup share the activations' loads, which outgrow the weights' beyond some 16 tokens an expert, where
   // the workgroups still fill the GPU (64 tokens, eight of 16 experts 5120 x 8192: first kernel 593 -> 448 us, second 303 ->
   // 238; 64 tokens of one expert 4096 x 8192: first, 256 workgroups, 43 -> 35 us, second, 64 workgroups, 41 -> 63;
-  // eight tokens an expert: none to 6% slower).
+  // four tokens an expert of 32, 7168 x 2048, the others' ids none: both 231 -> 249).
   auto count = [&](int cols) { return (int64_t)p.ranks * (((UP ? p.F : p.K) + cols - 1) / cols); };
   constexpr int COLS = UP ? 16 : 32;
-  const bool wide = (int64_t)p.T * p.topk >= 16 * (int64_t)p.E && count(2 * COLS) >= 224;
+  const bool wide = (int64_t)p.T * p.topk > 16 * (int64_t)p.E && count(2 * COLS) >= 224;
   const int64_t blocks = count(wide ? 2 * COLS : COLS);
   const dim3 grid((unsigned)(blocks + (UP ? p.ranks + 1 : 0)));
   // Short rows leave four waves a step or two each: two waves where the workgroups fill the GPU by themselves
