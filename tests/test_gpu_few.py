@@ -9,7 +9,7 @@ from oracle import few as of
 from oracle import codec as oc
 from oracle.quant import bf16_to_f32
 from oracle.swiglu import round_bf16
-from gpu_helpers import DEV, note, bf16_dev, i32_dev, host, bf16_bits_to_f64
+from gpu_helpers import DEV, note, bf16_dev, i32_dev, host, bf16_bits_to_f64, e8m0_rows_to_k4
 
 pytestmark = pytest.mark.gpu
 
@@ -153,6 +153,71 @@ def test_scales_at_the_ends():
     layer.v1, layer.v2 = dec(q1, s1, 2 * F, K), dec(q2, s2, K, F)
     ids, w = choices(rng, T, 2, E, "distinct")
     layer.check(round_bf16(rng.standard_normal((T, K))), ids, w)
+
+
+@pytest.mark.parametrize("k4", [False, True])
+def test_every_code_under_every_scale(k4):
+    """One token, one expert, one value of the activation that is exactly 1 (gate 256, up 2^-8): y is W2's first column, every
+    e4m3 code under every e8m0 scale up to 2^119. Exact where bf16 is normal; below 2^-126, zero or bf16's spacing."""
+    note(f"moe_few_tokens MX codes and scales k4 {k4}")
+    K, F = 247 * 256, 32
+    w1, s1 = np.zeros((1, 2 * F, K), np.uint8), np.zeros((2 * F, K // 32), np.uint8)
+    w1[0, 0, 0], s1[0, 0] = 0x78, 127                       # 256
+    w1[0, F, 0], s1[F, 0] = 0x38, 119                       # 2^-8
+    codes, scales = np.tile(np.arange(256), 247).astype(np.uint8), np.repeat(np.arange(247), 256).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0                       # the NaN codes
+    w2 = np.zeros((1, K, F), np.uint8)
+    w2[0, :, 0] = codes
+    lay = e8m0_rows_to_k4 if k4 else (lambda v: v)
+    dev = lambda v: torch.from_numpy(np.ascontiguousarray(v)).to(DEV)
+    x = np.zeros((1, K), np.uint16)
+    x[0, 0] = 0x3F80
+    y = fm.moe_few_tokens(bf16_dev(x), i32_dev([[0]]), torch.ones(1, 1, device=DEV), dev(w1), dev(lay(s1)), dev(w2),
+                          dev(lay(scales[:, None])), scale_kind=fm.SCALE_E8M0_K4 if k4 else fm.SCALE_E8M0)
+    got = bf16_bits_to_f64(host(y))[0]
+    want = np.ldexp(oc.decode(codes, 0), scales.astype(int) - 127)
+    normal = np.abs(want) >= 2.0 ** -126
+    assert (got[normal] == want[normal]).all()
+    assert (np.abs(got - want)[~normal] <= np.maximum(np.abs(want[~normal]), 2.0 ** -133)).all()
+
+
+def test_every_whole_number():
+    """The same with integer weights: every byte, -128 among them."""
+    note("moe_few_tokens int8 bytes")
+    K, F = 256, 16
+    w1, w2 = np.zeros((1, 2 * F, K), np.int8), np.zeros((1, K, F), np.int8)
+    w1[0, 0, 0], w1[0, F, 0] = 64, 1
+    w2[0, :, 0] = np.arange(-128, 128)
+    s1, s2 = np.ones((1, 2 * F), np.float32), np.ones((1, K), np.float32)
+    s1[0, F] = 64
+    dev = lambda v: torch.from_numpy(np.ascontiguousarray(v)).to(DEV)
+    x = np.zeros((1, K), np.uint16)
+    x[0, 0] = 0x3F80
+    y = fm.moe_few_tokens(bf16_dev(x), i32_dev([[0]]), torch.ones(1, 1, device=DEV), dev(w1), dev(s1), dev(w2), dev(s2),
+                          w_fmt=fm.OPD_INT8)
+    assert (bf16_bits_to_f64(host(y))[0] == np.arange(-128, 128)).all()
+
+
+def test_what_must_not_be_read():
+    """NaN in experts nobody chose, in weights of slots without an expert and all over the workspace reaches no output; one
+    workspace serves calls of different sizes one after the other."""
+    note("moe_few_tokens workspace and unread NaN")
+    rng = np.random.default_rng(11)
+    E, K, F = 6, 96, 64
+    layer = Layer(rng, E, K, F, "fp8")
+    q1, q2 = layer.w1.clone(), layer.w2.clone()
+    q1[4:], q2[4:] = 0x7F, 0x7F
+    layer.w1, layer.w2 = q1, q2
+    ws = torch.full((fm.moe_few_tokens_workspace_bytes(64, 8, K, F),), 0xFF, dtype=torch.uint8, device=DEV)
+    for T, k, kind in [(64, 8, "wild"), (3, 2, "distinct"), (40, 1, "one"), (1, 8, "wild"), (64, 8, "wild")]:
+        ids, w = choices(rng, T, k, 4, kind) if kind != "wild" else (rng.integers(-2, 4, (T, k)).astype(np.int32),
+                                                                    rng.standard_normal((T, k)).astype(np.float32))
+        w = np.where(ids < 0, np.float32("nan"), w).astype(np.float32)
+        ref_w = np.where(ids < 0, 0, w).astype(np.float32)
+        x = bf16_dev(round_bf16(rng.standard_normal((T, K))))
+        y = layer(x, i32_dev(ids), torch.from_numpy(w).to(DEV), workspace=ws)
+        ref = layer(x, i32_dev(ids), torch.from_numpy(ref_w).to(DEV))
+        assert torch.isfinite(y).all() and torch.equal(y, ref)
 
 
 @pytest.mark.parametrize("fmt", ["fp8", "int8"])

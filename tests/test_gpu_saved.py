@@ -160,6 +160,27 @@ def test_mx_forms(R, F, offs, rule, layout):
         assert torch.equal(copies[0], copies[1]), name
 
 
+def test_every_code_under_every_scale():
+    """Gate 256 (its silu is 256 exactly): the activation is 256 times the kept up value, every e4m3 code under every e8m0
+    scale up to 2^111, in both recipes. Exact where bf16 is normal; below 2^-126, zero or bf16's spacing."""
+    note("kept SwiGLU codes and scales")
+    R, F = 239, 256
+    hq, hs = np.full((R, 2 * F), 0x78, np.uint8), np.full((R, 2 * F // 32), 127, np.uint8)
+    codes = np.arange(256).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0                       # the NaN codes
+    hq[:, F:], hs[:, F // 32:] = codes, np.arange(R)[:, None]
+    want = 256 * np.ldexp(np.tile(oc.decode(codes, 0), (R, 1)), np.arange(R)[:, None] - 127)
+    d = bf16_dev(np.zeros((R, F), np.uint16))
+    rowwise = fm.swiglu_backward_quantize_rowwise_saved(d, u8_dev(hq), u8_dev(hs), codes=False, want_a2=True)[3]
+    mx = torch.empty(R, F, dtype=torch.bfloat16, device=DEV)
+    fm.swiglu_quantize_mx_dual_saved(u8_dev(hq), u8_dev(hs), i32_dev([R]), a2=mx)
+    for got in (rowwise, mx):
+        got = bf16_bits_to_f64(host(got))
+        normal = np.abs(want) >= 2.0 ** -118                # the kept value itself normal in bf16
+        assert (got[normal] == want[normal]).all()
+        assert (np.abs(got - want)[~normal] <= np.maximum(np.abs(want[~normal]), 2.0 ** -125)).all()
+
+
 def test_no_rows():
     note("kept SwiGLU without rows")
     h = torch.empty(0, 128, dtype=torch.bfloat16, device=DEV)
