@@ -36,6 +36,9 @@ __device__ __forceinline__ void dma_1(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, dst, 1, 0, 0);
 }
 
+// 16 bytes at any address of an element (global stores need no alignment on gfx950).
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // 16-byte store of output the kernel never reads back: streamed (non-temporal),
 // so finished tiles do not displace operand lines in L2 and leave less dirty
 // data behind for the kernels that follow.

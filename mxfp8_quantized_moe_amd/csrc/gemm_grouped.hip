@@ -1197,7 +1197,11 @@ void gemm_fp8_pipe(KParams p) {
   const int64_t out_base = cur.out_base;
   const float keep = c_hi > c_lo ? 1.0f : 0.0f;
   constexpr int ELEM = OUT == 0 ? 2 : 4;
-  if ((out_ld * ELEM) % 16 == 0) {
+  // Integer operands stage every result; rows that do not begin on 16 bytes take
+  // stores of 16 bytes at any address, kept in L2, where a line's parts meet
+  // (element stores: 4700 rows in 33 groups, 144 to 6103 columns, 107 us).
+  const bool aligned = (out_ld * ELEM) % 16 == 0;
+  if (I8 || aligned) {
     // Lane indices from a fresh opaque copy of the thread index: values kept
     // across the k loop may be spilled, and a reload would wait for the
     // stages now in flight.
@@ -1245,10 +1249,19 @@ void gemm_fp8_pipe(KParams p) {
       const int c = wn * WNE + PC * jp + VEC * k;
       uint8_t* const row0 = static_cast<uint8_t*>(p.out) +
                             (out_base + (int64_t)(wm * WM + 32 * i + rr) * out_ld + c) * ELEM;
+      auto store16 = [&](uint8_t* dst, u32x4 v) {
+        if constexpr (I8) {
+          if (!aligned) {
+            *reinterpret_cast<u32x4_any*>(dst) = u32x4_any{v.x, v.y, v.z, v.w};
+            return;
+          }
+        }
+        store_stream16(dst, v);
+      };
       if (full) {
 #pragma unroll
         for (int itr = 0; itr < 4; ++itr)
-          store_stream16(row0 + (int64_t)itr * 8 * out_ld * ELEM, __builtin_bit_cast(u32x4, dv[d][itr]));
+          store16(row0 + (int64_t)itr * 8 * out_ld * ELEM, __builtin_bit_cast(u32x4, dv[d][itr]));
         return;
       }
 #pragma unroll
@@ -1258,7 +1271,7 @@ void gemm_fp8_pipe(KParams p) {
         uint8_t* dst = row0 + (int64_t)itr * 8 * out_ld * ELEM;
         const lds_u4 dd = dv[d][itr];
         if (c + VEC <= q_valid) {
-          store_stream16(dst, __builtin_bit_cast(u32x4, dd));
+          store16(dst, __builtin_bit_cast(u32x4, dd));
         } else {
           const uint32_t w[4] = {dd.x, dd.y, dd.z, dd.w};
 #pragma unroll
