@@ -80,33 +80,42 @@ __device__ __forceinline__ FewTile few_tile(const uint8_t* w, const void* s, int
   else return FewTile{w + row * L, nullptr, 0};
 }
 
-// Products of NT tiles of 16 weight rows with the tokens of an expert, over the steps [s0, s1) of 64 Q
-// contraction values of rows of length L (a multiple of 16; a step that passes it loads a valid chunk again and
-// multiplies it by zero).
+// Products of NT tiles of 16 weight rows with the tokens of an expert, over a wave's steps of 64 Q contraction values of
+// rows of length L (a multiple of 16; a step that passes it loads a valid chunk again and multiplies it by zero).
 //
 // Q = 1: a tile is the instruction's 16 rows, NB blocks of 16 tokens its columns; a load takes 64 bytes of each
-// row.  Q = 2, 4 (up to 16 / Q tokens): a tile is Q parts of 16 / Q rows, and an instruction takes a part's rows Q times,
-// each time with another of Q neighbouring chunks of 64 bytes, and the tokens with those chunks in its
-// columns.  Of the result the Q blocks on the diagonal are products of one chunk; their sum is the answer, the rest
-// is not used.  A load then takes 64 Q bytes of a row together, whole cache lines, and the activations' loads are shared by
-// the parts: a Q-th of them.
+// row.  Q = 2, 4 (blocks of 16 / Q tokens): a tile is Q parts of 16 / Q rows, and an instruction takes each of a part's rows
+// Q times, in neighbouring lanes with neighbouring chunks of 16 bytes, and each token's chunks in Q neighbouring
+// columns.  Of the result only products of a row's q-th chunks with a token's q-th are of use; the sum over q, of
+// neighbouring lanes, is the answer.  A load then takes 64 Q bytes of a row, whole cache lines, and the activations' loads
+// are shared by the parts.  The address unit takes four lanes a cycle where they lie in one line, and one or two where they
+// do not, which is what bounds the loads of a CU: with a row's chunks 16 lanes apart 16 rows of 5120 x 5120 took 10.5 us,
+// this way 8.2.
+//
+// Part p has the rows p 4 / Q .. of each four, so that sums() leaves a lane four rows in order.
+//
+// W waves share the steps: ranges of them for Q > 1; for Q = 1 in turn, so that the other halves of the cache lines are
+// asked for at the same time, by the next wave (509 rows in 11 groups of 1999 x 2064 20 -> 18 us; with whole lines
+// 4 rows of 14336 x 4096 took 12.2 us in turn and 11.3 by ranges).
 //
 // STREAM: loads of whole cache lines are non-temporal, which leaves the activations in L2 (half lines that are streamed
 // would be fetched twice).
 template <int FMT, int NT, int NB, int Q, bool STREAM>
 struct FewDot {
-  static constexpr int ROWS = 16 / Q, PARTS = Q, R = NT * PARTS, STEP = 64 * Q;
+  static constexpr int ROWS = 16 / Q, PARTS = Q, R = NT * PARTS, STEP = 64 * Q, SUB = 4 / Q;
   static constexpr int U = R * NB >= 8 ? 1 : R * NB >= 4 ? 2 : 4;   // steps whose loads are in flight together
   using Acc = std::conditional_t<FMT == kFewInt8Both, few_v4i, few_v4f>;
   static constexpr int XB = FMT == kFewInt8Both ? 1 : 2;   // bytes of an activation
   Acc acc[R][NB];
 
   // x: byte offset of the lane's row of activations from `xb`
-  __device__ __forceinline__ void run(const FewTile (&tile)[NT], const void* xb, const uint32_t (&x)[NB], int L, int s0,
-                                      int s1) {
+  __device__ __forceinline__ void run(const FewTile (&tile)[NT], const void* xb, const uint32_t (&x)[NB], int L, int wave,
+                                      int W) {
+    const int all = (L + STEP - 1) / STEP, ds = Q == 1 ? W : 1;
+    const int s0 = Q == 1 ? wave : all * wave / W, s1 = Q == 1 ? all : all * (wave + 1) / W;
     const int lane = threadIdx.x & 63;
-    const int kl = 16 * (lane >> 4) + 64 * ((lane & 15) / ROWS);
-    const uint32_t row = (lane & 15) % ROWS;
+    const int kl = 16 * Q * (lane >> 4) + 16 * (lane % Q);
+    const uint32_t slot = (lane & 15) / Q, row = slot / SUB * 4 + slot % SUB;
     const uint32_t row_w = row * L, row_s = FMT == kFewMxK4 ? 4 * row : row * (L / 32);
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -118,15 +127,15 @@ struct FewDot {
       uint32_t e[U][R];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int kk = STEP * (s + u) + kl;
+        const int kk = STEP * (s + u * ds) + kl;
         const uint32_t k = WHOLE ? kk : min(kk, L - 16);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const FewTile& t = tile[r / PARTS];
-          wv[u][r] = few_load16<(STREAM && Q > 1)>(t.w + (int64_t)(r % PARTS) * ROWS * L, row_w + k);
-          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * ROWS * (L / 32))[row_s + (k >> 5)];
+          wv[u][r] = few_load16<(STREAM && Q > 1)>(t.w + (int64_t)(r % PARTS) * SUB * L, row_w + k);
+          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * SUB * (L / 32))[row_s + (k >> 5)];
           if constexpr (FMT == kFewMxK4)
-            e[u][r] = t.s[(int64_t)(k >> 7) * t.group + (row_s + (r % PARTS) * ROWS * 4 + ((k >> 5) & 3))];
+            e[u][r] = t.s[(int64_t)(k >> 7) * t.group + (row_s + (r % PARTS) * SUB * 4 + ((k >> 5) & 3))];
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -138,7 +147,7 @@ struct FewDot {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if constexpr (!WHOLE) {
-          const bool in = s + u < s1 && STEP * (s + u) + kl < L;
+          const bool in = s + u * ds < s1 && STEP * (s + u * ds) + kl < L;
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -154,31 +163,53 @@ struct FewDot {
                                                                 __builtin_bit_cast(few_v4i, xv[u][b][0]), acc[r][b], 0, 0, 0);
             continue;
           } else {
-          float sc = 1.0f;
-          if constexpr (FMT == kFewMx || FMT == kFewMxK4) sc = __uint_as_float(e[u][r] << 23);
-          const few_v8bf lo = few_bf16<FMT>(wv[u][r].x, wv[u][r].y, sc);
-          const few_v8bf hi = few_bf16<FMT>(wv[u][r].z, wv[u][r].w, sc);
+            float sc = 1.0f;
+            if constexpr (FMT == kFewMx || FMT == kFewMxK4) sc = __uint_as_float(e[u][r] << 23);
+            const few_v8bf lo = few_bf16<FMT>(wv[u][r].x, wv[u][r].y, sc);
+            const few_v8bf hi = few_bf16<FMT>(wv[u][r].z, wv[u][r].w, sc);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(few_v8bf, xv[u][b][0]), acc[r][b], 0, 0, 0);
-            acc[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(few_v8bf, xv[u][b][1]), acc[r][b], 0, 0, 0);
-          }
+            for (int b = 0; b < NB; ++b) {
+              acc[r][b] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, __builtin_bit_cast(few_v8bf, xv[u][b][0]), acc[r][b], 0, 0, 0);
+              acc[r][b] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, __builtin_bit_cast(few_v8bf, xv[u][b][1]), acc[r][b], 0, 0, 0);
+            }
           }
         }
       }
     };
     int s = s0;
-    for (; s + U <= s1 && STEP * (s + U) <= L; s += U) steps(s, std::true_type{});
-    for (; s < s1; s += U) steps(s, std::false_type{});
+    for (; s + (U - 1) * ds < s1 && STEP * (s + (U - 1) * ds + 1) <= L; s += U * ds) steps(s, std::true_type{});
+    for (; s < s1; s += U * ds) steps(s, std::false_type{});
   }
 
-  // The lane that holds rows 4 c .. 4 c + 3 of a tile (c = 0 .. 3) for token m of its block, of chunk q; the register
-  // is acc[tile * Q + c / (4 / Q)].
-  static __device__ __forceinline__ int lane_of(int c, int m, int q) { return 16 * (q * (4 / Q) + c % (4 / Q)) + q * ROWS + m; }
+  // Rows 4 (lane >> 4) .. + 3 of tile h for token (lane & 15) / Q of block b, in all lanes.
+  __device__ __forceinline__ Acc sums(int h, int b) const {
+    if constexpr (Q == 1) return acc[h][b];
+    const int q = threadIdx.x % Q;
+    Acc t;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      const Acc& a = acc[h * PARTS + p][b];
+      if constexpr (Q == 2) {
+        t[2 * p] = pair_sum<0xB1>(q ? a[1] : a[0]);
+        t[2 * p + 1] = pair_sum<0xB1>(q ? a[3] : a[2]);
+      } else if constexpr (Q == 4) {
+        t[p] = pair_sum<0x4E>(pair_sum<0xB1>(q & 2 ? (q & 1 ? a[3] : a[2]) : (q & 1 ? a[1] : a[0])));
+      }
+    }
+    return t;
+  }
+  // v plus the value of the lane that the quad permutation names: 0xB1 the neighbour, 0x4E the next but one.
+  template <int PERM, typename T>
+  static __device__ __forceinline__ T pair_sum(T v) {
+    return v + __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), PERM, 0xF, 0xF, true));
+  }
 };
 
-// Calls f(NB, Q) for n tokens (1 .. 64) and NT tiles: up to 16 tokens in blocks of 16 / Q with Q chunks, more in blocks
-// of 16 (four tiles: parts of four rows would be 16 accumulators of their own).
+// Calls f(NB, Q) for n tokens (1 .. 64) and NT tiles.  Whole lines (Q > 1) wherever their accumulators leave room for several
+// waves: two tiles up to 32 tokens (32 rows of 4096 x 4096: 14.4 -> 8.7 us), four up to 16; beyond that they would be 128
+// registers (64 rows in 64 groups, 2816 x 2048: 77 -> 128 us).
 template <int NT, typename Fn>
 __device__ __forceinline__ void few_blocks(int n, Fn&& f) {
   using I1 = std::integral_constant<int, 1>;
@@ -189,7 +220,7 @@ __device__ __forceinline__ void few_blocks(int n, Fn&& f) {
   }
   if (n <= 8) f(I1{}, I2{});
   else if (n <= 16) f(I2{}, I2{});
-  else if (n <= 32) f(I2{}, I1{});
+  else if (n <= 32) f(std::integral_constant<int, NT == 2 ? 4 : 2>{}, std::integral_constant<int, NT == 2 ? 2 : 1>{});
   else f(I4{}, I1{});
 }
 

@@ -4,7 +4,7 @@
 // With few rows the product is the read of the groups' weights. The persistent GEMM's
 // 256-column tiles are too few then to ask memory for enough at once (16 rows of 14336
 // columns of 4096: 56 workgroups on 256 CUs, 37 us; the weights at the copy rate take 11), so a
-// workgroup here takes 32 or 64 columns for up to 64 rows (14.6 us), its waves split the
+// workgroup here takes 32 or 64 columns for up to 64 rows (11.9 us), its waves split the
 // contraction, and the whole-number sums are added up through LDS. Sums are exact in any order and the
 // epilogue's operations are the persistent GEMM's, so both give the same bits.
 #include "few_dot.hpp"
@@ -45,50 +45,49 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
   const int e = __builtin_amdgcn_readfirstlane(un.e);
   const int m0 = __builtin_amdgcn_readfirstlane(un.lo + un.j * kUnitRows);
   const int n = min(kUnitRows, __builtin_amdgcn_readfirstlane(un.hi) - m0);
-  // a tile that N ends in starts earlier and leaves out the columns before `cn`
-  const int cn = tile * COLS, c0 = min(cn, p.N - COLS);
+  // A tile that N ends in starts earlier and leaves out the columns before `cn`; where N is below the tile's width (it is
+  // 16 or more) its later sixteens do.
+  const int cn = tile * COLS, c0 = max(0, min(cn, p.N - COLS));
   const int64_t row = (int64_t)e * p.N + c0, rows = (int64_t)p.E * p.N;
-  const int c = c0 + 4 * (lane >> 4);   // a lane writes columns c .. c + 3 of each tile of 16
+  int c[NT];   // of its h-th sixteen a lane writes columns c[h] .. c[h] + 3
   FewTile w[NT];
   few_f4u sq[NT];
 #pragma unroll
   for (int h = 0; h < NT; ++h) {
-    w[h] = few_tile<kFewInt8Both>(p.b, nullptr, row + 16 * h, rows, p.K);
-    sq[h] = *reinterpret_cast<const few_f4u*>(p.sb + row + 16 * h + 4 * (lane >> 4));
+    const int off = min(16 * h, p.N - c0 - 16);
+    c[h] = c0 + off + 4 * (lane >> 4);
+    w[h] = few_tile<kFewInt8Both>(p.b, nullptr, row + off, rows, p.K);
+    sq[h] = *reinterpret_cast<const few_f4u*>(p.sb + row + off + 4 * (lane >> 4));
   }
   few_blocks<NT>(n, [&](auto nb_tag, auto q_tag) {
     constexpr int NB = decltype(nb_tag)::value, Q = decltype(q_tag)::value;
     using Dot = FewDot<kFewInt8Both, NT, NB, Q, STREAM>;
     uint32_t x[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) x[b] = (uint32_t)(min(Dot::ROWS * b + (lane & 15) % Dot::ROWS, n - 1) * p.K);
-    const int steps = (p.K + Dot::STEP - 1) / Dot::STEP;
+    for (int b = 0; b < NB; ++b) x[b] = (uint32_t)(min(Dot::ROWS * b + (lane & 15) / Q, n - 1) * p.K);
     Dot d;
-    d.run(w, p.a + (int64_t)m0 * p.K, x, p.K, steps * wave / W, steps * (wave + 1) / W);
+    d.run(w, p.a + (int64_t)m0 * p.K, x, p.K, wave, W);
 #pragma unroll
-    for (int r = 0; r < Dot::R; ++r)
+    for (int h = 0; h < NT; ++h)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) red[wave][r * NB + b][lane] = d.acc[r][b];
+      for (int b = 0; b < NB; ++b) red[wave][h * NB + b][lane] = d.sums(h, b);
     __syncthreads();
     for (int i = wave; i < (NB * Dot::ROWS + 15) / 16; i += W) {
-      const int m = 16 * i + (lane & 15), cq = lane >> 4, b = m / Dot::ROWS;
+      const int m = 16 * i + (lane & 15), b = m / Dot::ROWS;
       if (m >= n) continue;
       const float inv_p = __frcp_rn(p.sa[m0 + m]);
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         few_v4i s = {0, 0, 0, 0};
 #pragma unroll
-        for (int v = 0; v < W; ++v)
-#pragma unroll
-          for (int q = 0; q < Q; ++q)
-            s += red[v][(h * Q + cq / (4 / Q)) * NB + b][Dot::lane_of(cq, m % Dot::ROWS, q)];
+        for (int v = 0; v < W; ++v) s += red[v][h * NB + b][16 * (lane >> 4) + Q * (m % Dot::ROWS)];
         float o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = (float)s[j] * inv_p * __frcp_rn(sq[h][j]);
-        const int col = c + 16 * h;
+        const int col = c[h], first = max(cn, c0 + 16 * h);
         const int64_t at = (int64_t)(m0 + m) * p.N + col;
-        if ((p.N * (OUT == 0 ? 2 : 4)) % 16 == 0) {   // then cn - c0 is a multiple of four
-          if (col < cn) continue;
+        if ((p.N * (OUT == 0 ? 2 : 4)) % 16 == 0) {   // then c0 and `first` are multiples of four
+          if (col < first) continue;
           if constexpr (OUT == 0)
             *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + at) = u32x2{few_pack(o[0], o[1]), few_pack(o[2], o[3])};
           else
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (col + j < cn) continue;
+            if (col + j < first) continue;
             if constexpr (OUT == 0) static_cast<__bf16*>(p.out)[at + j] = (__bf16)o[j];
             else static_cast<float*>(p.out)[at + j] = o[j];
           }
@@ -109,14 +108,16 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
 }  // namespace
 
 // When this kernel is taken, by the persistent GEMM's tiles of 256 columns (one for each group with rows). They fill the
-// GPU: up to eight rows a group (64 groups, 2816 x 2048: 384 rows 60 us here, 72 there; 1024 rows 81 and 72). They do not:
-// their time is one pass along K whatever the rows are, while the activations' loads here grow with them (14336 x 4096,
-// one group: 16 rows 14.6 and 37 us, 128 rows 34 and 40, 192 rows 49 and 46; 200 rows of 4096 x 1024 8.5 and 20; 509 rows in
-// 11 groups of 1999 x 2064 20 and 26).
+// GPU: up to 16 rows a group (64 groups, 2816 x 2048: 512 rows of 1408 37 us here, 44 there; 1024 rows 71 and 72; 1500 rows 75
+// and 73; 1000 rows of 32 groups 53 and 44). They do not: their time is one pass along K whatever the rows are, while the
+// activations' loads here grow with them (14336 x 4096, one group: 16 rows 12 and 40 us, 128 rows 34 and 43, 160 rows 54 and
+// 47; 4096 x 4096: 400 rows 33 and 45, 600 rows 48 and 44; 2000 rows of 1024 x 2048 20 and 28, 2048 rows in 8 groups 28 and
+// 19), and a short pass leaves its beginning and end (16080 rows of 177 x 400 13 and 18; 447 of 10756 x 288 19 and 18).
 bool i8_rows_wanted(const GemmArgs& g) {
-  if (g.N < 32) return false;
+  if (g.N < 16) return false;
   const int64_t groups = std::min<int64_t>(g.n_groups, g.M);
-  return g.M <= 8 * (int64_t)g.n_groups || (groups * ((g.N + 255) / 256) < 256 && (g.M + 64 * groups) * g.N <= 3000000);
+  return g.M <= 16 * (int64_t)g.n_groups ||
+         (groups * ((g.N + 255) / 256) < 256 && (g.M + 32 * groups) * g.N <= (g.K <= 512 ? 4000000 : 2300000));
 }
 
 template <int NT>
@@ -138,9 +139,11 @@ static hipError_t i8_rows(const GemmArgs& g, hipStream_t st) {
 }
 
 hipError_t launch_i8_rows(const GemmArgs& g, hipStream_t st) {
-  // Wider tiles share the activations' loads: 64 columns for more than 16 rows a group (64 rows of 14336 x 4096 25 -> 20 us;
-  // 4 rows 12.8 -> 15).
-  return g.N >= 64 && g.M > 16 * std::min<int64_t>(g.n_groups, g.M) ? i8_rows<4>(g, st) : i8_rows<2>(g, st);
+  // Wider tiles share the activations' loads: 64 columns for more than 32 rows a group where their workgroups fill the GPU
+  // (64 rows of 14336 x 4096 25 -> 19 us, 1000 of 1024 x 4096 25 -> 19; 32 of 14336 13 -> 15, 500 of 1024 14 -> 18).
+  const int64_t groups = std::min<int64_t>(g.n_groups, g.M);
+  return g.N >= 64 && g.M > 32 * groups && (g.M / kUnitRows + groups) * ((g.N + 63) / 64) >= 224 ? i8_rows<4>(g, st)
+                                                                                                  : i8_rows<2>(g, st);
 }
 
 }  // namespace fp8moe

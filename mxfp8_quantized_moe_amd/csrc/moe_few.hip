@@ -11,16 +11,21 @@
 //
 // Every used expert's weights have to be read once, 3 K F bytes, and with a few tokens nothing else is of that
 // size: the kernels stream weights.  A weight is the matrix instruction's row operand (16 rows of W a
-// tile), the expert's tokens its 16 columns, so one read of a tile serves up to 64 tokens.  A lane loads 16 bytes of a
-// row, 64 of a row lie in one instruction's four lane groups, and two v_mfma_f32_16x16x32_bf16
-// take them: both operands permute the contraction alike, so no byte moves between lanes.  Codes become
-// bf16 exactly (e4m3 and whole numbers up to 128 have at most eight significant bits); an e8m0 scale goes into
+// tile), the expert's tokens its columns, so one read of a tile serves up to 64 tokens; few_dot.hpp says how it is loaded.
+// Codes become bf16 exactly (e4m3 and whole numbers up to 128 have at most eight significant bits); an e8m0 scale goes into
 // that conversion, an fp32 scale divides the sum.  Activations come from L2 straight into registers.
 //
 // Tokens that choose one expert are found from the ids by every workgroup of the first kernel for itself (a
-// token that names an expert twice is one column with the sum of its weights); the workgroup of an expert's first tile
-// leaves the list for the second kernel, whose waves go through all experts: finding it there again cost 2 us a wave
-// and expert, a fifth of the time at 64 tokens of 32 experts.
+// token that names an expert twice is one column with the sum of its weights); workgroups behind the tiles' own leave the
+// lists for the second kernel, which waits for nothing else: with a search by each of its waves 64 tokens of 32 experts took a
+// fifth longer.
+//
+// Two kernels rather than one: the second needs all of a, and their launches overlap the reads by less than a barrier over
+// the GPU would cost.
+//
+// Rates, the used experts' weights over the time of both kernels: 16 tokens of 16 experts, MX, 5120 x 8192: 121 us, 6.9 TB/s;
+// 64 tokens of 32 experts 7168 x 2048, a quarter of their choices here: 215 us, 6.5 TB/s: bound by that read.  One token, six
+// of 64 experts 2048 x 1408: 17 us, 3 TB/s, where the launches and the beginnings of the reads count as much.
 #include "few_dot.hpp"
 #include "kernels.hpp"
 #include "swiglu_common.hpp"
@@ -251,20 +256,19 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
       uint32_t x[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int ts = list.ts[min(Dot::ROWS * b + (lane & 15) % Dot::ROWS, n - 1)];
+        const int ts = list.ts[min(Dot::ROWS * b + (lane & 15) / Q, n - 1)];
         x[b] = UP ? (uint32_t)(2 * (ts >> 16) * p.ld_x) : (uint32_t)(2 * (ts & 0xFFFF) * p.F);
       }
-      const int steps = (L + Dot::STEP - 1) / Dot::STEP;
       Dot d;
-      d.run(w, UP ? p.x : p.a2, x, L, steps * wave / W, steps * (wave + 1) / W);
+      d.run(w, UP ? p.x : p.a2, x, L, wave, W);
 #pragma unroll
-      for (int r = 0; r < Dot::R; ++r)
+      for (int h = 0; h < NT; ++h)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) red[wave][r * NB + b][lane] = d.acc[r][b];
+        for (int b = 0; b < NB; ++b) red[wave][h * NB + b][lane] = d.sums(h, b);
       __syncthreads();
       // a lane takes token 16 i + (l & 15), columns 4 (l >> 4) .. + 3 of the tiles, two tiles at a time
       for (int i = wave; i < (NB * Dot::ROWS + 15) / 16 * PAIRS; i += W) {
-        const int m = 16 * (i / PAIRS) + (lane & 15), cq = lane >> 4, b = m / Dot::ROWS;
+        const int m = 16 * (i / PAIRS) + (lane & 15), b = m / Dot::ROWS;
         const int col = 16 * (UP ? 1 : 2) * (tile * PAIRS + i % PAIRS);   // first column of the pair
         if (m >= n || col >= N) continue;
         few_v4f g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g, dg = div[0], du = div[1];
@@ -272,13 +276,11 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
           if (i % PAIRS) dg = div[2], du = div[3];
         }
 #pragma unroll
-        for (int v = 0; v < W; ++v)
-#pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const int from = Dot::lane_of(cq, m % Dot::ROWS, q), r = 2 * Q * (i % PAIRS) + cq / (4 / Q);
-            g += red[v][r * NB + b][from];
-            u += red[v][(Q + r) * NB + b][from];
-          }
+        for (int v = 0; v < W; ++v) {
+          const int from = 16 * (lane >> 4) + Q * (m % Dot::ROWS);
+          g += red[v][2 * (i % PAIRS) * NB + b][from];
+          u += red[v][(2 * (i % PAIRS) + 1) * NB + b][from];
+        }
         const int slot = list.ts[m] & 0xFFFF;
         if constexpr (UP) {
           float a[4];
@@ -337,13 +339,14 @@ __global__ __launch_bounds__(256) void few_zero_kernel(uint32_t* y, int64_t n) {
 
 template <int FMT, bool UP>
 static hipError_t few_launch(const FewParams& p, hipStream_t st) {
-  // Four tiles a workgroup share the activations' loads, which outgrow the weights' beyond some 16 tokens an expert, where
-  // the workgroups still fill the GPU (64 tokens, eight of 16 experts 5120 x 8192: first kernel 593 -> 448 us, second 303 ->
-  // 238; 64 tokens of one expert 4096 x 8192: first, 256 workgroups, 43 -> 35 us, second, 64 workgroups, 41 -> 63;
-  // four tokens an expert of 32, 7168 x 2048, the others' ids none: both 231 -> 249).
+  // Four tiles a workgroup share the activations' loads, which outgrow the weights' where experts have some 30 tokens (up to
+  // 32 two tiles load whole cache lines of them), if the workgroups still fill the GPU (64 tokens, eight of 16 experts
+  // 5120 x 8192: both kernels 835 -> 705 us by the first, -> 792 by the second; eight of 8 7168 x 2048 235 -> 187, -> 215; eight
+  // of 20 2048 x 2048, 26 an expert, 92 -> 93, -> 104; 64 tokens of one expert 4096 x 8192, the second's 64 workgroups: 85 ->
+  // 111).
   auto count = [&](int cols) { return (int64_t)p.ranks * (((UP ? p.F : p.K) + cols - 1) / cols); };
   constexpr int COLS = UP ? 16 : 32;
-  const bool wide = (int64_t)p.T * p.topk > 16 * (int64_t)p.E && count(2 * COLS) >= 224;
+  const bool wide = (int64_t)p.T * p.topk > 28 * (int64_t)p.E && count(2 * COLS) >= 224;
   const int64_t blocks = count(wide ? 2 * COLS : COLS);
   const dim3 grid((unsigned)(blocks + (UP ? p.ranks + 1 : 0)));
   // Short rows leave four waves a step or two each: two waves where the workgroups fill the GPU by themselves
