@@ -23,7 +23,7 @@
 // Two kernels rather than one: the second needs all of a, and their launches overlap the reads by less than a barrier over
 // the GPU would cost.
 //
-// Rates, the used experts' weights over the time of both kernels: 16 tokens of 16 experts, MX, 5120 x 8192: 121 us, 6.9 TB/s;
+// Rates, the used experts' weights over the time of both kernels: 8 tokens of 16 experts, MX, 5120 x 8192: 121 us, 6.9 TB/s;
 // 64 tokens of 32 experts 7168 x 2048, a quarter of their choices here: 215 us, 6.5 TB/s: bound by that read.  One token, six
 // of 64 experts 2048 x 1408: 17 us, 3 TB/s, where the launches and the beginnings of the reads count as much.
 #include "few_dot.hpp"
