@@ -82,7 +82,8 @@ extern "C" {
 #define FP8MOE_E4M3FNUZ 1
 /* Symmetric 8-bit integers: whole numbers in [-127, 127], two's complement, under the
  * rowwise recipe with s = fp32(127 * fp32(1 / max(amax, 1e-12f))) (the two roundings that torch
- * makes of `127 / amax`) and q = the whole number nearest to clamp(fp32(x * s)), ties to even.  Taken by the rowwise quantizers of forward operands (quantize_rowwise,
+ * makes of `127 / amax`) and q = the whole number nearest to clamp(fp32(x * s)), ties to even.
+ * Taken by the rowwise quantizers of forward operands (quantize_rowwise,
  * swiglu_quantize_rowwise, moe_permute_rowwise, moe_permute_quantized,
  * rmsnorm_quantize_rowwise); their product is grouped_mm_scaled with FP8MOE_OPD_INT8. */
 #define FP8MOE_INT8 4
@@ -875,7 +876,7 @@ int moe_gate_backward(const void *logits, int logit_dtype, int64_t tokens, int32
  *             one each
  *   Requires: tokens <= 64, tokens*topk <= 1024, n_experts <= 1024 (else
  *   FP8MOE_ERR_UNSUPPORTED: more tokens take moe_route and the grouped GEMMs);
- *   K, F <= 2^20, ld_x <= 2^24;
+ *   K, F <= 2^17, ld_x <= 2^24;
  *   K % 16 == 0 and F % 16 == 0 (e8m0 scales: 32); ld_x >= K, ld_x % 8 == 0; x, w1, w2,
  *   y 16-byte aligned, the int32 and f32 arrays 4-byte aligned.  Two kernels, no
  *   allocation.
@@ -900,7 +901,7 @@ int64_t moe_few_tokens_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, 
  *   a2      bf16 [rows][F]      bf16(a) (written), or NULL
  *   hq      u8   [rows][2F], hs_e8m0 u8 [rows][2F / 32]: quantize_mx(h1) with axis 1,
  *           `rule` and row-major scales (written)
- *   Requires: rows, F >= 0; F % 32 == 0; ld_h1 >= 2F, ld_h1 % 8 == 0; h1, a2, q, hq 16-byte
+ *   Requires: 0 <= rows < 2^24, F >= 0; F % 32 == 0; ld_h1 >= 2F, ld_h1 % 8 == 0; h1, a2, q, hq 16-byte
  *   aligned, scale 4-byte aligned; codec E4M3FN or E4M3FNUZ.  One kernel, no allocation.
  */
 int swiglu_quantize_rowwise_save(const void *h1_bf16, int64_t rows, int64_t F, int64_t ld_h1, int codec, int rule,
@@ -919,7 +920,7 @@ int swiglu_quantize_rowwise_save(const void *h1_bf16, int64_t rows, int64_t F, i
  *   q, scale  u8 [rows][2F], f32 [rows]: the rowwise recipe over those fp32 values (written), or
  *           NULL together
  *   a2      bf16 [rows][F]   bf16(g s u) (written), or NULL
- *   At least one result is asked for.  Requires: rows, F >= 0; F % 32 == 0; bf16 and code
+ *   At least one result is asked for.  Requires: 0 <= rows < 2^24, F >= 0; F % 32 == 0; bf16 and code
  *   pointers 16-byte aligned, scale 4-byte aligned; codec E4M3FN or E4M3FNUZ.  One kernel, no
  *   allocation.
  */

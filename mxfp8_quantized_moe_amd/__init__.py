@@ -621,8 +621,8 @@ def rmsnorm_quantize_rowwise(x, gamma=None, eps=1e-6, residual=None, codec=E4M3F
                              sum_out=None, h=None, q=None, scale=None, rstd=None, stream=None):
     """x bf16 [R, C] (row stride may exceed C), gamma bf16 or f32 [C] or None, residual bf16 [R, C] or None ->
     (h bf16 [R, C] or None, q u8 [R, C] or None, scale f32 [R] or None, rstd f32 [R], sum bf16 [R, C]): the residual's
-    addition, the RMS norm and the rowwise FP8 quantization of the normed rows (from fp32; int8 codes with codec=INT8) in one pass.  sum is
-    x + residual, the new residual stream (x itself without a residual); sum_out may be x or residual (contiguous).
+    addition, the RMS norm and the rowwise quantization of the normed rows (from fp32; int8 codes with codec=INT8) in one
+    pass.  sum is x + residual, the new residual stream (x itself without a residual); sum_out may be x or residual (contiguous).
     keep_bf16=False skips h, codes=False skips q and scale."""
     fn = "rmsnorm_quantize_rowwise"
     R, C, ld, ld_r, gt = _norm_inputs(fn, x, gamma, residual)

@@ -116,6 +116,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
 bool i8_rows_wanted(const GemmArgs& g) {
   if (g.N < 16) return false;
   const int64_t groups = std::min<int64_t>(g.n_groups, g.M);
+  if ((g.M / kUnitRows + groups) * ((g.N + 31) / 32) >= 1 << 24) return false;   // a launch takes fewer than 2^32 threads
   return g.M <= 16 * (int64_t)g.n_groups ||
          (groups * ((g.N + 255) / 256) < 256 && (g.M + 32 * groups) * g.N <= (g.K <= 512 ? 4000000 : 2300000));
 }
@@ -125,7 +126,6 @@ static hipError_t i8_rows(const GemmArgs& g, hipStream_t st) {
   const I8Params p{static_cast<const uint8_t*>(g.a), static_cast<const uint8_t*>(g.b), static_cast<const float*>(g.sa),
                    static_cast<const float*>(g.sb), g.offs, g.out, g.n_groups, (int)g.M, (int)g.N, (int)g.K};
   const int64_t blocks = (g.M / kUnitRows + std::min<int64_t>(g.n_groups, g.M)) * ((g.N + 16 * NT - 1) / (16 * NT));
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const bool two = g.K <= 2048 && blocks >= 512;
   const bool stream = (int64_t)g.n_groups * g.N * g.K > (256ll << 20);
   auto pick = [&](auto out_tag) {

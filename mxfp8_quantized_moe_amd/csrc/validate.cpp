@@ -585,7 +585,8 @@ int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x,
   if (!fp8 && !i8 && w_fmt != FP8MOE_OPD_E4M3FNUZ && w_fmt != FP8MOE_OPD_BF16) return FP8MOE_ERR_ENUM;
   if (scale_kind < 0 || scale_kind > 3) return FP8MOE_ERR_ENUM;
   const bool mx = scale_kind == FP8MOE_SCALE_E8M0, k4 = scale_kind == FP8MOE_SCALE_E8M0_K4;
-  if (tokens < 0 || K < 0 || F < 0 || topk < 1 || E < 1 || ld_x < K || K > kFewMaxWidth || F > kFewMaxWidth || ld_x > 16 * kFewMaxWidth)
+  if (tokens < 0 || K < 0 || F < 0 || topk < 1 || E < 1 || ld_x < K || K > kFewMaxWidth || F > kFewMaxWidth ||
+      ld_x > kFewMaxStride)
     return FP8MOE_ERR_SHAPE;
   if (!(fp8 || (i8 && !mx && !k4)) || scale_kind == FP8MOE_SCALE_NONE) return FP8MOE_ERR_UNSUPPORTED;
   if (tokens > kFewMaxTokens || topk > kFewMaxSlots || tokens * topk > kFewMaxSlots || E > kFewMaxExperts)
@@ -610,7 +611,7 @@ int check_swiglu_save(const void* h1, int64_t rows, int64_t F, int64_t ld_h1, in
                       const void* q, const void* scale, const void* hq, const void* hs) {
   if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
   if (rule != FP8MOE_MX_FLOOR_OCP && rule != FP8MOE_MX_CEIL) return FP8MOE_ERR_ENUM;
-  if (rows < 0 || F < 0 || rows > kI32Max || F > kI32Max / 4 || ld_h1 < 2 * F) return FP8MOE_ERR_SHAPE;
+  if (rows < 0 || F < 0 || rows > kSaveMaxRows || F > kI32Max / 4 || ld_h1 < 2 * F) return FP8MOE_ERR_SHAPE;
   const int64_t n = mul(rows, 2 * F);
   if (n < 0 || mul(rows, ld_h1) < 0) return FP8MOE_ERR_SHAPE;
   if (!need(h1, n) || !need(q, n) || !need(scale, n) || !need(hq, n) || !need(hs, n)) return FP8MOE_ERR_NULL;
@@ -622,7 +623,7 @@ int check_swiglu_save(const void* h1, int64_t rows, int64_t F, int64_t ld_h1, in
 int check_swiglu_saved_backward(const void* da2, const void* hq, const void* hs, int64_t rows, int64_t F, int codec,
                                 const void* dh1, const void* q, const void* scale, const void* a2) {
   if (codec != FP8MOE_E4M3FN && codec != FP8MOE_E4M3FNUZ) return FP8MOE_ERR_ENUM;
-  if (rows < 0 || F < 0 || rows > kI32Max || F > kI32Max / 4 || mul(rows, 2 * F) < 0) return FP8MOE_ERR_SHAPE;
+  if (rows < 0 || F < 0 || rows > kSaveMaxRows || F > kI32Max / 4 || mul(rows, 2 * F) < 0) return FP8MOE_ERR_SHAPE;
   const int64_t n = mul(rows, 2 * F);
   if (n && (q == nullptr) != (scale == nullptr)) return FP8MOE_ERR_NULL;   // codes and scales come together
   if (!need(da2, n) || !need(hq, n) || !need(hs, n) || (n && !dh1 && !q && !a2)) return FP8MOE_ERR_NULL;

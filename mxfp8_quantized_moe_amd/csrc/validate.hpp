@@ -138,7 +138,9 @@ int check_moe_gate_backward(int64_t tokens, int32_t topk, float route_scale, con
 constexpr int kFewMaxTokens = 64;
 constexpr int kFewMaxSlots = 1024;
 constexpr int kFewMaxExperts = 1024;
-constexpr int64_t kFewMaxWidth = 1 << 20;   // offsets within a tile and the activations are 32-bit
+constexpr int64_t kFewMaxWidth = 1 << 17;   // 1024 experts in tiles of 16 stay below a launch's 2^32 threads
+constexpr int64_t kFewMaxStride = 1 << 24;  // offsets of 64 rows are 32-bit
+constexpr int64_t kSaveMaxRows = (1 << 24) - 1;   // a row a workgroup of 256 threads, 2^32 threads a launch
 int64_t few_workspace_bytes(int64_t tokens, int32_t topk, int64_t K, int64_t F);
 int check_moe_few_tokens(const void* x, int64_t tokens, int64_t K, int64_t ld_x, const void* ids, const void* weights,
                          int32_t topk, const void* w1, const void* s1, const void* w2, const void* s2, int w_fmt,

@@ -28,7 +28,7 @@ def test_refusals(lib):
     assert call(lib, fmt=3) == L.ERR_ENUM
     assert call(lib, sk=4) == L.ERR_ENUM
     for kw in (dict(T=-1), dict(K=-16), dict(F=-16), dict(topk=0), dict(E=0), dict(ld=56), dict(K=1 << 40, ld=1 << 40),
-               dict(F=1 << 40)):
+               dict(F=1 << 40), dict(F=(1 << 17) + 32), dict(K=(1 << 17) + 32, ld=1 << 18), dict(ld=(1 << 24) + 8)):
         assert call(lib, **kw) == L.ERR_SHAPE, kw
     for kw in (dict(fmt=1), dict(fmt=2), dict(fmt=4, sk=1), dict(fmt=4, sk=3), dict(sk=2), dict(T=65), dict(T=64, topk=17),
                dict(T=1, topk=1025), dict(E=1025)):
@@ -45,7 +45,7 @@ def test_nothing_to_do(lib):
 
 def test_workspace_bytes():
     assert fm.moe_few_tokens_workspace_bytes(64, 16, 2048, 4096) >= 64 * 16 * (4096 * 2 + 2048 * 4)
-    for bad in ((-1, 1, 16, 16), (65, 1, 16, 16), (64, 17, 16, 16), (4, 0, 16, 16), (4, 1, 16, -16), (4, 1, -16, 16), (4, 1, 1 << 21, 16)):
+    for bad in ((-1, 1, 16, 16), (65, 1, 16, 16), (64, 17, 16, 16), (4, 0, 16, 16), (4, 1, 16, -16), (4, 1, -16, 16), (4, 1, 1 << 21, 16), (4, 1, 16, (1 << 17) + 16)):
         assert fm.moe_few_tokens_workspace_bytes(*bad) == -1
 
 
