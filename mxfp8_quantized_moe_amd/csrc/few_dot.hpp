@@ -108,15 +108,25 @@ struct FewDot {
   static constexpr int XB = FMT == kFewInt8Both ? 1 : 2;   // bytes of an activation
   Acc acc[R][NB];
 
+  // Of a block of rows or tokens, the one whose bytes the lane loads.
+  static __device__ __forceinline__ int slot_of(int lane) { return Q == 1 ? lane >> 2 : (lane & 15) / Q; }
+
   // x: byte offset of the lane's row of activations from `xb`
   __device__ __forceinline__ void run(const FewTile (&tile)[NT], const void* xb, const uint32_t (&x)[NB], int L, int wave,
                                       int W) {
     const int all = (L + STEP - 1) / STEP, ds = Q == 1 ? W : 1;
     const int s0 = Q == 1 ? wave : all * wave / W, s1 = Q == 1 ? all : all * (wave + 1) / W;
     const int lane = threadIdx.x & 63;
-    const int kl = 16 * Q * (lane >> 4) + 16 * (lane % Q);
-    const uint32_t slot = (lane & 15) / Q, row = slot / SUB * 4 + slot % SUB;
-    const uint32_t row_w = row * L, row_s = FMT == kFewMxK4 ? 4 * row : row * (L / 32);
+    const uint32_t slot = slot_of(lane), row = Q == 1 ? slot : slot / SUB * 4 + slot % SUB, row_w = row * L;
+    const int kl = Q == 1 ? 16 * (lane & 3) : 16 * Q * (lane >> 4) + 16 * (lane % Q);
+    // the row and the chunk that the matrix instruction takes from the lane
+    const uint32_t row_m = Q == 1 ? lane & 15 : row, row_s = FMT == kFewMxK4 ? 4 * row_m : row_m * (L / 32);
+    const int kl_m = Q == 1 ? 16 * (lane >> 4) : kl, from = 16 * (lane & 15) + 4 * (lane >> 4);
+    auto turn = [&](u32x4 v) {
+      if constexpr (Q > 1) return v;
+      return u32x4{(uint32_t)__builtin_amdgcn_ds_bpermute(from, v.x), (uint32_t)__builtin_amdgcn_ds_bpermute(from, v.y),
+                   (uint32_t)__builtin_amdgcn_ds_bpermute(from, v.z), (uint32_t)__builtin_amdgcn_ds_bpermute(from, v.w)};
+    };
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -128,14 +138,14 @@ struct FewDot {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int kk = STEP * (s + u * ds) + kl;
-        const uint32_t k = WHOLE ? kk : min(kk, L - 16);
+        const uint32_t k = WHOLE ? kk : min(kk, L - 16), k_m = WHOLE ? kk - kl + kl_m : min(kk - kl + kl_m, L - 16);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const FewTile& t = tile[r / PARTS];
           wv[u][r] = few_load16<(STREAM && Q > 1)>(t.w + (int64_t)(r % PARTS) * SUB * L, row_w + k);
-          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * SUB * (L / 32))[row_s + (k >> 5)];
+          if constexpr (FMT == kFewMx) e[u][r] = (t.s + (int64_t)(r % PARTS) * SUB * (L / 32))[row_s + (k_m >> 5)];
           if constexpr (FMT == kFewMxK4)
-            e[u][r] = t.s[(int64_t)(k >> 7) * t.group + (row_s + (r % PARTS) * SUB * 4 + ((k >> 5) & 3))];
+            e[u][r] = t.s[(int64_t)(k_m >> 7) * t.group + (row_s + (r % PARTS) * SUB * 4 + ((k_m >> 5) & 3))];
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -155,7 +165,12 @@ struct FewDot {
               if (!in) xv[u][b][h] = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int h = 0; h < XB; ++h) xv[u][b][h] = turn(xv[u][b][h]);
+#pragma unroll
         for (int r = 0; r < R; ++r) {
+          wv[u][r] = turn(wv[u][r]);
           if constexpr (FMT == kFewInt8Both) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
     using Dot = FewDot<kFewInt8Both, NT, NB, Q, STREAM>;
     uint32_t x[NB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) x[b] = (uint32_t)(min(Dot::ROWS * b + (lane & 15) / Q, n - 1) * p.K);
+    for (int b = 0; b < NB; ++b) x[b] = (uint32_t)(min(Dot::ROWS * b + Dot::slot_of(lane), n - 1) * p.K);
     Dot d;
     d.run(w, p.a + (int64_t)m0 * p.K, x, p.K, wave, W);
 #pragma unroll

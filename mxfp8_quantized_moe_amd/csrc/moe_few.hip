@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * W) void few_kernel(FewParams p) {
       uint32_t x[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int ts = list.ts[min(Dot::ROWS * b + (lane & 15) / Q, n - 1)];
+        const int ts = list.ts[min(Dot::ROWS * b + Dot::slot_of(lane), n - 1)];
         x[b] = UP ? (uint32_t)(2 * (ts >> 16) * p.ld_x) : (uint32_t)(2 * (ts & 0xFFFF) * p.F);
       }
       Dot d;
