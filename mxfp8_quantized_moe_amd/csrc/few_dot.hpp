@@ -1,8 +1,7 @@
 // Products of 8-bit weight rows with the activations of a few tokens (at most 64), bound by the read of the weights.
 //
 // A weight is the matrix instruction's row operand (16 rows a tile), a token a column, so one read of a tile serves all
-// tokens.  A lane loads 16 bytes of a row, and both operands permute the contraction alike, so no byte moves between
-// lanes.  With bf16 activations the codes become bf16 on the way (exactly: e4m3 and whole numbers up to 128 have at most
+// tokens.  A lane loads 16 bytes of a row, and both operands permute the contraction alike.  With bf16 activations the codes become bf16 on the way (exactly: e4m3 and whole numbers up to 128 have at most
 // eight significant bits) and two v_mfma_f32_16x16x32_bf16 take a lane's bytes; with whole-number activations
 // one v_mfma_i32_16x16x64_i8 does.  Activations come from L2 straight into registers.
 #pragma once
@@ -88,9 +87,12 @@ __device__ __forceinline__ FewTile few_tile(const uint8_t* w, const void* s, int
 // Q times, in neighbouring lanes with neighbouring chunks of 16 bytes, and each token's chunks in Q neighbouring
 // columns.  Of the result only products of a row's q-th chunks with a token's q-th are of use; the sum over q, of
 // neighbouring lanes, is the answer.  A load then takes 64 Q bytes of a row, whole cache lines, and the activations' loads
-// are shared by the parts.  The address unit takes four lanes a cycle where they lie in one line, and one or two where they
-// do not, which is what bounds the loads of a CU: with a row's chunks 16 lanes apart 16 rows of 5120 x 5120 took 10.5 us,
-// this way 8.2.
+// are shared by the parts.
+//
+// The address unit takes four lanes a cycle where they lie in one line, and one or two where they do not, which is what bounds
+// the loads of a CU: with a row's chunks 16 lanes apart 16 rows of 5120 x 5120 took 10.5 us, this way 8.2.  For Q = 1, where
+// the instruction wants them 16 apart, neighbouring lanes load a row's four chunks and hand them over (400 rows of 4096 x
+// 4096 34 -> 22 us; for Q = 2, pairs already, the handing over costs what it gains: 32 rows 8.6 -> 9.4).
 //
 // Part p has the rows p 4 / Q .. of each four, so that sums() leaves a lane four rows in order.
 //
@@ -103,9 +105,11 @@ __device__ __forceinline__ FewTile few_tile(const uint8_t* w, const void* s, int
 template <int FMT, int NT, int NB, int Q, bool STREAM>
 struct FewDot {
   static constexpr int ROWS = 16 / Q, PARTS = Q, R = NT * PARTS, STEP = 64 * Q, SUB = 4 / Q;
-  static constexpr int U = R * NB >= 8 ? 1 : R * NB >= 4 ? 2 : 4;   // steps whose loads are in flight together
   using Acc = std::conditional_t<FMT == kFewInt8Both, few_v4i, few_v4f>;
   static constexpr int XB = FMT == kFewInt8Both ? 1 : 2;   // bytes of an activation
+  // Steps whose loads are in flight together, by their registers (whole numbers 64 x 4096 x 4096: two 11.7 -> 10.4 us; bf16
+  // 64 tokens, six of 16 experts 2048 x 1408: 62 -> 67).
+  static constexpr int U = R * NB >= 16 ? 1 : R * NB >= 8 ? (XB == 1 && Q == 1 ? 2 : 1) : R * NB >= 4 ? 2 : 4;
   Acc acc[R][NB];
 
   // Of a block of rows or tokens, the one whose bytes the lane loads.

@@ -108,17 +108,17 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
 }  // namespace
 
 // When this kernel is taken, by the persistent GEMM's tiles of 256 columns (one for each group with rows). They fill the
-// GPU: up to 16 rows a group (64 groups, 2816 x 2048: 512 rows of 1408 37 us here, 44 there; 1024 rows 71 and 72; 1500 rows 75
-// and 73; 1000 rows of 32 groups 53 and 44). They do not: their time is one pass along K whatever the rows are, while the
-// activations' loads here grow with them (14336 x 4096, one group: 16 rows 12 and 40 us, 128 rows 34 and 43, 160 rows 54 and
-// 47; 4096 x 4096: 400 rows 33 and 45, 600 rows 48 and 44; 2000 rows of 1024 x 2048 20 and 28, 2048 rows in 8 groups 28 and
-// 19), and a short pass leaves its beginning and end (16080 rows of 177 x 400 13 and 18; 447 of 10756 x 288 19 and 18).
+// GPU: up to 16 rows a group (64 groups, 2816 x 2048: 512 rows of 1408 37 us here, 44 there; 1024 rows 70 and 72; 1500 rows 76
+// and 73; 1000 rows of 32 groups 53 and 45). They do not: their time is one pass along K whatever the rows are, while the
+// activations' loads here grow with them (one group of 14336 x 4096: 16 rows 12 and 40 us, 256 rows 40 and 46; 4096 x 4096: 400
+// rows 22 and 45, 1024 rows 44 and 45; 4000 of 1024 x 1024 14 and 20; 2048 rows in 8 groups of 1024 x 2048 18 and 19; 447 of
+// 10756 x 1024 27 and 22).
 bool i8_rows_wanted(const GemmArgs& g) {
   if (g.N < 16) return false;
   const int64_t groups = std::min<int64_t>(g.n_groups, g.M);
   if ((g.M / kUnitRows + groups) * ((g.N + 31) / 32) >= 1 << 24) return false;   // a launch takes fewer than 2^32 threads
   return g.M <= 16 * (int64_t)g.n_groups ||
-         (groups * ((g.N + 255) / 256) < 256 && (g.M + 32 * groups) * g.N <= (g.K <= 512 ? 4000000 : 2300000));
+         (groups * ((g.N + 255) / 256) < 256 && (g.M + 64 * groups) * g.N <= 4600000);
 }
 
 template <int NT>
@@ -140,7 +140,8 @@ static hipError_t i8_rows(const GemmArgs& g, hipStream_t st) {
 
 hipError_t launch_i8_rows(const GemmArgs& g, hipStream_t st) {
   // Wider tiles share the activations' loads: 64 columns for more than 32 rows a group where their workgroups fill the GPU
-  // (64 rows of 14336 x 4096 25 -> 19 us, 1000 of 1024 x 4096 25 -> 19; 32 of 14336 13 -> 15, 500 of 1024 14 -> 18).
+  // (128 rows of 14336 x 4096 34 -> 23 us, 1000 of 1024 x 4096 17 -> 15; 128 of 4096 12.6 -> 14.5, 700 rows in 32 groups of
+  // 7168 x 2048 90 -> 103).
   const int64_t groups = std::min<int64_t>(g.n_groups, g.M);
   return g.N >= 64 && g.M > 32 * groups && (g.M / kUnitRows + groups) * ((g.N + 63) / 64) >= 224 ? i8_rows<4>(g, st)
                                                                                                   : i8_rows<2>(g, st);

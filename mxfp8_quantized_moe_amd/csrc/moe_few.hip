@@ -339,14 +339,14 @@ __global__ __launch_bounds__(256) void few_zero_kernel(uint32_t* y, int64_t n) {
 
 template <int FMT, bool UP>
 static hipError_t few_launch(const FewParams& p, hipStream_t st) {
-  // Four tiles a workgroup share the activations' loads, which outgrow the weights' where experts have some 30 tokens (up to
+  // Four tiles a workgroup share the activations' loads, which outgrow the weights' where experts have some 25 tokens (up to
   // 32 two tiles load whole cache lines of them), if the workgroups still fill the GPU (64 tokens, eight of 16 experts
-  // 5120 x 8192: both kernels 835 -> 705 us by the first, -> 792 by the second; eight of 8 7168 x 2048 235 -> 187, -> 215; eight
-  // of 20 2048 x 2048, 26 an expert, 92 -> 93, -> 104; 64 tokens of one expert 4096 x 8192, the second's 64 workgroups: 85 ->
-  // 111).
+  // 5120 x 8192: both kernels 669 -> 585 us by the first, -> 643 by the second; eight of 8 7168 x 2048 191 -> 153, -> 174; six
+  // of 16 2048 x 1408, 24 an expert, 64.6 -> 65.1, -> 61.7; 64 tokens of one expert 4096 x 8192, the second's 64 workgroups:
+  // 69 -> 90; four tokens an expert of 32, 7168 x 2048, the others' ids none: both 231 -> 249).
   auto count = [&](int cols) { return (int64_t)p.ranks * (((UP ? p.F : p.K) + cols - 1) / cols); };
   constexpr int COLS = UP ? 16 : 32;
-  const bool wide = (int64_t)p.T * p.topk > 28 * (int64_t)p.E && count(2 * COLS) >= 224;
+  const bool wide = (int64_t)p.T * p.topk >= 24 * (int64_t)p.E && count(2 * COLS) >= 224;
   const int64_t blocks = count(wide ? 2 * COLS : COLS);
   const dim3 grid((unsigned)(blocks + (UP ? p.ranks + 1 : 0)));
   // Short rows leave four waves a step or two each: two waves where the workgroups fill the GPU by themselves
