@@ -266,7 +266,7 @@ int swiglu_quantize_mx_dual(const void* h1_bf16, int64_t rows, int64_t F, int64_
                                       a2_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
   if (st) return st;
   return launch_status(launch_swiglu_mx_dual(
-      static_cast<const uint16_t*>(h1_bf16), nullptr, rows, F, ld_h1, offs, n_groups, rule, scale_layout,
+      static_cast<const uint16_t*>(h1_bf16), nullptr, false, rows, F, ld_h1, offs, n_groups, rule, scale_layout,
       static_cast<uint16_t*>(a2_bf16), static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale_e8m0),
       static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad, offs_pad_out, as_stream(stream)));
 }
@@ -279,8 +279,8 @@ int swiglu_backward_quantize_mx_dual(const void* da2_bf16, const void* h1_bf16, 
                                       dh1_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
   if (st) return st;
   return launch_status(launch_swiglu_mx_dual(
-      static_cast<const uint16_t*>(h1_bf16), static_cast<const uint16_t*>(da2_bf16), rows, F, ld_h1, offs, n_groups,
-      rule, scale_layout, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q),
+      static_cast<const uint16_t*>(h1_bf16), static_cast<const uint16_t*>(da2_bf16), true, rows, F, ld_h1, offs,
+      n_groups, rule, scale_layout, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q),
       static_cast<uint8_t*>(scale_e8m0), static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad,
       offs_pad_out, as_stream(stream)));
 }
@@ -458,7 +458,7 @@ int swiglu_quantize_mx_dual_saved(const void* hq, const void* hs_e8m0, int64_t r
                                             a2_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
   if (st) return st;
   return launch_status(launch_swiglu_mx_dual_saved(
-      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), nullptr, rows, F, offs, n_groups, rule,
+      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), nullptr, false, rows, F, offs, n_groups, rule,
       scale_layout, static_cast<uint16_t*>(a2_bf16), static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale_e8m0),
       static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad, offs_pad_out, as_stream(stream)));
 }
@@ -471,8 +471,8 @@ int swiglu_backward_quantize_mx_dual_saved(const void* da2_bf16, const void* hq,
                                             dh1_bf16, q, scale_e8m0, q_t, scale_t_e8m0, rows_pad, offs_pad_out);
   if (st) return st;
   return launch_status(launch_swiglu_mx_dual_saved(
-      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), static_cast<const uint16_t*>(da2_bf16), rows, F,
-      offs, n_groups, rule, scale_layout, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q),
+      static_cast<const uint8_t*>(hq), static_cast<const uint8_t*>(hs_e8m0), static_cast<const uint16_t*>(da2_bf16), true, rows,
+      F, offs, n_groups, rule, scale_layout, static_cast<uint16_t*>(dh1_bf16), static_cast<uint8_t*>(q),
       static_cast<uint8_t*>(scale_e8m0), static_cast<uint8_t*>(q_t), static_cast<uint8_t*>(scale_t_e8m0), rows_pad,
       offs_pad_out, as_stream(stream)));
 }

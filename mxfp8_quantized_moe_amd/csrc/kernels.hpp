@@ -37,8 +37,8 @@ hipError_t launch_moe_permute_mx_dual(const uint16_t* x, int64_t tokens, int64_t
                                      const float* weights, int64_t rows, const int32_t* offs, int32_t n_groups,
                                      int rule, int scale_layout, uint16_t* xg, uint8_t* q, uint8_t* sc, uint8_t* q_t,
                                      uint8_t* sc_t, int64_t rows_pad, int32_t* offs_pad_out, hipStream_t st);
-hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, int64_t rows, int64_t F, int64_t ld_h1,
-                                 const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
+hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, bool bwd, int64_t rows, int64_t F,
+                                 int64_t ld_h1, const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
                                  uint8_t* q, uint8_t* sc, uint8_t* q_t, uint8_t* sc_t, int64_t rows_pad,
                                  int32_t* offs_pad_out, hipStream_t st);
 
@@ -189,8 +189,8 @@ hipError_t launch_swiglu_save(const uint16_t* h1, int64_t rows, int64_t F, int64
                               uint16_t* a2, uint8_t* q, float* scale, uint8_t* hq, uint8_t* hs, hipStream_t st);
 hipError_t launch_swiglu_saved_backward(const uint16_t* da2, const uint8_t* hq, const uint8_t* hs, int64_t rows, int64_t F,
                                         int codec, uint16_t* dh1, uint8_t* q, float* scale, uint16_t* a2, hipStream_t st);
-hipError_t launch_swiglu_mx_dual_saved(const uint8_t* hq, const uint8_t* hs, const uint16_t* da2, int64_t rows, int64_t F,
-                                       const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
+hipError_t launch_swiglu_mx_dual_saved(const uint8_t* hq, const uint8_t* hs, const uint16_t* da2, bool bwd, int64_t rows,
+                                       int64_t F, const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
                                        uint8_t* q, uint8_t* sc, uint8_t* q_t, uint8_t* sc_t, int64_t rows_pad,
                                        int32_t* offs_pad_out, hipStream_t st);
 

@@ -750,11 +750,11 @@ hipError_t launch_quantize_mx_dual(const uint16_t* x, int64_t batch, int64_t row
                                        offs_pad_out, grid, n_strips, st);
 }
 
-hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, int64_t rows, int64_t F, int64_t ld_h1,
-                                 const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
+hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, bool bwd, int64_t rows, int64_t F,
+                                 int64_t ld_h1, const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
                                  uint8_t* q, uint8_t* sc, uint8_t* q_t, uint8_t* sc_t, int64_t rows_pad,
                                  int32_t* offs_pad_out, hipStream_t st) {
-  const bool k4 = scale_layout == 1, bwd = da2 != nullptr;
+  const bool k4 = scale_layout == 1;   // without rows a backward's da2 may be null
   const int64_t cols = bwd ? 2 * F : F;
   if (cols == 0 && offs_pad_out == nullptr) return hipSuccess;
   const int64_t cols_i = bwd ? F : cols;   // the backward's items stride over F (two output tiles each)
@@ -774,11 +774,11 @@ hipError_t launch_swiglu_mx_dual(const uint16_t* h1, const uint16_t* da2, int64_
                                        offs_pad_out, grid, n_strips, st);
 }
 
-hipError_t launch_swiglu_mx_dual_saved(const uint8_t* hq, const uint8_t* hs, const uint16_t* da2, int64_t rows, int64_t F,
-                                       const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
+hipError_t launch_swiglu_mx_dual_saved(const uint8_t* hq, const uint8_t* hs, const uint16_t* da2, bool bwd, int64_t rows,
+                                       int64_t F, const int32_t* offs, int32_t n_groups, int rule, int scale_layout, uint16_t* out,
                                        uint8_t* q, uint8_t* sc, uint8_t* q_t, uint8_t* sc_t, int64_t rows_pad,
                                        int32_t* offs_pad_out, hipStream_t st) {
-  const bool k4 = scale_layout == 1, bwd = da2 != nullptr;
+  const bool k4 = scale_layout == 1;   // without rows a backward's da2 may be null
   const int64_t cols = bwd ? 2 * F : F;
   if (cols == 0 && offs_pad_out == nullptr) return hipSuccess;
   const int n_strips = (int)std::max<int64_t>((F + kDualCols - 1) / kDualCols, 1);   // the backward's items stride over F

@@ -190,6 +190,27 @@ def test_no_rows():
     assert out[0].shape == (0, 128) and out[3].shape == (0, 64)
 
 
+@pytest.mark.parametrize("layout", [fm.MX_LAYOUT_ROWS, fm.MX_LAYOUT_K4])
+@pytest.mark.parametrize("saved", [False, True])
+def test_backward_without_rows_writes_the_padding(saved, layout):
+    """No rows: the columns' form of the whole gradient, 2F of them, is padding."""
+    note(f"SwiGLU backward, MX, no rows, saved {saved} layout {layout}")
+    F, pad = 128, 256
+    da2, offs = torch.empty(0, F, dtype=torch.bfloat16, device=DEV), i32_dev([0, 0])
+    q_t = torch.full((2 * F, pad), 0xAB, dtype=torch.uint8, device=DEV)
+    sc_t = torch.full((2 * F * pad // 32,), 0xAB, dtype=torch.uint8, device=DEV).view(
+        fm.mx_k4_shape(2 * F, pad // 32) if layout == fm.MX_LAYOUT_K4 else (2 * F, pad // 32))
+    if saved:
+        hq, hs = u8_dev(np.empty((0, 2 * F), np.uint8)), u8_dev(np.empty((0, 2 * F // 32), np.uint8))
+        out = fm.swiglu_backward_quantize_mx_dual_saved(da2, hq, hs, offs, rows_pad=pad, q_t=q_t, scale_t=sc_t, layout=layout)
+    else:
+        h1 = torch.empty(0, 2 * F, dtype=torch.bfloat16, device=DEV)
+        out = fm.swiglu_backward_quantize_mx_dual(da2, h1, offs, rows_pad=pad, q_t=q_t, scale_t=sc_t, layout=layout)
+    assert out[1].shape == (0, 2 * F)
+    assert (q_t == 0).all()
+    assert torch.unique(sc_t).numel() == 1 and (sc_t != 0xAB).all()
+
+
 class Block:
     """An expert block's step in the rowwise recipe whose forward keeps 8 bits of h1 and nothing of a2."""
 
