@@ -95,6 +95,21 @@ def test_steps_that_end_inside(K, F, fmt):
     Layer(rng, 3, K, F, fmt).check(round_bf16(rng.standard_normal((7, K))), ids, w)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,k,E,K,F", [
+    (60, 1, 1, 96, 224), (28, 1, 1, 224, 96), (60, 2, 2, 32, 160),   # more tokens than an instruction's columns
+    (64, 2, 2, 96, 7232), (64, 2, 2, 7264, 96), (50, 3, 3, 160, 4832),   # four tiles in the first kernel, the second, the first
+])
+def test_many_tokens_an_expert(T, k, E, K, F, fmt):
+    """Every token's choices differ, so each of E = k experts has all of them; steps that end inside, in each way to load."""
+    if fmt in ("fp8", "int8"):
+        K, F = K - 16, F - 16
+    note(f"moe_few_tokens {fmt} T {T} topk {k} E {E} K {K} F {F}, all tokens at each expert")
+    rng = np.random.default_rng(K + F)
+    ids, w = choices(rng, T, k, E, "distinct")
+    Layer(rng, E, K, F, fmt).check(round_bf16(rng.standard_normal((T, K))), ids, w)
+
+
 def test_no_expert_no_tokens_no_columns():
     note("moe_few_tokens empty forms")
     rng = np.random.default_rng(1)

@@ -128,6 +128,8 @@ def check_product(M, N, K, offs, f32, seed=0, a=None, b=None):
     (7, 14336, 64, [7]), (200, 14336, 64, [200]),
     # few columns, short of a tile's width
     (70, 16, 80, [70]), (33, 17, 1040, [33]), (40, 24, 192, [3, 40]), (5, 31, 272, [2, 2, 5]), (100, 15, 144, [100]), (90, 40, 528, [90]),
+    # a contraction shorter than a step, one step, and little more
+    (50, 40, 16, [50]), (20, 40, 16, [20]), (3, 40, 16, [3]), (60, 80, 48, [60]), (60, 80, 80, [60]), (200, 4096, 272, [200]),
     # the persistent kernel: rows of the output that do not begin on 16 bytes, tiles that N or a group ends in
     (1200, 2503, 320, [600, 1150]), (700, 4099, 208, [650]), (4200, 779, 176, [1000, 1000, 4100]), (900, 3586, 144, [5, 900]),
 ])
