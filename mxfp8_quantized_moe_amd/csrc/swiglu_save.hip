@@ -66,20 +66,39 @@ __device__ __forceinline__ float sv_most(float m, const float (&f)[8]) {
   return m;
 }
 
-// e^-|g| and from it sigmoid(g) and its complement sigmoid(-g), both with their own digits (1 - s keeps none where s nears
-// 1). -|g| log2(e) is taken as a rounded product t and the rest of it, which the product rule of the exponential puts
-// back: within 2 ulp, in half the instructions of expf, whose checks for overflow cannot act here (the kernels are bound
-// by their arithmetic: 46 instructions a value before).
-__device__ __forceinline__ void sv_sigmoid(float g, float& s, float& n) {
-  const float x = fmaxf(-fabsf(g), -104.0f);                  // below, e^x is 0 in fp32
+// e^-|g|. -|g| log2(e) is taken as a rounded product t and the rest of it, which the product rule of the exponential puts
+// back: within 2 ulp, in half the instructions of expf (the kernels are bound by their arithmetic: 46 instructions a value
+// before). The hardware's exponential gives 0 below 2^-126; FAR (gates beyond 87) takes it 2^64 up there and
+// rounds once on the way back, to fp32's spacing of 2^-149.
+template <bool FAR>
+__device__ __forceinline__ float sv_exp(float g) {
+  const float x = FAR ? fmaxf(-fabsf(g), -104.0f) : -fabsf(g);   // below -104, e^x rounds to 0 in fp32
   const float t = x * 1.44269504f;
   const float rest = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504f, -t));
-  float e = __builtin_amdgcn_exp2f(t);
+  const bool low = FAR && t < -126.0f;
+  float e = __builtin_amdgcn_exp2f(low ? t + 64.0f : t);   // exact: 64 brings t nearer to 0
   e = fmaf(e * rest, 0.693147182f, e);
-  const float rc = __builtin_amdgcn_rcpf(1.0f + e), er = e * rc;   // the denominator lies in [1, 2]
-  const bool pos = g >= 0.0f;
-  s = pos ? rc : er;
-  n = pos ? er : rc;
+  return low ? e * 0x1p-64f : e;
+}
+
+// sigmoid(g) and its complement sigmoid(-g) of eight gates, both with their own digits (1 - s keeps none where s nears 1).
+// far: the lane may have a gate beyond 87; its whole wave then takes the exponentials again the longer way (16384 x 2048:
+// forward 42 us so, as without the longer way; 44 with it for every value, 52 with a branch between the two).
+__device__ __forceinline__ void sv_sigmoids(const float (&g)[8], bool far, float (&s)[8], float (&n)[8]) {
+  float e[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = sv_exp<false>(g[k]);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(far) != 0ull, 0)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = sv_exp<true>(g[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float rc = __builtin_amdgcn_rcpf(1.0f + e[k]), er = e[k] * rc;   // the denominator lies in [1, 2]
+    const bool pos = g[k] >= 0.0f;
+    s[k] = pos ? rc : er;
+    n[k] = pos ? er : rc;
+  }
 }
 
 // Keeps chunk c of a row's MX form; the four lanes of a block call it together.
@@ -133,12 +152,11 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(SaveArgs p) {
     float gf[8], uf[8];
     sv_unpack(g, gf);
     sv_unpack(u, uf);
+    const uint32_t m = pk_fold(pk_absmax_bf16(pk_absmax_bf16(pk_absmax_bf16(pk_absmax_bf16(0u, g.x), g.y), g.z), g.w));
+    float s[8], n[8];
+    sv_sigmoids(gf, m > 0x42AEu, s, n);   // bf16(87)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float s, n;
-      sv_sigmoid(gf[k], s, n);
-      a[k] = gf[k] * s * uf[k];
-    }
+    for (int k = 0; k < 8; ++k) a[k] = gf[k] * s[k] * uf[k];
   };
   auto first = [&](const u32x4& g, const u32x4& u, int c, float (&a)[8]) {
     sv_keep(g, p.rule, hq, hs, c);
@@ -214,12 +232,12 @@ __global__ __launch_bounds__(256) void swiglu_saved_bwd_kernel(SaveArgs p) {
     sv_unpack(d, df);
     sv_values(g, (uint8_t)eg, gf);
     sv_values(u, (uint8_t)eu, uf);
+    float s[8], n[8];
+    sv_sigmoids(gf, eg >= 125, s, n);   // 448 * 2^-3 is 56
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float s, n;
-      sv_sigmoid(gf[k], s, n);
-      const float gs_ = gf[k] * s;
-      dg[k] = df[k] * uf[k] * s * (1.0f + gf[k] * n);
+      const float gs_ = gf[k] * s[k];
+      dg[k] = df[k] * uf[k] * s[k] * (1.0f + gf[k] * n[k]);
       du[k] = df[k] * gs_;
       a[k] = gs_ * uf[k];
     }
