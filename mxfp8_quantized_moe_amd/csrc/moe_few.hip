@@ -167,9 +167,11 @@ __device__ __forceinline__ int few_members(const FewParams& p, int rank, bool wa
 
 // ---------------------------------------------------------------- the two kernels
 
-// Sixteen bytes to memory past the XCD's caches, as a relaxed atomic store at agent scope would go, in one piece.
+// Sixteen bytes to memory past the XCD's caches, as a relaxed atomic store at agent scope would go, in one piece.  The
+// registers of such a wide store may be written again two wait states later, which the compiler, blind to what the
+// block does, would not keep.
 __device__ __forceinline__ void few_store_agent16(float* to, few_v4f v) {
-  asm volatile("global_store_dwordx4 %0, %1, off sc1" ::"v"(to), "v"(v) : "memory");
+  asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 1" ::"v"(to), "v"(v) : "memory");
 }
 
 // A workgroup takes NT (2 or 4) tiles of 16 weight rows of one expert for all its tokens; its W waves split the
