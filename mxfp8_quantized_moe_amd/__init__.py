@@ -586,6 +586,13 @@ def _out(fn, name, t, shape, dtype, dev):
     return t
 
 
+def _given(fn, name, t, shape, dtypes, dev):
+    """A caller's output tensor is None or has this shape, one of these types and this device, contiguous."""
+    if t is not None and (t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev):
+        raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)} on "
+                         f"{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
 def _vec(fn, name, t, n, dtypes):
     if t is not None and (t.dtype not in dtypes or t.dim() != 1 or t.numel() != n or not t.is_contiguous()):
         raise ValueError(f"{fn}: {name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of {n} elements, "
@@ -841,6 +848,7 @@ def _gate_backward(fn, logits, T, E, ld, dt, topk, ids, dweights, score, token_m
 
 
 _F8_CODES = (torch.uint8, torch.float8_e4m3fn)
+_E8M0_CODES = (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _saved_input(fn, hq, hs):
@@ -848,7 +856,7 @@ def _saved_input(fn, hq, hs):
     R, F2, ld = _rows2d(fn, "hq", hq, _F8_CODES)
     if F2 % 64 or (ld != F2 and R > 1):
         raise ValueError(f"{fn}: hq must be contiguous [R, 2F] with F a multiple of 32, got {tuple(hq.shape)}, strides {hq.stride()}")
-    if hs.dtype not in (torch.uint8, torch.float8_e8m0fnu) or tuple(hs.shape) != (R, F2 // 32) or not hs.is_contiguous():
+    if hs.dtype not in _E8M0_CODES or tuple(hs.shape) != (R, F2 // 32) or not hs.is_contiguous():
         raise ValueError(f"{fn}: hs must be a contiguous e8m0 (uint8) tensor of shape {(R, F2 // 32)}, got {hs.dtype} "
                          f"{tuple(hs.shape)}")
     return R, F2 // 2
@@ -909,6 +917,18 @@ def _saved_groups(fn, offs):
     _vec(fn, "offs", offs, offs.numel(), _I32)
 
 
+def _given_dual_outputs(fn, R, C, offs, rows_pad, layout, dev, bf16_name, bf16, q, scale, q_t, scale_t, offs_pad):
+    """Checks the caller's outputs of a dual form of R rows of C columns."""
+    rp = rows_pad or quantize_mx_rows_bound(R, offs.numel())
+    sc_shape = mx_k4_shape if layout == MX_LAYOUT_K4 else lambda n_rows, n_blocks: (n_rows, n_blocks)
+    _given(fn, bf16_name, bf16, (R, C), _BF16, dev)
+    _given(fn, "q", q, (R, C), _F8_CODES, dev)
+    _given(fn, "scale", scale, sc_shape(R, C // 32), _E8M0_CODES, dev)
+    _given(fn, "q_t", q_t, (C, rp), _F8_CODES, dev)
+    _given(fn, "scale_t", scale_t, sc_shape(C, rp // 32), _E8M0_CODES, dev)
+    _given(fn, "offs_pad", offs_pad, (offs.numel(),), _I32, dev)
+
+
 def swiglu_quantize_mx_dual_saved(hq, hs, offs, rule=MX_FLOOR_OCP, rows_pad=None, a2=None, q=None, scale=None, q_t=None,
                                   scale_t=None, offs_pad=None, layout=MX_LAYOUT_K4, stream=None):
     """swiglu_quantize_mx_dual from the input kept in MXFP8, hq [R, 2F] and hs [R, 2F / 32]: the same results from the kept
@@ -916,6 +936,7 @@ def swiglu_quantize_mx_dual_saved(hq, hs, offs, rule=MX_FLOOR_OCP, rows_pad=None
     fn = "swiglu_quantize_mx_dual_saved"
     R, F = _saved_input(fn, hq, hs)
     _saved_groups(fn, offs)
+    _given_dual_outputs(fn, R, F, offs, rows_pad, layout, hq.device, "a2", a2, q, scale, q_t, scale_t, offs_pad)
     with _on(fn, stream, hq, hs, offs):
         rp, q, scale, q_t, scale_t, offs_pad = _mx_dual_outputs(R, F, offs, rows_pad, q, scale, q_t, scale_t, offs_pad,
                                                                 layout, hq.device)
@@ -933,6 +954,7 @@ def swiglu_backward_quantize_mx_dual_saved(da2, hq, hs, offs, rule=MX_FLOOR_OCP,
     R, F = _saved_input(fn, hq, hs)
     _saved_gradient(fn, da2, R, F)
     _saved_groups(fn, offs)
+    _given_dual_outputs(fn, R, 2 * F, offs, rows_pad, layout, hq.device, "dh1", dh1, q, scale, q_t, scale_t, offs_pad)
     with _on(fn, stream, da2, hq, hs, offs):
         rp, q, scale, q_t, scale_t, offs_pad = _mx_dual_outputs(R, 2 * F, offs, rows_pad, q, scale, q_t, scale_t, offs_pad,
                                                                 layout, hq.device)
