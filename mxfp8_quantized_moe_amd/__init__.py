@@ -976,13 +976,13 @@ def _few_weights(fn, name, w, scale, E, rows, cols, w_fmt, scale_kind):
                          f"{(E, rows, cols)}, got {w.dtype} {tuple(w.shape)}")
     n = E * rows
     if scale_kind == SCALE_F32:
-        dtype, need = torch.float32, n
+        dtypes, need = _F32, n
     else:
         nb = cols // 32
-        dtype, need = torch.uint8, 4 * n * -(-nb // 4) if scale_kind == SCALE_E8M0_K4 else n * nb
-    if scale.dtype != dtype or scale.numel() != need or not scale.is_contiguous():
-        raise ValueError(f"{fn}: {name}_scale must be a contiguous {dtype} tensor of {need} elements, got {scale.dtype} "
-                         f"{tuple(scale.shape)}")
+        dtypes, need = _E8M0_CODES, 4 * n * -(-nb // 4) if scale_kind == SCALE_E8M0_K4 else n * nb
+    if scale.dtype not in dtypes or scale.numel() != need or not scale.is_contiguous():
+        raise ValueError(f"{fn}: {name}_scale must be a contiguous {' or '.join(map(str, dtypes))} tensor of {need} elements, "
+                         f"got {scale.dtype} {tuple(scale.shape)}")
 
 
 def moe_few_tokens(x, ids, weights, w1, w1_scale, w2, w2_scale, w_fmt=OPD_E4M3FN, scale_kind=SCALE_F32, y=None,
@@ -990,7 +990,7 @@ def moe_few_tokens(x, ids, weights, w1, w1_scale, w2, w2_scale, w_fmt=OPD_E4M3FN
     """The whole expert block for at most 64 tokens: x bf16 [T, K] (row stride may exceed K), ids int32 and weights f32
     [T, topk] (as moe_gate gives them), w1 [E, 2F, K] (gate | up rows) and w2 [E, K, F] in 8 bits with their scales ->
     y bf16 [T, K] = the weighted sum of the experts' SwiGLU blocks.  Formats: e4m3fn codes (uint8 or float8_e4m3fn) with
-    f32 row scales or e8m0 scales (SCALE_E8M0, SCALE_E8M0_K4), or OPD_INT8 codes with f32 row scales, as quantize_rowwise
+    f32 row scales or e8m0 scales (uint8 or float8_e8m0fnu; SCALE_E8M0, SCALE_E8M0_K4), or OPD_INT8 codes with f32 row scales, as quantize_rowwise
     and quantize_mx give them.  y may be x (contiguous)."""
     fn = "moe_few_tokens"
     T, K, ld = _rows2d(fn, "x", x, _BF16)
