@@ -130,8 +130,10 @@ static hipError_t i8_rows(const GemmArgs& g, hipStream_t st) {
   const bool stream = (int64_t)g.n_groups * g.N * g.K > (256ll << 20);
   auto pick = [&](auto out_tag) {
     constexpr int OUT = decltype(out_tag)::value;
-    return stream ? (two ? i8_rows_kernel<OUT, 2, NT, true> : i8_rows_kernel<OUT, 4, NT, true>)
-                  : (two ? i8_rows_kernel<OUT, 2, NT, false> : i8_rows_kernel<OUT, 4, NT, false>);
+    if constexpr (NT == 2) {
+      if (stream && two) return i8_rows_kernel<OUT, 2, NT, true>;
+    }   // wider tiles have (M + 64 groups) * N <= 4600000 and M > 32 groups, so streamed rows are longer than 5600
+    return stream ? i8_rows_kernel<OUT, 4, NT, true> : two ? i8_rows_kernel<OUT, 2, NT, false> : i8_rows_kernel<OUT, 4, NT, false>;
   };
   auto kern = g.out_dtype == 0 ? pick(std::integral_constant<int, 0>{}) : pick(std::integral_constant<int, 1>{});
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(two ? 128 : 256), 0, st, p);

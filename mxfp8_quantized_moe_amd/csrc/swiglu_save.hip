@@ -327,7 +327,9 @@ static hipError_t sv_pick(const SaveArgs& p, hipStream_t st) {
   if (nc <= 32 && p.rows >= 2048) return sv_launch<BWD, CODEC, 16, 2>(p, st);   // 49152 x 256 27 -> 20 us; 500 rows 2.7 -> 3.3
   if (nc <= 64) return sv_launch<BWD, CODEC, 64, 1>(p, st);
   if (nc <= 128) return sv_launch<BWD, CODEC, 64, 2>(p, st);
-  if (!BWD && nc <= 192) return sv_launch<BWD, CODEC, 64, 3>(p, st);
+  if constexpr (!BWD) {
+    if (nc <= 192) return sv_launch<BWD, CODEC, 64, 3>(p, st);
+  }
   if (nc <= 512) return sv_launch<BWD, CODEC, 256, 2>(p, st);
   if (nc <= 1024) return sv_launch<BWD, CODEC, 256, 4>(p, st);
   if (nc <= 2048) return sv_launch<BWD, CODEC, 256, 8>(p, st);
