@@ -672,7 +672,8 @@ int64_t quantize_mx_rows_bound(int64_t rows, int32_t n_groups);
  *   channel; K <= 131071, for which no sum of products leaves 32 bits, else
  *   FP8MOE_ERR_UNSUPPORTED; any byte is a valid code).
  *   Accumulation is fp32 (INT8: exact 32-bit integers, then one fp32 rounding
- *   and the two scales' reciprocals); out is bf16 (round to nearest even) or fp32.
+ *   and for bf16 the products with the two scales' reciprocals, for fp32 two
+ *   rounded divisions); out is bf16 (round to nearest even) or fp32.
  *   Requires: M, N, K >= 0; FP8 and INT8 operands: K % 16 == 0 and K <= 2^23 (GROUPED_M) or
  *   M % 16 == 0 and M <= 2^23 (GROUPED_K); BF16 operands: M, N, K % 8 == 0;
  *   all pointers 16-byte aligned.

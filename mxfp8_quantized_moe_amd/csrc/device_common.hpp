@@ -176,6 +176,13 @@ __device__ __forceinline__ float scale_clamp(float x, float s) {
   return __builtin_amdgcn_fmed3f(__fmul_rn(x, s), -fm, fm);
 }
 
+// x / s from r = fp32(1 / s): the product's error, which one fused operation gives exactly, divided by s once more leaves the
+// rounded quotient (half a step of fp32; the product alone is off by two). For s whose reciprocal is finite and not 0.
+__device__ __forceinline__ float div_refined(float x, float s, float r) {
+  const float q = __fmul_rn(x, r);
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+
 // Four values already clamped to [-127, 127] -> four int8 codes packed little-endian in a u32, ties to even.
 // Adding 1.5 * 2^23 (unit in the last place 1) rounds to a whole number whose two's complement stands in the low
 // bits of the sum's pattern: one addition a value and three byte permutes for four of them.

@@ -543,13 +543,16 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
 // v_mfma_i32_32x32x32_i8 (each lane half takes the 16-byte half of its fragment
 // registers that the FP8 instruction takes too; both operands permute the
 // contraction alike), which together take the FP8 instruction's cycles; sums are
-// exact 32-bit integers, turned to fp32 in the epilogue.  8192 rows of 4096 to 14336:
+// exact 32-bit integers, turned to fp32 in the epilogue, which for fp32 outputs
+// divides by both scales to half a step each (8192 rows of 4096 to 14336 in fp32:
+// 438 us with products by reciprocals as for bf16, 447 so).  8192 rows of 4096 to 14336:
 // 383 us, 2.5 POP/s, the matrix cores busy 56%; 49152 of 2048 to 2816 in 64 groups 330 us
 // (FP8 operands 341).
 template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT, bool I8 = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_pipe(KParams p) {
   static_assert(!I8 || SK == 0, "integer operands: fp32 scales");
+  constexpr bool DIV = I8 && OUT == 1;   // quotients in full fp32 (div_refined): the scales stay beside their reciprocals
   using Acc = std::conditional_t<I8, v16i, v16f>;
   using R = PipeRing<BK>;
   constexpr int CH = R::CH, KS = BK / 64;
@@ -702,7 +705,7 @@ void gemm_fp8_pipe(KParams p) {
     const float* psf;       // fp32 scales of the tile's rows and columns
     const float* qsf;
   };
-  __shared__ __attribute__((aligned(16))) float s_inv[2][SK == 0 ? BM + BN : 4];
+  __shared__ __attribute__((aligned(16))) float s_inv[2][SK == 0 ? (DIV ? 2 : 1) * (BM + BN) : 4];
   constexpr int SPT = (BM + BN + 255) / 256;   // fp32 scales per thread
   // Fill `tl` for logical tile L.  Every thread calls it (without a group
   // table it synchronizes the workgroup).
@@ -854,13 +857,16 @@ void gemm_fp8_pipe(KParams p) {
       });
     }
   };
-  // Reciprocals of the scales in s_raw, into `sinv`.
+  // Reciprocals of the scales in s_raw (DIV: and behind them the scales), into `sinv`.
   auto scale_commit = [&](float* sinv) {
     if constexpr (SK == 0) {
 #pragma unroll
       for (int s = 0; s < SPT; ++s) {
         const int idx = threadIdx.x + 256 * s;
-        if (idx < BM + BN) sinv[idx] = __frcp_rn(s_raw[idx]);
+        if (idx < BM + BN) {
+          sinv[idx] = __frcp_rn(s_raw[idx]);
+          if constexpr (DIV) sinv[BM + BN + idx] = s_raw[idx];
+        }
       }
     }
   };
@@ -1291,11 +1297,11 @@ void gemm_fp8_pipe(KParams p) {
       constexpr int jp = decltype(jpc)::value;
       // reciprocals of the lane's columns in this pass (register quad q of
       // block jj: columns 32 jj + 8 q + 4 g + e of the pass) and of its rows
-      f32x4 inv_q[JPP][4];
-      float inv_p[TME];
+      f32x4 inv_q[JPP][4], sc_q[DIV ? JPP : 1][4];
+      float inv_p[TME], sc_p[DIV ? TME : 1];
       if constexpr (SK == 0) {
-        lds_u4 rq[JPP][4];
-        uint32_t rp[TME];
+        lds_u4 rq[JPP][4], wq[DIV ? JPP : 1][4];
+        uint32_t rp[TME], wp[DIV ? TME : 1];
 #pragma unroll
         for (int jj = 0; jj < JPP; ++jj)
 #pragma unroll
@@ -1303,6 +1309,15 @@ void gemm_fp8_pipe(KParams p) {
             rq[jj][q] = lds_read16(sinv_l + 4 * (BM + wn * WNE + 32 * (JPP * jp + jj) + 8 * q + 4 * g));
 #pragma unroll
         for (int i = 0; i < TME; ++i) rp[i] = lds_read4(sinv_l + 4 * (wm * WM + 32 * i + lrow));
+        if constexpr (DIV) {
+#pragma unroll
+          for (int jj = 0; jj < JPP; ++jj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              wq[jj][q] = lds_read16(sinv_l + 4 * (BM + BN + BM + wn * WNE + 32 * (JPP * jp + jj) + 8 * q + 4 * g));
+#pragma unroll
+          for (int i = 0; i < TME; ++i) wp[i] = lds_read4(sinv_l + 4 * (BM + BN + wm * WM + 32 * i + lrow));
+        }
         lds_wait();
 #pragma unroll
         for (int jj = 0; jj < JPP; ++jj)
@@ -1315,6 +1330,20 @@ void gemm_fp8_pipe(KParams p) {
         for (int i = 0; i < TME; ++i) {
           lds_ready(rp[i]);
           inv_p[i] = __builtin_bit_cast(float, rp[i]) * keep;
+        }
+        if constexpr (DIV) {
+#pragma unroll
+          for (int jj = 0; jj < JPP; ++jj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              lds_ready(wq[jj][q]);
+              sc_q[jj][q] = __builtin_bit_cast(f32x4, wq[jj][q]);
+            }
+#pragma unroll
+          for (int i = 0; i < TME; ++i) {
+            lds_ready(wp[i]);
+            sc_p[i] = __builtin_bit_cast(float, wp[i]);
+          }
         }
       } else {
 #pragma unroll
@@ -1335,9 +1364,14 @@ void gemm_fp8_pipe(KParams p) {
             // e8m0 scales were applied inside the MFMAs; an empty contraction
             // range leaves the zero accumulators untouched
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = SK == 0 ? (float)acc[i][JPP * jp + jj][4 * q + e] * inv_p[i] * inv_q[jj][q][e]
-                             : acc[i][JPP * jp + jj][4 * q + e];
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (DIV)
+                v[e] = div_refined(div_refined((float)acc[i][JPP * jp + jj][4 * q + e], sc_p[i], inv_p[i]), sc_q[jj][q][e],
+                                   inv_q[jj][q][e]);
+              else
+                v[e] = SK == 0 ? (float)acc[i][JPP * jp + jj][4 * q + e] * inv_p[i] * inv_q[jj][q][e]
+                               : acc[i][JPP * jp + jj][4 * q + e];
+            }
             const int u = 8 * jj + 2 * q + g;
             if constexpr (OUT == 0) {
               const bf16x2 lo = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);

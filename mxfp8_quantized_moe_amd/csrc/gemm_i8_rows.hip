@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
     for (int i = wave; i < (NB * Dot::ROWS + 15) / 16; i += W) {
       const int m = 16 * i + (lane & 15), b = m / Dot::ROWS;
       if (m >= n) continue;
-      const float inv_p = __frcp_rn(p.sa[m0 + m]);
+      const float sp = p.sa[m0 + m], inv_p = __frcp_rn(sp);
 #pragma unroll
       for (int h = 0; h < NT; ++h) {
         few_v4i s = {0, 0, 0, 0};
@@ -83,7 +83,11 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
         for (int v = 0; v < W; ++v) s += red[v][h * NB + b][16 * (lane >> 4) + Q * (m % Dot::ROWS)];
         float o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = (float)s[j] * inv_p * __frcp_rn(sq[h][j]);
+        for (int j = 0; j < 4; ++j) {
+          const float inv_q = __frcp_rn(sq[h][j]);
+          if constexpr (OUT == 0) o[j] = (float)s[j] * inv_p * inv_q;
+          else o[j] = div_refined(div_refined((float)s[j], sp, inv_p), sq[h][j], inv_q);
+        }
         const int col = c[h], first = max(cn, c0 + 16 * h);
         const int64_t at = (int64_t)(m0 + m) * p.N + col;
         if ((p.N * (OUT == 0 ? 2 : 4)) % 16 == 0) {   // then c0 and `first` are multiples of four
