@@ -546,8 +546,8 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
 // exact 32-bit integers, turned to fp32 in the epilogue, which for fp32 outputs
 // divides by both scales to half a step each (8192 rows of 4096 to 14336 in fp32:
 // 438 us with products by reciprocals as for bf16, 447 so).  8192 rows of 4096 to 14336:
-// 383 us, 2.5 POP/s, the matrix cores busy 56%; 49152 of 2048 to 2816 in 64 groups 330 us
-// (FP8 operands 341).
+// 388 to 443 us by the card, 2.2 to 2.5 POP/s, the matrix cores busy 65%; 49152 of 2048 to 2816 in
+// 64 groups 330 to 385 us (FP8 operands 341), 46%.
 template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT, bool I8 = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_pipe(KParams p) {
@@ -1207,7 +1207,8 @@ void gemm_fp8_pipe(KParams p) {
   constexpr int ELEM = OUT == 0 ? 2 : 4;
   // Integer operands stage every result; rows that do not begin on 16 bytes take
   // stores of 16 bytes at any address, kept in L2, where a line's parts meet
-  // (element stores: 4700 rows in 33 groups, 144 to 6103 columns, 107 us).
+  // (element stores: 4700 rows in 33 groups, 144 to 6103 columns, 107 us; 7054 rows in
+  // 21 groups, 2352 to 7945 columns 280 us so, to 7952, on 16 bytes, 278).
   const bool aligned = (out_ld * ELEM) % 16 == 0;
   if (I8 || aligned) {
     // Lane indices from a fresh opaque copy of the thread index: values kept

@@ -4,7 +4,7 @@
 // With few rows the product is the read of the groups' weights. The persistent GEMM's
 // 256-column tiles are too few then to ask memory for enough at once (16 rows of 14336
 // columns of 4096: 56 workgroups on 256 CUs, 37 us; the weights at the copy rate take 11), so a
-// workgroup here takes 32 or 64 columns for up to 64 rows (11.9 us), its waves split the
+// workgroup here takes 32 or 64 columns for up to 64 rows (12 us), its waves split the
 // contraction, and the whole-number sums are added up through LDS. Sums are exact in any order and the
 // epilogue's operations are the persistent GEMM's, so both give the same bits.
 #include "few_dot.hpp"

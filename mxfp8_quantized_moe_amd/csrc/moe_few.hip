@@ -20,10 +20,9 @@
 // lists for the second kernel, which waits for nothing else: with a search by each of its waves 64 tokens of 32 experts took a
 // fifth longer.
 //
-// Two kernels rather than one: the second needs all of a, and their launches overlap the reads by less than a barrier over
-// the GPU would cost.
+// Two kernels rather than one: the second needs all of a, so one kernel would hold a barrier over the GPU (not tried).
 //
-// Rates, the used experts' weights over the time of both kernels: 8 tokens of 16 experts, MX, 5120 x 8192: 121 us, 6.9 TB/s;
+// Rates, the used experts' weights over the time of both kernels: 8 tokens of 16 experts, MX, 5120 x 8192: 115 us, 7 TB/s;
 // 64 tokens of 32 experts 7168 x 2048, a quarter of their choices here: 215 us, 6.5 TB/s: bound by that read.  One token, six
 // of 64 experts 2048 x 1408: 17 us, 3 TB/s, where the launches and the beginnings of the reads count as much.
 #include "few_dot.hpp"
@@ -345,7 +344,8 @@ static hipError_t few_launch(const FewParams& p, hipStream_t st) {
   // 32 two tiles load whole cache lines of them), if the workgroups still fill the GPU (64 tokens, eight of 16 experts
   // 5120 x 8192: both kernels 669 -> 585 us by the first, -> 643 by the second; eight of 8 7168 x 2048 191 -> 153, -> 174; six
   // of 16 2048 x 1408, 24 an expert, 64.6 -> 65.1, -> 61.7; 64 tokens of one expert 4096 x 8192, the second's 64 workgroups:
-  // 69 -> 90; four tokens an expert of 32, 7168 x 2048, the others' ids none: both 231 -> 249).
+  // 69 -> 90; four tokens an expert of 32, 7168 x 2048, the others' ids none: both 231 -> 249). The host knows the choices, not
+  // how many of them name an expert here.
   auto count = [&](int cols) { return (int64_t)p.ranks * (((UP ? p.F : p.K) + cols - 1) / cols); };
   constexpr int COLS = UP ? 16 : 32;
   const bool wide = (int64_t)p.T * p.topk >= 24 * (int64_t)p.E && count(2 * COLS) >= 224;
@@ -355,8 +355,8 @@ static hipError_t few_launch(const FewParams& p, hipStream_t st) {
   // (64 tokens of 64 experts 2048 x 1408: first kernel 75 -> 68 us; rows of 7168: 149 -> 154 us).
   const bool two = !wide && (UP ? p.K : p.F) <= 2048 && blocks >= 512;
   // Streamed loads where the experts' weights are beyond the last-level cache (64 tokens of 32 experts 7168 x 2048, 1.4 GB:
-  // first kernel 153 -> 144 us); weights that stay there from one call to the next are not (4 tokens of 7 experts
-  // 1040 x 336, 7 MB: 11.9 us streamed, 5.8 not).
+  // first kernel 153 -> 144 us); smaller ones are not, which may stay there from one call to the next (4 tokens of 7 experts
+  // 1040 x 336, 7 MB: 11.9 us streamed, 5.8 not; 5 tokens of them, weights from HBM: 16.5 and 11.6, both kernels).
   const bool stream = (int64_t)p.E * 3 * p.K * p.F > (256ll << 20);
   auto kern = wide ? few_kernel<FMT, UP, 4, 4, false>
               : stream ? (two ? few_kernel<FMT, UP, 2, 2, true> : few_kernel<FMT, UP, 4, 2, true>)

@@ -16,8 +16,8 @@
 // of eight columns; four neighbouring lanes hold one block of 32.  Rows beyond that are read twice and
 // computed twice.
 //
-// 49152 x 1408: forward 85 us (5.7 TB/s of 7 bytes a value; the vector units issue all the time), backward with a2
-// 141 us (5.9 TB/s; they issue 80% of it).
+// 49152 x 1408: forward 86 us (5.7 TB/s of 7 bytes a value; the vector units issue all the time), backward with a2
+// 141 us (5.9 TB/s; they issue 78% of it).
 #include "device_common.hpp"
 #include "kernels.hpp"
 #include "swiglu_common.hpp"

@@ -131,6 +131,7 @@ def check_product(M, N, K, offs, f32, seed=0, a=None, b=None):
     # a contraction shorter than a step, one step, and little more
     (50, 40, 16, [50]), (20, 40, 16, [20]), (3, 40, 16, [3]), (60, 80, 48, [60]), (60, 80, 80, [60]), (200, 4096, 272, [200]),
     # the persistent kernel: rows of the output that do not begin on 16 bytes, tiles that N or a group ends in
+    # (sizes that the kernel for few rows takes by now; the persistent one's are in test_gpu_int8_persistent.py)
     (1200, 2503, 320, [600, 1150]), (700, 4099, 208, [650]), (4200, 779, 176, [1000, 1000, 4100]), (900, 3586, 144, [5, 900]),
 ])
 def test_product(M, N, K, offs, f32):

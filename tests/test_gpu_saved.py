@@ -15,6 +15,7 @@ from gpu_helpers import DEV, note, bf16_dev, i32_dev, u8_dev, host, bf16_bits_to
 pytestmark = pytest.mark.gpu
 
 # Row lengths for each kernel: 16, 64 and 256 threads a row, one to eight chunks a thread, and rows read twice.
+# (For few rows, that is; the kernels taken from 2048 rows on are in test_gpu_saved_many_rows.py.)
 SIZES = [(1, 32), (37, 96), (18, 128), (9, 160), (300, 512), (21, 544), (5, 1056), (66, 1408), (7, 2048), (3, 2080), (4, 4128),
          (2, 8192), (3, 8224), (2, 16384), (2, 16416)]
 
