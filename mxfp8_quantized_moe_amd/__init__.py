@@ -990,8 +990,8 @@ def moe_few_tokens(x, ids, weights, w1, w1_scale, w2, w2_scale, w_fmt=OPD_E4M3FN
     """The whole expert block for at most 64 tokens: x bf16 [T, K] (row stride may exceed K), ids int32 and weights f32
     [T, topk] (as moe_gate gives them), w1 [E, 2F, K] (gate | up rows) and w2 [E, K, F] in 8 bits with their scales ->
     y bf16 [T, K] = the weighted sum of the experts' SwiGLU blocks.  Formats: e4m3fn codes (uint8 or float8_e4m3fn) with
-    f32 row scales or e8m0 scales (uint8 or float8_e8m0fnu; SCALE_E8M0, SCALE_E8M0_K4), or OPD_INT8 codes with f32 row scales, as quantize_rowwise
-    and quantize_mx give them.  y may be x (contiguous)."""
+    f32 row scales or e8m0 scales (uint8 or float8_e8m0fnu; SCALE_E8M0, SCALE_E8M0_K4), or OPD_INT8 codes with f32 row
+    scales, as quantize_rowwise and quantize_mx give them.  y may be x (contiguous)."""
     fn = "moe_few_tokens"
     T, K, ld = _rows2d(fn, "x", x, _BF16)
     topk = _gate_slots(fn, "ids", ids, T, _I32)

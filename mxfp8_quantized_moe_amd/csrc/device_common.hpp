@@ -176,11 +176,13 @@ __device__ __forceinline__ float scale_clamp(float x, float s) {
   return __builtin_amdgcn_fmed3f(__fmul_rn(x, s), -fm, fm);
 }
 
-// x / s from r = fp32(1 / s): the product's error, which one fused operation gives exactly, divided by s once more leaves the
-// rounded quotient (half a step of fp32; the product alone is off by two). For s whose reciprocal is finite and not 0.
-__device__ __forceinline__ float div_refined(float x, float s, float r) {
-  const float q = __fmul_rn(x, r);
-  return fmaf(fmaf(-q, s, x), r, q);
+// x / s / t from r = fp32(1 / s) and u = fp32(1 / t): a product's error, which one fused operation gives exactly, divided
+// once more leaves the rounded quotient, half a step of fp32 each (the products alone are off by two each).  Results beyond
+// fp32 and scales of 0 or infinity have no such error; there the products stand, as IEEE division gives them.
+__device__ __forceinline__ float div_both(float x, float s, float r, float t, float u) {
+  const float p = __fmul_rn(x, r), a = fmaf(fmaf(-p, s, x), r, p);
+  const float q = __fmul_rn(a, u), b = fmaf(fmaf(-q, t, a), u, q);
+  return fabsf(b) < INFINITY ? b : __fmul_rn(p, u);
 }
 
 // Four values already clamped to [-127, 127] -> four int8 codes packed little-endian in a u32, ties to even.

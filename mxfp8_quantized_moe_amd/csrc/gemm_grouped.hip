@@ -545,14 +545,15 @@ __device__ __forceinline__ T* uniform_ptr(T* p) {
 // contraction alike), which together take the FP8 instruction's cycles; sums are
 // exact 32-bit integers, turned to fp32 in the epilogue, which for fp32 outputs
 // divides by both scales to half a step each (8192 rows of 4096 to 14336 in fp32:
-// 438 us with products by reciprocals as for bf16, 447 so).  8192 rows of 4096 to 14336:
+// 438 us with products by reciprocals as for bf16, 452 so; a quotient by the product of the
+// scales, with a branch for those beyond fp32, takes as long).  8192 rows of 4096 to 14336:
 // 388 to 443 us by the card, 2.2 to 2.5 POP/s, the matrix cores busy 65%; 49152 of 2048 to 2816 in
 // 64 groups 330 to 385 us (FP8 operands 341), 46%.
 template <int BM, int BN, int BK, int SLOTS, int MODE, int SK, int OUT, bool I8 = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_pipe(KParams p) {
   static_assert(!I8 || SK == 0, "integer operands: fp32 scales");
-  constexpr bool DIV = I8 && OUT == 1;   // quotients in full fp32 (div_refined): the scales stay beside their reciprocals
+  constexpr bool DIV = I8 && OUT == 1;   // quotients in full fp32 (div_both): the scales stay beside their reciprocals
   using Acc = std::conditional_t<I8, v16i, v16f>;
   using R = PipeRing<BK>;
   constexpr int CH = R::CH, KS = BK / 64;
@@ -1367,8 +1368,7 @@ void gemm_fp8_pipe(KParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if constexpr (DIV)
-                v[e] = div_refined(div_refined((float)acc[i][JPP * jp + jj][4 * q + e], sc_p[i], inv_p[i]), sc_q[jj][q][e],
-                                   inv_q[jj][q][e]);
+                v[e] = div_both((float)acc[i][JPP * jp + jj][4 * q + e], sc_p[i], inv_p[i], sc_q[jj][q][e], inv_q[jj][q][e]);
               else
                 v[e] = SK == 0 ? (float)acc[i][JPP * jp + jj][4 * q + e] * inv_p[i] * inv_q[jj][q][e]
                                : acc[i][JPP * jp + jj][4 * q + e];

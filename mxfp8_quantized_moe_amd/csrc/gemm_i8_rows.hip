@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * W) void i8_rows_kernel(I8Params p) {
         for (int j = 0; j < 4; ++j) {
           const float inv_q = __frcp_rn(sq[h][j]);
           if constexpr (OUT == 0) o[j] = (float)s[j] * inv_p * inv_q;
-          else o[j] = div_refined(div_refined((float)s[j], sp, inv_p), sq[h][j], inv_q);
+          else o[j] = div_both((float)s[j], sp, inv_p, sq[h][j], inv_q);
         }
         const int col = c[h], first = max(cn, c0 + 16 * h);
         const int64_t at = (int64_t)(m0 + m) * p.N + col;

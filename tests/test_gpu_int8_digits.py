@@ -54,3 +54,28 @@ def test_an_infinite_row(M, N):
     assert not torch.isfinite(got[7]).any()
     keep = torch.arange(M, device=DEV) != 7
     assert torch.equal(got[keep], ref[keep])
+
+
+@pytest.mark.parametrize("M,N", [(16, 40), (2600, 3001)])
+def test_beyond_fp32(M, N):
+    """Quotients beyond fp32 are infinities of their sign, as division makes them, in each order of overflow; a sum of 0 over
+    such scales is 0; scales of infinity give 0."""
+    note(f"grouped_mm_scaled INT8 fp32 {M}x{N} beyond the range")
+    K = 16
+    a, b = torch.ones(M, K, dtype=torch.int8, device=DEV), torch.ones(N, K, dtype=torch.int8, device=DEV)
+    a[::3] = -1
+    a[2::3, ::2] = -1                      # sums -16, 16, 0
+    sa, sb = torch.ones(M, device=DEV), torch.ones(N, device=DEV)
+    sa[3:], sb[5:] = 2.0 ** -125, 2.0 ** -100     # the second quotient overflows from row 3 and column 5 on
+    sa[9:] = 2.0 ** -126                          # 16 / 2^-126 does not fit in fp32: the first quotient overflows
+    sb[12], sa[15] = float("inf"), 0.0
+    out = fm.grouped_mm_scaled(fm.GROUPED_M, a, fm.OPD_INT8, sa, b, fm.OPD_INT8, sb, fm.SCALE_F32, None, 1, M, N, K,
+                               out_dtype=fm.OUT_F32)
+    # as quotients, in fp32: the sum over the row's scale, and that over the column's
+    sums = (a.double() @ b.double().t().contiguous()).float()
+    ref = (sums / sa[:, None]) / sb
+    finite = torch.isfinite(ref)
+    assert torch.equal(out[finite], ref[finite])              # powers of two: exact
+    assert torch.equal(torch.isnan(out), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert inf.any() and torch.equal(out[inf], ref[inf])
